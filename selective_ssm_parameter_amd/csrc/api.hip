@@ -10,6 +10,7 @@
 #include <string>
 #include <vector>
 
+#include "api_common.hpp"
 #include "launch.hpp"
 #include "swimba.h"
 
@@ -22,6 +23,10 @@ static __device__ __align__(256) unsigned char scratch[kScratchBytes];
 namespace {
 
 thread_local std::string g_err;
+
+}  // namespace
+
+namespace swimba {
 
 swimba_status fail(swimba_status st, const char* fmt, ...) {
   char buf[512];
@@ -38,15 +43,7 @@ swimba_status hip_status(hipError_t e, const char* what) {
   return fail(SWIMBA_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // ---------------------------------------------------------------- dims
-
-struct Dims {
-  int64_t Bt, T, D, H, P, N, G, E, k, L, M, W, HP, GN;
-  bool bf16;
-  size_t esize;
-};
 
 swimba_status read_dims(const swimba_dims* d, Dims& o) {
   if (!d) return fail(SWIMBA_ERR_NULL, "dims is NULL");
@@ -74,6 +71,18 @@ swimba_status read_dims(const swimba_dims* d, Dims& o) {
   return SWIMBA_OK;
 }
 
+swimba_status check_ws(void* ws, size_t have, size_t need) {
+  if (need == 0) return SWIMBA_OK;
+  if (!ws) return fail(SWIMBA_ERR_WORKSPACE, "workspace of %zu bytes required, got NULL", need);
+  if (have < need) return fail(SWIMBA_ERR_WORKSPACE, "workspace of %zu bytes required, got %zu", need, have);
+  if (!aligned16(ws)) return fail(SWIMBA_ERR_ALIGN, "workspace is not 16-byte aligned");
+  return SWIMBA_OK;
+}
+
+}  // namespace swimba
+
+namespace {
+
 swimba_status check_kernel_shape(const Dims& d) {
   if (d.P != 64) return fail(SWIMBA_ERR_UNSUPPORTED, "headdim %lld: only 64 has a kernel", (long long)d.P);
   if (d.N != 16 && d.N != 32 && d.N != 64 && d.N != 128)
@@ -90,7 +99,6 @@ swimba_status check_kernel_shape(const Dims& d) {
 // not read take the offset 2^31 (kOOB), which returns zeros only while it lies
 // past the record, so records stay below 2^31 bytes (0x7FFFFFF0, "2 GiB"
 // below). Larger tensors are rejected here instead of being read wrongly.
-constexpr int64_t kMaxRecord = 0x7FFFFFF0ll;
 
 swimba_status check_records(const Dims& d, bool router, bool experts) {
   const int64_t ein = d.bf16 ? 2 : 4;  // u and weight elements
@@ -131,8 +139,6 @@ swimba_status check_scan_shape(const Dims& d, int kmax = 4) {
 }
 
 // ---------------------------------------------------------------- workspace
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct ProjWs {
   size_t counts, offsets, tiles, sorted, sortw, cpart, total;
@@ -251,24 +257,6 @@ size_t scan_bytes(const Dims& d) {
                   scan_ws_bytes(scan_geom((int)d.Bt, (int)d.T, (int)d.H, (int)d.G, (int)d.N,
                                           (int)d.P, (int)d.k, (int)d.L, (int)d.esize, true)));
 }
-
-swimba_status check_ws(void* ws, size_t have, size_t need) {
-  if (need == 0) return SWIMBA_OK;
-  if (!ws) return fail(SWIMBA_ERR_WORKSPACE, "workspace of %zu bytes required, got NULL", need);
-  if (have < need) return fail(SWIMBA_ERR_WORKSPACE, "workspace of %zu bytes required, got %zu", need, have);
-  if (!aligned16(ws)) return fail(SWIMBA_ERR_ALIGN, "workspace is not 16-byte aligned");
-  return SWIMBA_OK;
-}
-
-#define REQUIRE_PTR(p)                                                  \
-  do {                                                                  \
-    if (!(p)) return fail(SWIMBA_ERR_NULL, "%s is NULL", #p);           \
-    if (!aligned16(p)) return fail(SWIMBA_ERR_ALIGN, "%s is not 16-byte aligned", #p); \
-  } while (0)
-#define OPTIONAL_PTR(p)                                                 \
-  do {                                                                  \
-    if ((p) && !aligned16(p)) return fail(SWIMBA_ERR_ALIGN, "%s is not 16-byte aligned", #p); \
-  } while (0)
 
 ProjGeom proj_geom(const Dims& d, int64_t M, bool bw_one = false) {
   ProjGeom g;
