@@ -170,7 +170,8 @@ swimba_status swimba_gated_step(const swimba_dims* dims, const void* x, const vo
  *   x       [M, D] dtype
  *   w_in    [2 F, D] dtype: F rows for g, then F rows for u
  *   act     swimba_activation
- *   z       [M, 2 F] dtype out: [g | u] for the backward, or NULL
+ *   z       [M, 2 F] dtype out: [g | u], rounded, or NULL (the backward does
+ *           not need it)
  *   h       [M, F] dtype out
  * D and F must be multiples of 8 (else SWIMBA_ERR_UNSUPPORTED); w_in at most
  * 2 GiB (else SWIMBA_ERR_DIMS).
@@ -179,18 +180,21 @@ swimba_status swimba_gated_project(const swimba_dims* dims, const void* x, const
                                    int32_t act, void* z, void* h, hipStream_t stream);
 
 /*
- * Backward of swimba_gated_project. With z = [g | u] of the forward:
- *   dg = dh u act'(g),  du = dh act(g),  dz = [dg | du] (rounded to dtype, as
- *   the operand of both products),   dx = dz w_in,   dw_in = dz^T x.
- *   x, w_in, act as given to the forward;  z as it wrote it
+ * Backward of swimba_gated_project. g and u are recomputed in float32 from x
+ * and w_in, so that the forward keeps nothing:
+ *   dg = dh u act'(g),  du = dh act(g),  dz = [dg | du],
+ *   dx = dz w_in,   dw_in = dz^T x.
+ * bf16 problems take dz into both products as the sum of two bf16 numbers (16
+ * bits of it), so that dx and dw_in carry no bf16 rounding.
+ *   x, w_in, act as given to the forward
  *   dh      [M, F] dtype
  *   dx      [M, D] float32 out;  dw_in [2 F, D] float32 out (zeros without tokens)
  *   ws      workspace of SWIMBA_LAYER_GATED_PROJECT_BACKWARD
  */
 swimba_status swimba_gated_project_backward(const swimba_dims* dims, const void* x,
-                                            const void* w_in, const void* z, const void* dh,
-                                            int32_t act, float* dx, float* dw_in, void* ws,
-                                            size_t ws_bytes, hipStream_t stream);
+                                            const void* w_in, const void* dh, int32_t act,
+                                            float* dx, float* dw_in, void* ws, size_t ws_bytes,
+                                            hipStream_t stream);
 
 /*
  * Backward of swimba_output_project (out = y w_out^T):

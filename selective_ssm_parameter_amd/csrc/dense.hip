@@ -10,9 +10,17 @@
 //   gated projection  [g | u] = x w_in^T        rows x rows
 //   dx = dz w_in,  dy = dout w_out               rows x columns
 //   dw_in = dz^T x,  dw_out = dout^T y           columns x columns, k = tokens
-// Tiles of 256 x 256 (8 waves), 128 x 128 (4 waves), k steps of 32; four LDS stages, filled three steps ahead by buffer-to-LDS copies that
-// are waited for with a fixed count; fp32 accumulation in the matrix cores.
+// Tiles of 256 x 256 (8 waves), 128 x 128 or 64 x 64 / 64 x 128 (4 waves), k
+// steps of 32; four LDS stages, filled three steps ahead by buffer-to-LDS
+// copies that are waited for with a fixed count; fp32 accumulation in the
+// matrix cores. The gated projection's backward recomputes g and u with the
+// forward's product and turns them into dz in the epilogue, in fp32; for bf16
+// problems dz then goes through both products as hi + lo, two bf16 numbers (16
+// bits of dz, so that dx and dw_in are good to fp32 sums of them and not to
+// one bf16 rounding): each LDS stage holds both, three stages of them, and a
+// fragment of the other operand serves both.
 // Bound by the matrix cores for many tokens.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.hpp"
@@ -32,30 +40,39 @@ struct Cfg {
 };
 typedef Cfg<256, 256, 2, 4> Big;
 typedef Cfg<128, 128, 2, 2> Mid;
+typedef Cfg<64, 128, 2, 2> Small;   // gated products (32 columns of g and of u per wave)
+typedef Cfg<64, 64, 2, 2> Small64;  // the others
 
-enum Mode { kGated, kNN, kTN };
+// kGated: h; kGatedBwd: the same product, dz in the epilogue
+enum Mode { kGated, kGatedBwd, kNN, kTN };
+constexpr bool is_gated(Mode m) { return m == kGated || m == kGatedBwd; }
 
 struct DenseArgs {
   const void *a, *b;
-  void* out;      // kGated: h
-  void* z;        // kGated: [g | u] or null
-  int R, S, K;    // kGated: S = F, the columns of h
+  const void* a_lo;  // split operands: a = a (bf16) + a_lo (bf16)
+  void* out;         // kGated: h; kGatedBwd: dz (its lo half behind it for bf16)
+  void* z;           // kGated: [g | u] or null
+  const void* dh;    // kGatedBwd
+  int R, S, K;       // gated: S = F, the columns of h
   int act;
   int splits;     // kTN: k is cut into this many runs of ksplit rows
   int ksplit;
 };
 
-constexpr int kBK = 32, kStages = 4;
+constexpr int kBK = 32;
 
-template <typename T, class C, Mode MODE>
+template <typename T, class C, Mode MODE, bool SPLIT>
 struct DLay {
   static constexpr int ES = sizeof(T), EPC = 16 / ES;
-  static constexpr bool ACOL = MODE == kTN, BCOL = MODE != kGated;
+  static constexpr int NS = SPLIT ? 3 : 4;  // LDS stages, NS - 1 steps in flight
+  static constexpr bool ACOL = MODE == kTN, BCOL = !is_gated(MODE);
   // tile in LDS: rows of CPR 16-byte chunks
   static constexpr int AROWS = ACOL ? kBK : C::BM, ACPR = (ACOL ? C::BM : kBK) / EPC;
   static constexpr int BROWS = BCOL ? kBK : C::BN, BCPR = (BCOL ? C::BN : kBK) / EPC;
-  static constexpr int AB = AROWS * ACPR * 16, BB = BROWS * BCPR * 16, STAGE = AB + BB;
+  static constexpr int AB = AROWS * ACPR * 16, BB = BROWS * BCPR * 16, STAGE = AB * (SPLIT ? 2 : 1) + BB;
+  static constexpr int BOFF = STAGE - BB;  // a (, a_lo), b
   static constexpr int MA = AB / 1024 / C::NW, MB = BB / 1024 / C::NW;  // copies per wave
+  static constexpr int CPW = MA * (SPLIT ? 2 : 1) + MB;
   static_assert(AB % (1024 * C::NW) == 0 && BB % (1024 * C::NW) == 0, "whole copies per wave");
 };
 
@@ -99,21 +116,21 @@ __device__ __forceinline__ bool unit_of(int nr, int nc, int& tr, int& tc) {
   return true;
 }
 
-template <typename T, class C, Mode MODE, typename TO>
+template <typename T, class C, Mode MODE, typename TO, bool SPLIT>
 __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
-  typedef DLay<T, C, MODE> L;
+  typedef DLay<T, C, MODE, SPLIT> L;
   typedef typename Vec<T>::x8 F;
   constexpr int BM = C::BM, BN = C::BN, NW = C::NW, TM = C::TM, TN = C::TN;
   constexpr int MA = L::MA, MB = L::MB, EPC = L::EPC;
   constexpr uint32_t ES = L::ES;
   // columns of out per tile: the gated tile holds BN / 2 of g and the same of u
-  constexpr int SN = MODE == kGated ? BN / 2 : BN;
+  constexpr int SN = is_gated(MODE) ? BN / 2 : BN;
 
-  // four stage arrays: copies into one are known not to touch the others
+  // an array per stage: copies into one are known not to touch the others
   __shared__ __align__(16) unsigned char stg0[L::STAGE];
   __shared__ __align__(16) unsigned char stg1[L::STAGE];
   __shared__ __align__(16) unsigned char stg2[L::STAGE];
-  __shared__ __align__(16) unsigned char stg3[L::STAGE];
+  __shared__ __align__(16) unsigned char stg3[L::NS == 4 ? L::STAGE : 16];
 
   const int nr = (A.R + BM - 1) / BM, nc = (A.S + SN - 1) / SN;
   int tr, tc, split = 0;
@@ -141,15 +158,18 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   // split's rows have to stay below 2 GiB.
   const T* ap = static_cast<const T*>(A.a);
   const T* bp = static_cast<const T*>(A.b);
-  BufRes rA, rB;
+  const T* lp = static_cast<const T*>(A.a_lo);
+  BufRes rA, rL, rB;
   uint32_t aoff[MA], boff[MB];
   int akc[MA], bkc[MB];  // rows operands: the chunk's first k, to cut at K
   uint32_t astep, bstep;
   if constexpr (L::ACOL) {
     rA = make_rsrc(ap + (size_t)kbeg * A.R, (uint64_t)K * A.R * ES);
+    if constexpr (SPLIT) rL = make_rsrc(lp + (size_t)kbeg * A.R, (uint64_t)K * A.R * ES);
     astep = kBK * (uint32_t)A.R * ES;
   } else {
     rA = make_rsrc(ap + (size_t)r0 * A.K, (uint64_t)nrows * A.K * ES);
+    if constexpr (SPLIT) rL = make_rsrc(lp + (size_t)r0 * A.K, (uint64_t)nrows * A.K * ES);
     astep = kBK * ES;
   }
   if constexpr (L::BCOL) {
@@ -199,12 +219,16 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rA, (__attribute__((address_space(3))) void*)(st + 1024 * (wave + NW * m)), 16, off, 0, 0,
           0);
+      if constexpr (SPLIT)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rL, (__attribute__((address_space(3))) void*)(st + L::AB + 1024 * (wave + NW * m)), 16,
+            off, 0, 0, 0);
     }
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
       const uint32_t off = k0 + bkc[m] < K && boff[m] != kOOB ? boff[m] + kt * bstep : kOOB;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rB, (__attribute__((address_space(3))) void*)(st + L::AB + 1024 * (wave + NW * m)), 16,
+          rB, (__attribute__((address_space(3))) void*)(st + L::BOFF + 1024 * (wave + NW * m)), 16,
           off, 0, 0, 0);
     }
   };
@@ -228,14 +252,14 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   };
   auto bfrag = [&](const unsigned char* st, int j) -> F {
     if constexpr (L::BCOL) {
-      return load_kmajor<T, L::BCPR>(st + L::AB, 0, wn * TN * 16 + 16 * j, lane);
+      return load_kmajor<T, L::BCPR>(st + L::BOFF, 0, wn * TN * 16 + 16 * j, lane);
     } else {
       const int r = wn * TN * 16 + 32 * (j >> 1) + 8 * (c >> 2) + 4 * (j & 1) + (c & 3);
       if constexpr (ES == 2)
         return load8<T>(reinterpret_cast<const T*>(
-            st + L::AB + (r * L::BCPR + (g ^ swz_row<T, L::BCPR>(r))) * 16));
+            st + L::BOFF + (r * L::BCPR + (g ^ swz_row<T, L::BCPR>(r))) * 16));
       else
-        return load8<T>(reinterpret_cast<const T*>(st + L::AB + r * L::BCPR * 16 + 32 * g));
+        return load8<T>(reinterpret_cast<const T*>(st + L::BOFF + r * L::BCPR * 16 + 32 * g));
     }
   };
 
@@ -254,30 +278,46 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = mma16(bf[j], af[i], acc[i][j]);
+    if constexpr (SPLIT) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i) af[i] = afrag(st + L::AB, i);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = mma16(bf[j], af[i], acc[i][j]);
+    }
   };
 
-  // whole turns of the four stages, every copy unconditional (steps past K
+  // whole turns of the stages, every copy unconditional (steps past K
   // multiply zeros)
-  const int nk4 = ((K + kBK - 1) / kBK + kStages - 1) / kStages * kStages;
-  fetch(stg0, 0);
-  fetch(stg1, 1);
-  fetch(stg2, 2);
+  const int nks = ((K + kBK - 1) / kBK + L::NS - 1) / L::NS * L::NS;
   auto iter = [&](int kt, const unsigned char* cur, unsigned char* far) {
-    wait_vm<2 * (MA + MB)>();  // step kt landed (steps kt + 1, kt + 2 may be in flight)
-    stage_barrier();           // step kt visible to all waves; step kt - 1 no longer read
-    fetch(far, kt + 3);
+    wait_vm<(L::NS - 2) * L::CPW>();  // step kt landed (the steps after it may be in flight)
+    stage_barrier();                  // step kt visible to all waves; step kt - 1 no longer read
+    fetch(far, kt + L::NS - 1);
     compute(cur);
   };
-  for (int kt = 0; kt < nk4; kt += kStages) {
-    iter(kt, stg0, stg3);
-    iter(kt + 1, stg1, stg0);
-    iter(kt + 2, stg2, stg1);
-    iter(kt + 3, stg3, stg2);
+  fetch(stg0, 0);
+  fetch(stg1, 1);
+  if constexpr (L::NS == 4) {
+    fetch(stg2, 2);
+    for (int kt = 0; kt < nks; kt += 4) {
+      iter(kt, stg0, stg3);
+      iter(kt + 1, stg1, stg0);
+      iter(kt + 2, stg2, stg1);
+      iter(kt + 3, stg3, stg2);
+    }
+  } else {
+    for (int kt = 0; kt < nks; kt += 3) {
+      iter(kt, stg0, stg2);
+      iter(kt + 1, stg1, stg0);
+      iter(kt + 2, stg2, stg1);
+    }
   }
   wait_vm<0>();  // the copies past the end land before the workgroup's LDS is released
 
   // ---- epilogue
-  if constexpr (MODE == kGated) {
+  if constexpr (is_gated(MODE)) {
     static_assert(TN % 4 == 0, "a pair of g tiles and the pair of u tiles per wave");
     TO* h = static_cast<TO*>(A.out);
     TO* z = static_cast<TO*>(A.z);
@@ -288,6 +328,34 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
       for (int jj = 0; jj < TN / 4; ++jj) {
         const int col = s0 + (wn * (TN / 4) + jj) * 32 + 8 * g;
         if (r >= nrows || col >= A.S) continue;
+        if constexpr (MODE == kGatedBwd) {
+          const size_t row = (size_t)(r0 + r);
+          const typename Vec<T>::x8 dv = load8<T>(static_cast<const T*>(A.dh) + row * A.S + col);
+          floatx8 dg, du;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float v, d;
+            act_grad(A.act, acc[i][4 * jj + (q >> 2)][q & 3], v, d);
+            const float dd = to_f32(dv[q]);
+            dg[q] = dd * acc[i][4 * jj + 2 + (q >> 2)][q & 3] * d;
+            du[q] = dd * v;
+          }
+          TO* hi = static_cast<TO*>(A.out) + row * 2 * A.S + col;
+          const typename Vec<TO>::x8 hg = convert8<TO, float>(dg), hu = convert8<TO, float>(du);
+          store8<TO>(hi, hg);
+          store8<TO>(hi + A.S, hu);
+          if constexpr (ES == 2) {
+            TO* lo = hi + (size_t)A.R * 2 * A.S;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              dg[q] -= to_f32(hg[q]);
+              du[q] -= to_f32(hu[q]);
+            }
+            store8<TO>(lo, convert8<TO, float>(dg));
+            store8<TO>(lo + A.S, convert8<TO, float>(du));
+          }
+          continue;
+        }
         typename Vec<TO>::x8 og, ou, oh;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
@@ -324,33 +392,6 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   }
 }
 
-// dz = [dh u act'(g) | dh act(g)], 8 columns per thread.
-template <typename T>
-__global__ __launch_bounds__(256) void gated_dz_kernel(const T* __restrict__ z,
-                                                       const T* __restrict__ dh,
-                                                       T* __restrict__ dz, int M, int F, int act) {
-  const int f8 = F / 8;
-  const size_t n = (size_t)M * f8;
-  for (size_t q = (size_t)blockIdx.x * 256 + threadIdx.x; q < n; q += (size_t)gridDim.x * 256) {
-    const size_t m = q / f8;
-    const int c = (int)(q - m * f8) * 8;
-    const typename Vec<T>::x8 gv = load8<T>(z + m * 2 * F + c);
-    const typename Vec<T>::x8 uv = load8<T>(z + m * 2 * F + F + c);
-    const typename Vec<T>::x8 dv = load8<T>(dh + m * F + c);
-    typename Vec<T>::x8 og, ou;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float v, d;
-      act_grad(act, to_f32(gv[j]), v, d);
-      const float dd = to_f32(dv[j]);
-      og[j] = from_f32<T>(dd * to_f32(uv[j]) * d);
-      ou[j] = from_f32<T>(dd * v);
-    }
-    store8<T>(dz + m * 2 * F + c, og);
-    store8<T>(dz + m * 2 * F + F + c, ou);
-  }
-}
-
 // out = the splits' partial products added in split order.
 __global__ __launch_bounds__(256) void dense_sum_kernel(const float* __restrict__ part, int splits,
                                                         size_t n4, float* __restrict__ out) {
@@ -361,37 +402,54 @@ __global__ __launch_bounds__(256) void dense_sum_kernel(const float* __restrict_
   }
 }
 
-template <typename T, class C, Mode MODE, typename TO>
+template <typename T, class C, Mode MODE, typename TO, bool SPLIT = false>
 hipError_t go(const char* name, const DenseArgs& A, hipStream_t s) {
-  constexpr int SN = MODE == kGated ? C::BN / 2 : C::BN;
+  constexpr int SN = is_gated(MODE) ? C::BN / 2 : C::BN;
   const int64_t units = (int64_t)((A.R + C::BM - 1) / C::BM) * ((A.S + SN - 1) / SN) *
                         (MODE == kTN ? A.splits : 1);
   hipEvent_t e0, e1;
   prof_kernel(name, &e0, &e1);
-  hipExtLaunchKernelGGL((dense_kernel<T, C, MODE, TO>), dim3((unsigned)((units + 7) / 8 * 8)),
-                        dim3(C::NTH), 0, s, e0, e1, 0, A);
+  hipExtLaunchKernelGGL((dense_kernel<T, C, MODE, TO, SPLIT>),
+                        dim3((unsigned)((units + 7) / 8 * 8)), dim3(C::NTH), 0, s, e0, e1, 0, A);
   return hipGetLastError();
 }
 
-unsigned grid_1d(size_t threads) {
-  const size_t b = (threads + 255) / 256;
-  return (unsigned)(b < 4096 ? b : 4096);
+// The tile (256, 128 or 64 rows) for an R x S product: the largest that still
+// gives most of the 256 CUs a workgroup. fp32 stages of 256 rows do not fit LDS.
+int tile_of(bool is_bf16, int64_t R, int64_t S, int64_t copies = 1) {
+  auto units = [&](int64_t t) { return (R + t - 1) / t * ((S + t - 1) / t) * copies; };
+  if (is_bf16 && units(256) >= 192) return 256;
+  return units(128) >= 192 ? 128 : 64;
 }
 
-// k runs of a weight gradient: enough workgroups to fill the chip, at least
-// 512 tokens each, and every run's operand rows below 2 GiB.
-void tn_splits(bool is_bf16, int M, int R, int S, int& splits, int& ksplit) {
-  const int bt = is_bf16 && (int64_t)R * S >= 256 * 256 * 16 ? 256 : 128;
-  const int64_t units = (int64_t)((R + bt - 1) / bt) * ((S + bt - 1) / bt);
-  int64_t n = (256 + units - 1) / units;
-  const int64_t most = (M + 511) / 512;
-  if (n > most) n = most;
+// The k runs of a weight gradient: at least 512 tokens each, as many as bring
+// the product near 256 workgroups; and every run's operand rows below 2 GiB.
+void tn_plan(bool is_bf16, int M, int R, int S, int& tile, int& splits, int& ksplit) {
+  const int64_t most = std::max<int64_t>(1, M / 512);
+  tile = tile_of(is_bf16, R, S, std::min<int64_t>(most, 16));
+  const int64_t units = (int64_t)((R + tile - 1) / tile) * ((S + tile - 1) / tile);
+  int64_t n = std::min(most, (256 + units - 1) / units);
   const int64_t row = (int64_t)(R > S ? R : S) * (is_bf16 ? 2 : 4);
-  const int64_t least = (M * row + (1ll << 30) - 1) >> 30;
-  if (n < least) n = least;
-  if (n < 1) n = 1;
+  n = std::max<int64_t>(n, (M * row + (int64_t(1) << 30) - 1) >> 30);
   ksplit = (int)(((M + n - 1) / n + kBK - 1) / kBK * kBK);
   splits = (M + ksplit - 1) / ksplit;
+}
+
+template <typename T, Mode MODE>
+hipError_t go_gated(const char* name, const DenseArgs& A, hipStream_t s) {
+  const int tile = tile_of(sizeof(T) == 2, A.R, 2 * (int64_t)A.S);
+  if constexpr (sizeof(T) == 2)
+    if (tile == 256) return go<T, Big, MODE, T>(name, A, s);
+  if (tile == 128) return go<T, Mid, MODE, T>(name, A, s);
+  return go<T, Small, MODE, T>(name, A, s);
+}
+
+template <typename T, Mode MODE, typename TO, bool SPLIT>
+hipError_t go_tile(int tile, const char* name, const DenseArgs& A, hipStream_t s) {
+  if constexpr (sizeof(T) == 2)
+    if (tile == 256) return go<T, Big, MODE, TO, SPLIT>(name, A, s);
+  if (tile == 128) return go<T, Mid, MODE, TO, SPLIT>(name, A, s);
+  return go<T, Small64, MODE, TO, SPLIT>(name, A, s);
 }
 
 }  // namespace
@@ -400,59 +458,55 @@ hipError_t launch_gated_project(bool is_bf16, int M, int D, int F, int act, cons
                                 const void* w_in, void* z, void* h, hipStream_t s) {
   DenseArgs A{};
   A.a = x; A.b = w_in; A.out = h; A.z = z; A.R = M; A.S = F; A.K = D; A.act = act;
-  if (is_bf16) {
-    if (M >= 2048) return go<bf16, Big, kGated, bf16>("gated_project", A, s);
-    return go<bf16, Mid, kGated, bf16>("gated_project", A, s);
-  }
-  return go<float, Mid, kGated, float>("gated_project", A, s);
+  return is_bf16 ? go_gated<bf16, kGated>("gated_project", A, s)
+                 : go_gated<float, kGated>("gated_project", A, s);
 }
 
-hipError_t launch_gated_dz(bool is_bf16, int M, int F, int act, const void* z, const void* dh,
-                           void* dz, hipStream_t s) {
-  hipEvent_t e0, e1;
-  prof_kernel("gated_dz", &e0, &e1);
-  const dim3 grid(grid_1d((size_t)M * (F / 8)));
-  if (is_bf16)
-    hipExtLaunchKernelGGL(gated_dz_kernel<bf16>, grid, dim3(256), 0, s, e0, e1, 0, (const bf16*)z,
-                          (const bf16*)dh, (bf16*)dz, M, F, act);
-  else
-    hipExtLaunchKernelGGL(gated_dz_kernel<float>, grid, dim3(256), 0, s, e0, e1, 0,
-                          (const float*)z, (const float*)dh, (float*)dz, M, F, act);
-  return hipGetLastError();
+size_t gated_dz_bytes(bool is_bf16, int M, int F) {
+  return (size_t)M * 2 * F * 4;  // fp32, or two bf16 halves
 }
 
-hipError_t launch_dense_nn(bool is_bf16, bool out_f32, const char* name, int M, int K, int S,
-                           const void* a, const void* b, void* out, hipStream_t s) {
+hipError_t launch_gated_dz(bool is_bf16, int M, int D, int F, int act, const void* x,
+                           const void* w_in, const void* dh, void* dz, hipStream_t s) {
   DenseArgs A{};
-  A.a = a; A.b = b; A.out = out; A.R = M; A.S = S; A.K = K;
-  if (!is_bf16) return go<float, Mid, kNN, float>(name, A, s);
-  const bool big = M >= 4096 && S >= 192;
-  if (out_f32)
-    return big ? go<bf16, Big, kNN, float>(name, A, s) : go<bf16, Mid, kNN, float>(name, A, s);
-  return big ? go<bf16, Big, kNN, bf16>(name, A, s) : go<bf16, Mid, kNN, bf16>(name, A, s);
+  A.a = x; A.b = w_in; A.out = dz; A.dh = dh; A.R = M; A.S = F; A.K = D; A.act = act;
+  return is_bf16 ? go_gated<bf16, kGatedBwd>("gated_dz", A, s)
+                 : go_gated<float, kGatedBwd>("gated_dz", A, s);
+}
+
+hipError_t launch_dense_nn(bool is_bf16, const char* name, int M, int K, int S, const void* a,
+                           const void* a_lo, const void* b, void* out, hipStream_t s) {
+  DenseArgs A{};
+  A.a = a; A.a_lo = a_lo; A.b = b; A.out = out; A.R = M; A.S = S; A.K = K;
+  const int tile = tile_of(is_bf16, M, S);
+  if (!is_bf16) return go_tile<float, kNN, float, false>(tile, name, A, s);
+  return a_lo ? go_tile<bf16, kNN, float, true>(tile, name, A, s)
+              : go_tile<bf16, kNN, bf16, false>(tile, name, A, s);
 }
 
 size_t dense_tn_ws_bytes(bool is_bf16, int M, int R, int S) {
-  int splits, ksplit;
-  tn_splits(is_bf16, M, R, S, splits, ksplit);
+  int tile, splits, ksplit;
+  tn_plan(is_bf16, M, R, S, tile, splits, ksplit);
   return splits > 1 ? sizeof(float) * (size_t)splits * R * S : 0;
 }
 
 hipError_t launch_dense_tn(bool is_bf16, const char* name, int M, int R, int S, const void* a,
-                           const void* b, float* out, void* ws, hipStream_t s) {
+                           const void* a_lo, const void* b, float* out, void* ws, hipStream_t s) {
   DenseArgs A{};
-  A.a = a; A.b = b; A.R = R; A.S = S; A.K = M;
-  tn_splits(is_bf16, M, R, S, A.splits, A.ksplit);
+  A.a = a; A.a_lo = a_lo; A.b = b; A.R = R; A.S = S; A.K = M;
+  int tile;
+  tn_plan(is_bf16, M, R, S, tile, A.splits, A.ksplit);
   A.out = A.splits > 1 ? ws : (void*)out;
   hipError_t e;
-  if (!is_bf16) e = go<float, Mid, kTN, float>(name, A, s);
-  else if ((int64_t)R * S >= 256 * 256 * 16) e = go<bf16, Big, kTN, float>(name, A, s);
-  else e = go<bf16, Mid, kTN, float>(name, A, s);
+  if (!is_bf16) e = go_tile<float, kTN, float, false>(tile, name, A, s);
+  else if (a_lo) e = go_tile<bf16, kTN, float, true>(tile, name, A, s);
+  else e = go_tile<bf16, kTN, float, false>(tile, name, A, s);
   if (e != hipSuccess || A.splits == 1) return e;
   hipEvent_t e0, e1;
   prof_kernel("dense_sum", &e0, &e1);
   const size_t n4 = (size_t)R * S / 4;
-  hipExtLaunchKernelGGL(dense_sum_kernel, dim3(grid_1d(n4)), dim3(256), 0, s, e0, e1, 0,
+  const unsigned blocks = (unsigned)std::min<size_t>((n4 + 255) / 256, 4096);
+  hipExtLaunchKernelGGL(dense_sum_kernel, dim3(blocks), dim3(256), 0, s, e0, e1, 0,
                         (const float*)ws, A.splits, n4, out);
   return hipGetLastError();
 }

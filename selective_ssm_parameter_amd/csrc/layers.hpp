@@ -61,15 +61,19 @@ hipError_t launch_gscan_step(bool is_bf16, const void* x, const void* f, const v
 // h = act(g) u, [g | u] = x w_in^T; z may be null.
 hipError_t launch_gated_project(bool is_bf16, int M, int D, int F, int act, const void* x,
                                 const void* w_in, void* z, void* h, hipStream_t s);
-// dz [M, 2F] from z, dh.
-hipError_t launch_gated_dz(bool is_bf16, int M, int F, int act, const void* z, const void* dh,
-                           void* dz, hipStream_t s);
-// out [M, S] = a [M, K] b [K, S], out in the input type or float32.
-hipError_t launch_dense_nn(bool is_bf16, bool out_f32, const char* name, int M, int K, int S,
-                           const void* a, const void* b, void* out, hipStream_t s);
-// out [R, S] (float32) = a^T b over M rows: a [M, R], b [M, S].
+// dz = [dh u act'(g) | dh act(g)] [M, 2F], g and u recomputed from x and w_in:
+// float32, or for bf16 problems hi [M, 2F] and then lo [M, 2F], dz = hi + lo.
+size_t gated_dz_bytes(bool is_bf16, int M, int F);
+hipError_t launch_gated_dz(bool is_bf16, int M, int D, int F, int act, const void* x,
+                           const void* w_in, const void* dh, void* dz, hipStream_t s);
+// out [M, S] = a [M, K] b [K, S]; with a_lo (bf16 problems) a is a + a_lo and
+// out is float32, else out has the input type.
+hipError_t launch_dense_nn(bool is_bf16, const char* name, int M, int K, int S, const void* a,
+                           const void* a_lo, const void* b, void* out, hipStream_t s);
+// out [R, S] (float32) = (a + a_lo)^T b over M rows: a, a_lo [M, R] (a_lo may
+// be null), b [M, S].
 size_t dense_tn_ws_bytes(bool is_bf16, int M, int R, int S);
 hipError_t launch_dense_tn(bool is_bf16, const char* name, int M, int R, int S, const void* a,
-                           const void* b, float* out, void* ws, hipStream_t s);
+                           const void* a_lo, const void* b, float* out, void* ws, hipStream_t s);
 
 }  // namespace swimba

@@ -62,7 +62,9 @@ swimba_status check_act(int32_t act) {
   return SWIMBA_OK;
 }
 
-size_t gated_bwd_dz_bytes(const Dims& d) { return align256((size_t)(d.M * 2 * d.HP * elem(d))); }
+size_t gated_bwd_dz_bytes(const Dims& d) {
+  return align256(gated_dz_bytes(d.bf16, (int)d.M, (int)d.HP));
+}
 
 size_t layer_ws(const Dims& d, int32_t call) {
   if (d.M == 0) return 0;
@@ -268,9 +270,9 @@ swimba_status swimba_gated_project(const swimba_dims* dims, const void* x, const
 }
 
 swimba_status swimba_gated_project_backward(const swimba_dims* dims, const void* x,
-                                            const void* w_in, const void* z, const void* dh,
-                                            int32_t act, float* dx, float* dw_in, void* ws,
-                                            size_t ws_bytes, hipStream_t stream) {
+                                            const void* w_in, const void* dh, int32_t act,
+                                            float* dx, float* dw_in, void* ws, size_t ws_bytes,
+                                            hipStream_t stream) {
   Dims d;
   swimba_status st = read_layer_dims(dims, d);
   if (st != SWIMBA_OK) return st;
@@ -282,18 +284,19 @@ swimba_status swimba_gated_project_backward(const swimba_dims* dims, const void*
                       "gated_project_backward launch");
   REQUIRE_PTR(x);
   REQUIRE_PTR(w_in);
-  REQUIRE_PTR(z);
   REQUIRE_PTR(dh);
   REQUIRE_PTR(dx);
   if ((st = check_ws(ws, ws_bytes, layer_ws(d, SWIMBA_LAYER_GATED_PROJECT_BACKWARD))) != SWIMBA_OK)
     return st;
   const int M = (int)d.M, D = (int)d.D, F = (int)d.HP;
-  unsigned char* part = static_cast<unsigned char*>(ws) + gated_bwd_dz_bytes(d);
-  hipError_t e = launch_gated_dz(d.bf16, M, F, act, z, dh, ws, stream);
+  unsigned char* w8 = static_cast<unsigned char*>(ws);
+  const void* lo = d.bf16 ? w8 + (size_t)M * 2 * F * 2 : nullptr;
+  hipError_t e = launch_gated_dz(d.bf16, M, D, F, act, x, w_in, dh, ws, stream);
   if (e != hipSuccess) return hip_status(e, "gated_project_backward dz launch");
-  e = launch_dense_nn(d.bf16, true, "gated_dx", M, 2 * F, D, ws, w_in, dx, stream);
+  e = launch_dense_nn(d.bf16, "gated_dx", M, 2 * F, D, ws, lo, w_in, dx, stream);
   if (e != hipSuccess) return hip_status(e, "gated_project_backward dx launch");
-  return hip_status(launch_dense_tn(d.bf16, "gated_dw", M, 2 * F, D, ws, x, dw_in, part, stream),
+  return hip_status(launch_dense_tn(d.bf16, "gated_dw", M, 2 * F, D, ws, lo, x, dw_in,
+                                    w8 + gated_bwd_dz_bytes(d), stream),
                     "gated_project_backward dw launch");
 }
 
@@ -316,9 +319,10 @@ swimba_status swimba_output_project_backward(const swimba_dims* dims, const void
   if ((st = check_ws(ws, ws_bytes, layer_ws(d, SWIMBA_LAYER_OUTPUT_PROJECT_BACKWARD))) != SWIMBA_OK)
     return st;
   const int M = (int)d.M, D = (int)d.D, F = (int)d.HP;
-  hipError_t e = launch_dense_nn(d.bf16, false, "output_project_dy", M, D, F, dout, w_out, dy, stream);
+  hipError_t e = launch_dense_nn(d.bf16, "output_project_dy", M, D, F, dout, nullptr, w_out, dy, stream);
   if (e != hipSuccess) return hip_status(e, "output_project_backward dy launch");
-  return hip_status(launch_dense_tn(d.bf16, "output_project_dw", M, D, F, dout, y, dw_out, ws, stream),
+  return hip_status(launch_dense_tn(d.bf16, "output_project_dw", M, D, F, dout, nullptr, y, dw_out, ws,
+                                    stream),
                     "output_project_backward dw launch");
 }
 

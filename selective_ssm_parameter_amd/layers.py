@@ -14,7 +14,7 @@ import ctypes
 import torch
 
 from . import binding as sb
-from .binding import SwimbaError, _check, _stream  # noqa: F401  (SwimbaError: what calls raise)
+from .binding import SwimbaError, _check  # noqa: F401  (SwimbaError: what calls raise)
 
 ACT_SILU, ACT_GELU = 0, 1
 (LAYER_NORM_BACKWARD, LAYER_GATED_SCAN, LAYER_GATED_SCAN_BACKWARD, LAYER_GATED_PROJECT_BACKWARD,
@@ -51,7 +51,7 @@ def lib() -> ctypes.CDLL:
             ("swimba_gated_step", I32, [D, P, P, P, I64, P, P, P, P]),
             ("swimba_gated_project", I32, [D, P, P, I32, P, P, P]),
             ("swimba_gated_project_backward", I32,
-             [D, P, P, P, P, I32, P, P, P, SZ, P]),
+             [D, P, P, P, I32, P, P, P, SZ, P]),
             ("swimba_output_project_backward", I32, [D, P, P, P, P, P, P, SZ, P])):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = res, args
@@ -78,33 +78,57 @@ def gated_scan_carry(dims, device="cuda") -> torch.Tensor:
     return torch.empty(max(n // 4, 4), dtype=torch.float32, device=device)
 
 
-def _ptr(t):
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensor on {t.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return sb._ptr(t)
+def _ptrs(*tensors):
+    """Device pointers of contiguous tensors on the current device (None stays None)."""
+    cur, out = torch.cuda.current_device() if torch.cuda.is_initialized() else -1, []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if not t.is_contiguous():
+            raise ValueError("tensors passed to the Swimba library must be contiguous")
+        if t.get_device() != cur:
+            _wrong_device(t, cur)
+        out.append(t.data_ptr())
+    return out
+
+
+def _wrong_device(t, cur):
+    raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
 
 
 def _rows(*tensors):
     """Pointers of [M, C] tensors whose rows are equally far apart, and that distance."""
+    cur = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
     ld, ptrs = None, []
     for t in tensors:
         if t is None:
             ptrs.append(None)
             continue
-        t2 = t.reshape(-1, t.shape[-1]) if t.dim() != 2 and t.is_contiguous() else t
-        if t2.dim() != 2 or (t2.stride(1) != 1 and t2.shape[1] > 1):
-            raise ValueError("rows of the gated scan must be [tokens, channels] with unit stride "
-                             "along the channels")
-        step = t2.stride(0) if t2.shape[0] > 1 else max(t2.stride(0), t2.shape[1])
-        if ld is None or t2.shape[0] <= 1:
-            ld = step if ld is None else ld
+        if t.dim() != 2:
+            t = t.view(-1, t.shape[-1])
+        rows, cols = t.shape
+        step, unit = t.stride()
+        if unit != 1 and cols > 1:
+            raise ValueError("rows of the gated scan must have unit stride along the channels")
+        if rows <= 1:
+            step = max(step, cols) if ld is None else ld
+        if ld is None:
+            ld = step
         elif step != ld:
             raise ValueError("the gated scan's tensors must have one row stride")
-        if t2.is_cuda and t2.device.index != torch.cuda.current_device():
-            _ptr(t2)  # raises
-        ptrs.append(t2.data_ptr())
+        if t.get_device() != cur:
+            _wrong_device(t, cur)
+        ptrs.append(t.data_ptr())
     return ptrs, ld
+
+
+def _stream(stream):
+    if stream is None:
+        # the current stream's handle without a Stream object: a decode step is
+        # a few microseconds on the GPU
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _ws(ws, ws_bytes):
@@ -116,9 +140,9 @@ def _ws(ws, ws_bytes):
 
 def swimba_layer_norm(dims, x, residual, weight, bias, eps, sum, y, mean=None, rstd=None,
                       stream=None):
-    _check(lib().swimba_layer_norm(
-        ctypes.byref(dims), _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), eps, _ptr(sum),
-        _ptr(y), _ptr(mean), _ptr(rstd), _stream(stream)))
+    px, pr, pw, pb, ps, py, pm, pq = _ptrs(x, residual, weight, bias, sum, y, mean, rstd)
+    _check(lib().swimba_layer_norm(ctypes.byref(dims), px, pr, pw, pb, eps, ps, py, pm, pq,
+                                   _stream(stream)))
 
 
 def swimba_layer_norm_backward(dims, s, weight, mean, rstd, dy, dres, dx, dweight, dbias, ws,
@@ -126,50 +150,48 @@ def swimba_layer_norm_backward(dims, s, weight, mean, rstd, dy, dres, dx, dweigh
     if dy is not None and dy.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"dy of {dy.dtype}: bfloat16 or float32")
     dy_dtype = sb.BF16 if dy is not None and dy.dtype == torch.bfloat16 else sb.F32
-    _check(lib().swimba_layer_norm_backward(
-        ctypes.byref(dims), _ptr(s), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy), dy_dtype,
-        _ptr(dres), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ws), _ws(ws, ws_bytes),
-        _stream(stream)))
+    p = _ptrs(s, weight, mean, rstd, dy, dres, dx, dweight, dbias, ws)
+    _check(lib().swimba_layer_norm_backward(ctypes.byref(dims), *p[:5], dy_dtype, *p[5:],
+                                            _ws(ws, ws_bytes), _stream(stream)))
 
 
 def swimba_gated_scan(dims, x, forget, gate, seq_lens, h_init, y, h_final, carry, ws,
                       ws_bytes=None, stream=None):
-    (px, pf, po), ld = _rows(x, forget, gate)
-    _check(lib().swimba_gated_scan(
-        ctypes.byref(dims), px, pf, po, ld, _ptr(seq_lens), _ptr(h_init), _ptr(y), _ptr(h_final),
-        _ptr(carry), _ptr(ws), _ws(ws, ws_bytes), _stream(stream)))
+    rows, ld = _rows(x, forget, gate)
+    p = _ptrs(seq_lens, h_init, y, h_final, carry, ws)
+    _check(lib().swimba_gated_scan(ctypes.byref(dims), *rows, ld, *p, _ws(ws, ws_bytes),
+                                   _stream(stream)))
 
 
 def swimba_gated_scan_backward(dims, x, forget, gate, seq_lens, carry, dy, dh_final, dx, dforget,
                                dgate, dh_init, ws, ws_bytes=None, stream=None):
-    (px, pf, po), ld = _rows(x, forget, gate)
-    (pdx, pdf, pdo), ldd = _rows(dx, dforget, dgate if gate is not None else None)
-    _check(lib().swimba_gated_scan_backward(
-        ctypes.byref(dims), px, pf, po, ld, _ptr(seq_lens), _ptr(carry), _ptr(dy),
-        _ptr(dh_final), pdx, pdf, pdo, ldd, _ptr(dh_init), _ptr(ws), _ws(ws, ws_bytes),
-        _stream(stream)))
+    rows, ld = _rows(x, forget, gate)
+    drows, ldd = _rows(dx, dforget, dgate if gate is not None else None)
+    p = _ptrs(seq_lens, carry, dy, dh_final, dh_init, ws)
+    _check(lib().swimba_gated_scan_backward(ctypes.byref(dims), *rows, ld, *p[:4], *drows, ldd,
+                                            *p[4:], _ws(ws, ws_bytes), _stream(stream)))
 
 
 def swimba_gated_step(dims, x, forget, gate, h_prev, h, y, stream=None):
-    (px, pf, po), ld = _rows(x, forget, gate)
-    _check(lib().swimba_gated_step(ctypes.byref(dims), px, pf, po, ld, _ptr(h_prev), _ptr(h),
-                                   _ptr(y), _stream(stream)))
+    rows, ld = _rows(x, forget, gate)
+    _check(lib().swimba_gated_step(ctypes.byref(dims), *rows, ld, *_ptrs(h_prev, h, y),
+                                   _stream(stream)))
 
 
 def swimba_gated_project(dims, x, w_in, act, z, h, stream=None):
-    _check(lib().swimba_gated_project(ctypes.byref(dims), _ptr(x), _ptr(w_in), act, _ptr(z),
-                                      _ptr(h), _stream(stream)))
+    px, pw, pz, ph = _ptrs(x, w_in, z, h)
+    _check(lib().swimba_gated_project(ctypes.byref(dims), px, pw, act, pz, ph, _stream(stream)))
 
 
-def swimba_gated_project_backward(dims, x, w_in, z, dh, act, dx, dw_in, ws, ws_bytes=None,
+def swimba_gated_project_backward(dims, x, w_in, dh, act, dx, dw_in, ws, ws_bytes=None,
                                   stream=None):
-    _check(lib().swimba_gated_project_backward(
-        ctypes.byref(dims), _ptr(x), _ptr(w_in), _ptr(z), _ptr(dh), act, _ptr(dx), _ptr(dw_in),
-        _ptr(ws), _ws(ws, ws_bytes), _stream(stream)))
+    px, pw, pd, pdx, pdw, pws = _ptrs(x, w_in, dh, dx, dw_in, ws)
+    _check(lib().swimba_gated_project_backward(ctypes.byref(dims), px, pw, pd, act, pdx, pdw, pws,
+                                               _ws(ws, ws_bytes), _stream(stream)))
 
 
 def swimba_output_project_backward(dims, y, w_out, dout, dy, dw_out, ws, ws_bytes=None,
                                    stream=None):
     _check(lib().swimba_output_project_backward(
-        ctypes.byref(dims), _ptr(y), _ptr(w_out), _ptr(dout), _ptr(dy), _ptr(dw_out), _ptr(ws),
-        _ws(ws, ws_bytes), _stream(stream)))
+        ctypes.byref(dims), *_ptrs(y, w_out, dout, dy, dw_out, ws), _ws(ws, ws_bytes),
+        _stream(stream)))

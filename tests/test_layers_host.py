@@ -65,8 +65,8 @@ def proj(d, x=FAKE, w=FAKE, act=0, z=None, h=FAKE):
     return lib().swimba_gated_project(ref(d), x, w, act, z, h, None)
 
 
-def proj_b(d, x=FAKE, w=FAKE, z=FAKE, dh=FAKE, act=0, dx=FAKE, dw=FAKE, ws=FAKE, nb=BIG):
-    return lib().swimba_gated_project_backward(ref(d), x, w, z, dh, act, dx, dw, ws, nb, None)
+def proj_b(d, x=FAKE, w=FAKE, dh=FAKE, act=0, dx=FAKE, dw=FAKE, ws=FAKE, nb=BIG):
+    return lib().swimba_gated_project_backward(ref(d), x, w, dh, act, dx, dw, ws, nb, None)
 
 
 def out_b(d, y=FAKE, w=FAKE, do=FAKE, dy=FAKE, dw=FAKE, ws=FAKE, nb=BIG):
@@ -175,9 +175,9 @@ def test_projection_refusals():
     assert proj(dims(seqlen=0), x=None, w=None, h=None) == 0
     need = sl.layer_workspace_size(d, sl.LAYER_GATED_PROJECT_BACKWARD)
     assert need >= 200 * 2 * 192 * 2
-    for kw in ("x", "w", "z", "dh", "dx", "dw"):
+    for kw in ("x", "w", "dh", "dx", "dw"):
         assert proj_b(d, **{kw: None}) == -1, kw
-    for kw in ("x", "w", "z", "dh", "dx", "dw", "ws"):
+    for kw in ("x", "w", "dh", "dx", "dw", "ws"):
         assert proj_b(d, **{kw: MISALIGNED}) == -5, kw
     assert proj_b(d, nb=need - 1) == -4 and proj_b(d, act=9) == -2
     for kw in ("y", "w", "do", "dy", "dw"):
