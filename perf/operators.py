@@ -275,7 +275,7 @@ def _run_own(st):
         return {"h": st["h"]}
     if kind == "gated_train":
         sl.swimba_gated_project(dims, st["x"], st["w_in"], st["act"], st["z"], st["h"])
-        sl.swimba_gated_project_backward(dims, st["x"], st["w_in"], st["z"], st["dh"], st["act"],
+        sl.swimba_gated_project_backward(dims, st["x"], st["w_in"], st["dh"], st["act"],
                                          st["dx"], st["dw"], st["ws"])
         return {"h": st["h"], "z": st["z"], "dx": st["dx"], "dw": st["dw"]}
     sl.swimba_output_project_backward(dims, st["y"], st["w_out"], st["dout"], st["dy"], st["dw"],
