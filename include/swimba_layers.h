@@ -106,7 +106,7 @@ swimba_status swimba_layer_norm_backward(const swimba_dims* dims, const void* s,
  * therefore gives infinity or NaN from that token on, in that channel
  * of that sequence only).
  *   x, forget, gate  [M, C] dtype, gate may be NULL; rows `ld` elements apart
- *             (ld >= C), so that all three may be column ranges of one
+ *             (C <= ld < 2^22), so that all three may be column ranges of one
  *             projection's output
  *   seq_lens  [batch] int32, or NULL: tokens of each sequence that are in
  *             use (a value outside [0, seqlen] counts as the nearest bound).
@@ -137,8 +137,8 @@ size_t swimba_gated_scan_carry_size(const swimba_dims* dims);
  *   x, forget, gate, ld, seq_lens   as given to the forward
  *   carry     as the forward wrote it for the same inputs
  *   dy        [M, C] dtype;  dh_final [batch, C] float32, or NULL for zeros
- *   dx, dforget, dgate  [M, C] dtype out, rows `ldd` elements apart (ldd >=
- *             C), zeros past a sequence's length; dgate is required with a
+ *   dx, dforget, dgate  [M, C] dtype out, rows `ldd` elements apart (C <=
+ *             ldd < 2^22), zeros past a sequence's length; dgate is required with a
  *             gate and ignored without
  *   dh_init   [batch, C] float32 out, or NULL; may be the same tensor as
  *             dh_final
@@ -155,7 +155,7 @@ swimba_status swimba_gated_scan_backward(const swimba_dims* dims, const void* x,
  * One token of the recurrence for `batch` sequences (dims->seqlen must be 1),
  * without a workspace:
  *   h = f h_prev + (1 - f) x,   y = h silu(gate).
- *   x, forget, gate  [batch, C] dtype, rows `ld` apart; gate may be NULL
+ *   x, forget, gate  [batch, C] dtype, rows `ld` apart (C <= ld < 2^22); gate may be NULL
  *   h_prev    [batch, C] float32;  h [batch, C] float32 out, may be h_prev
  *   y         [batch, C] dtype out
  */

@@ -4,10 +4,20 @@
 //   e_t = dy silu(gate) + f_{t+1} e_{t+1},  dx = g e,  dforget = f g e (h_{t-1} - x),
 //   dgate = dy h silu'(gate).
 // A run of tokens maps the state that enters it to P h + S, with P the product
-// of its f: runs are composed as (P_a P_b, S_b + P_b S_a), which is how threads,
-// waves and chunks are joined (chunks of 256 tokens x 64 channels per
-// workgroup; a thread holds 32 elements, so a chunk is read once per pass and
-// its tokens are walked in registers).
+// of its f, and runs are composed: thread (16 tokens of 2 channels, walked in
+// registers), wave (128 channels), workgroup (8 waves, a chunk of 128 tokens),
+// sequence. Bound by HBM: each tensor is read once, by one kernel. A chunk's
+// workgroup publishes its run, then waits for what precedes it: the runs of the
+// earlier chunks of its group of 16, and the state that enters the group, which
+// the last workgroup of the group before publishes; so a sequence is a chain of
+// one hop per 2048 tokens, and the order of every sum is fixed. A published
+// value is one 64-bit word that is stored and loaded whole, all ones until then
+// (a fill before the kernel; a NaN is stored in its canonical form), so no
+// ordering between words is needed. A workgroup's index gives its sequence and
+// channels (its chain); its chunk is the next number of the chain's counter, so
+// that it only ever waits for workgroups that took an earlier number of the
+// same chain and hence already run: every wait ends. (One counter for all
+// workgroups cost about 115 ns each: 65536 tokens x 2048 channels took 957 us.)
 //
 // The steps keep their relative precision where f is near 1 (a memory of many
 // tokens) and near 0 (a reset): with small = min(f, g) = t / (1 + t), t =
@@ -15,6 +25,9 @@
 // x - f (x - h) otherwise; the pair is kept as k = small with forget's sign.
 // P is kept the same way: 1 - P (as G) next to P, and the one that is not
 // close to 1 is used.
+#include <algorithm>
+#include <type_traits>
+
 #include "common.hpp"
 #include "layers.hpp"
 
@@ -23,41 +36,37 @@ namespace swimba {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kChunk = 256;   // tokens per chunk
-constexpr int kCh = 64;       // channels per workgroup
-constexpr int kTh = 512;      // threads per workgroup
-constexpr int kEl = kChunk * kCh / kTh;  // elements per thread
+constexpr int kTpt = 16;            // consecutive tokens per thread
+constexpr int kWaves = 8;
+constexpr int kTh = 64 * kWaves;
+constexpr int kChunk = kTpt * kWaves;  // tokens per workgroup
+constexpr int kGroup = 16;          // chunks per group
+constexpr uint64_t kUnset = ~0ull;
 
-// Thread layout for VEC channels per access: LC lanes cover the workgroup's 64
-// channels, TG groups of TPT consecutive tokens cover the chunk.
-template <int VEC>
-struct Lay {
-  static constexpr int LC = kCh / VEC, TG = kTh / LC, TPT = kChunk / TG, GW = 64 / LC;
-  static_assert(TPT * VEC == kEl, "elements per thread");
-};
-
-template <typename T, int VEC> struct Raw {
-  typedef T t __attribute__((ext_vector_type(VEC)));
-};
-template <typename T> struct Raw<T, 1> {
-  struct t {
-    T v;
-    __device__ T operator[](int) const { return v; }
-  };
-};
+// One access of VEC channels (2 or 4 bytes) at byte offset off of a row that
+// starts `row` bytes into a buffer: with off = kOOB a load reads zeros and a
+// store is dropped.
 template <typename T, int VEC>
-__device__ __forceinline__ typename Raw<T, VEC>::t load_raw(const T* p) {
-  return *reinterpret_cast<const typename Raw<T, VEC>::t*>(p);
+__device__ __forceinline__ uint32_t load_bits(BufRes r, uint32_t off, uint32_t row) {
+  if constexpr (sizeof(T) * VEC == 4) return __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0);
+  else return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, row, 0);
 }
 template <typename T, int VEC>
-__device__ __forceinline__ void store_raw(T* p, const float* v) {
-  if constexpr (VEC == 1) {
-    p[0] = from_f32<T>(v[0]);
+__device__ __forceinline__ float channel(uint32_t bits, int j) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(bits);
+  else return __uint_as_float(j == 0 ? bits << 16 : bits & 0xFFFF0000u);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_bits(BufRes r, uint32_t off, uint32_t row, const float* v) {
+  if constexpr (sizeof(T) == 4) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), r, off, row, 0);
+  } else if constexpr (VEC == 2) {
+    typedef T T2 __attribute__((ext_vector_type(2)));
+    const T2 t = {from_f32<T>(v[0]), from_f32<T>(v[1])};
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, t), r, off, row, 0);
   } else {
-    typename Raw<T, VEC>::t r;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) r[j] = from_f32<T>(v[j]);
-    *reinterpret_cast<typename Raw<T, VEC>::t*>(p) = r;
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, from_f32<T>(v[0])), r, off, row,
+                                          0);
   }
 }
 
@@ -89,18 +98,18 @@ struct Run {
   float G, P, S;
 };
 __device__ __forceinline__ Run identity() { return Run{0.f, 1.f, 0.f}; }
-__device__ __forceinline__ float apply(const Run& r, float h) {
-  return r.S + (r.G <= 0.5f ? __builtin_fmaf(-r.G, h, h) : r.P * h);
-}
+// P as one number: G, or -P where that is the smaller one (as k for a token)
+__device__ __forceinline__ float factor(const Run& r) { return r.G <= 0.5f ? r.G : -r.P; }
+__device__ __forceinline__ float apply(const Run& r, float h) { return r.S + decay(factor(r), h); }
 // a, then b
 __device__ __forceinline__ Run join(const Run& a, const Run& b) {
   return Run{__builtin_fmaf(-a.G, b.G, a.G + b.G), a.P * b.P, apply(b, a.S)};
 }
-__device__ __forceinline__ Run shfl_up(const Run& r, int d) {
-  return Run{__shfl_up(r.G, d), __shfl_up(r.P, d), __shfl_up(r.S, d)};
-}
-__device__ __forceinline__ Run shfl_down(const Run& r, int d) {
-  return Run{__shfl_down(r.G, d), __shfl_down(r.P, d), __shfl_down(r.S, d)};
+// One more token: S by the caller; G and P are the responses to a constant
+// input 1 and to an initial state 1.
+__device__ __forceinline__ void extend(Run& r, float k) {
+  r.G = __builtin_fmaf(k, 1.f - r.G, neg(k) ? 1.f : r.G);
+  r.P = decay(k, r.P);
 }
 
 __device__ __forceinline__ int seq_len(const int32_t* lens, int b, int T) {
@@ -109,298 +118,324 @@ __device__ __forceinline__ int seq_len(const int32_t* lens, int b, int T) {
   return n < 0 ? 0 : (n > T ? T : n);
 }
 
-// What precedes this thread's tokens within the chunk (exclusive run), per
-// channel, and the whole chunk's run. REV: runs are joined from the last token
-// backwards (the backward's direction).
-template <int VEC, bool REV>
-__device__ __forceinline__ void chunk_runs(const Run (&own)[VEC], Run (&excl)[VEC],
-                                           Run (&total)[VEC], float (&sh)[3][8][kCh]) {
-  typedef Lay<VEC> L;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int cl = lane % L::LC;
-  Run incl[VEC];
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) incl[j] = own[j];
-#pragma unroll
-  for (int d = L::LC; d < 64; d *= 2) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const Run o = REV ? shfl_down(incl[j], d) : shfl_up(incl[j], d);
-      const bool ok = REV ? lane + d < 64 : lane >= d;
-      const Run n = join(o, incl[j]);
-      if (ok) incl[j] = n;
-    }
-  }
-  // the wave's run is in its last (REV: first) token group
-  const bool last = REV ? lane < L::LC : lane >= 64 - L::LC;
-  __syncthreads();  // sh is no longer read
-  if (last) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      sh[0][wave][cl * VEC + j] = incl[j].G;
-      sh[1][wave][cl * VEC + j] = incl[j].P;
-      sh[2][wave][cl * VEC + j] = incl[j].S;
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    Run ex = identity();
-    if constexpr (L::GW > 1) {
-      const Run o = REV ? shfl_down(incl[j], L::LC) : shfl_up(incl[j], L::LC);
-      const bool first = REV ? lane >= 64 - L::LC : lane < L::LC;
-      if (!first) ex = o;
-    }
-    Run before = identity(), all = identity();
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int w = REV ? 7 - q : q;
-      const Run r{sh[0][w][cl * VEC + j], sh[1][w][cl * VEC + j], sh[2][w][cl * VEC + j]};
-      if (w == wave) before = all;
-      all = join(all, r);
-    }
-    excl[j] = join(before, ex);
-    total[j] = all;
-  }
-}
+// ---------------------------------------------------------------- chunks
 
-// Tokens of the chunk that this thread holds and whether its channels exist.
+struct Shared {
+  float run[3][kWaves][128];           // each wave's run
+  float2 prev[kGroup][128];            // the earlier runs of the group: factor, S
+  float enter[128];                    // the state that enters the group
+  uint32_t ticket;
+};
+
+// A workgroup's chain (sequence and block of channels) and chunk, and the tokens
+// of this thread. REV: the chain runs from the last chunk.
 template <int VEC>
 struct Place {
   int b, chunk, c, t0, len;  // c: first channel; t0: first token within the sequence
+  int step, nc, wave;        // position along the direction of the scan
   size_t cw;                 // row of the chunk among all sequences' chunks
   bool on;
-  __device__ Place(const GScanArgs& A) {
-    typedef Lay<VEC> L;
-    const unsigned ncb = (A.C + kCh - 1) / kCh;  // chunks run slowest, then sequences
-    const unsigned q = blockIdx.x / ncb;
-    b = q % A.Bt;
-    chunk = q / A.Bt;
-    cw = (size_t)b * ((A.T + kChunk - 1) / kChunk) + chunk;
-    c = (blockIdx.x - q * ncb) * kCh + (threadIdx.x % L::LC) * VEC;
-    t0 = chunk * kChunk + (threadIdx.x / L::LC) * L::TPT;
-    len = seq_len(A.lens, b, A.T);
-    on = c < A.C;
+  template <bool REV>
+  static __device__ Place make(const GScanArgs& A, unsigned chain, int step) {
+    Place p;
+    const unsigned ncb = (A.C + 64 * VEC - 1) / (64 * VEC);
+    p.nc = (A.T + kChunk - 1) / kChunk;
+    // uniform, and said to be: buffers are built from them
+    p.b = __builtin_amdgcn_readfirstlane(chain / ncb);
+    p.step = step;
+    p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    p.chunk = REV ? p.nc - 1 - p.step : p.step;
+    p.cw = (size_t)p.b * p.nc + p.chunk;
+    p.c = (chain - p.b * ncb) * 64 * VEC + (threadIdx.x & 63) * VEC;
+    p.t0 = p.chunk * kChunk + p.wave * kTpt;
+    p.len = __builtin_amdgcn_readfirstlane(seq_len(A.lens, p.b, A.T));
+    p.on = p.c < A.C;
+    return p;
   }
 };
 
-// ---------------------------------------------------------------- forward
+__device__ __forceinline__ uint64_t word(float lo, float hi) {
+  return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ float canonical(float v) {
+  return v != v ? __uint_as_float(0x7FC00000u) : v;
+}
+__device__ __forceinline__ uint64_t peek(const uint64_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void post(uint64_t* p, uint64_t v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 
-// Pass 1: each chunk's run, to ws [Bt][chunks][3][C].
-template <typename T, int VEC>
-__global__ __launch_bounds__(kTh) void gscan_runs_kernel(GScanArgs A) {
-  typedef Lay<VEC> L;
-  __shared__ float sh[3][8][kCh];
-  const Place<VEC> p(A);
-  const T* x = static_cast<const T*>(A.x);
-  const T* f = static_cast<const T*>(A.f);
-  Run own[VEC], excl[VEC], total[VEC];
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) own[j] = identity();
-#pragma unroll
-  for (int i = 0; i < L::TPT; ++i) {
-    if (p.on && p.t0 + i < p.len) {
-      const size_t off = ((size_t)p.b * A.T + p.t0 + i) * A.ld + p.c;
-      const auto xr = load_raw<T, VEC>(x + off);
-      const auto fr = load_raw<T, VEC>(f + off);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float k = gate_of(to_f32(fr[j]));
-        const float g = neg(k) ? 1.f + k : k;
-        own[j].G = __builtin_fmaf(g, 1.f - own[j].G, own[j].G);
-        own[j].P *= forget_of(k);
-        own[j].S = step(k, to_f32(xr[j]), own[j].S);
-      }
-    }
+// The workspace: a counter per chain, 128 bytes apart; a word per chunk and
+// channel (the chunk's run: S, factor); a word per group and channel (the state
+// entering it). All of it starts as all ones.
+constexpr size_t kCounterStep = 128;
+size_t __host__ __device__ inline counter_bytes(int Bt, int C) {
+  return kCounterStep * (size_t)Bt * ((C + 63) / 64);  // the most chains there are
+}
+struct Board {
+  uint64_t *runs, *enter;
+  int ng;  // groups per sequence
+  __device__ Board(const GScanArgs& A, int nc) {
+    runs = reinterpret_cast<uint64_t*>(static_cast<char*>(A.ws) + counter_bytes(A.Bt, A.C));
+    enter = runs + (size_t)A.Bt * nc * A.C;
+    ng = (nc + kGroup - 1) / kGroup;
   }
-  chunk_runs<VEC, false>(own, excl, total, sh);
-  if (p.on && threadIdx.x < L::LC) {
-    float* w = static_cast<float*>(A.ws) + p.cw * 3 * A.C + p.c;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      w[j] = total[j].G;
-      w[A.C + j] = total[j].P;
-      w[2 * (size_t)A.C + j] = total[j].S;
-    }
+};
+
+// The workgroup's place: its chain from its index, its chunk from the chain's
+// counter.
+template <int VEC, bool REV, bool CHAIN>
+__device__ __forceinline__ Place<VEC> take_place(const GScanArgs& A, Shared& sh) {
+  if constexpr (CHAIN) {
+    const unsigned chains = (unsigned)A.Bt * ((A.C + 64 * VEC - 1) / (64 * VEC));
+    const unsigned chain = blockIdx.x % chains;
+    if (threadIdx.x == 0)
+      sh.ticket = atomicAdd(reinterpret_cast<uint32_t*>(static_cast<char*>(A.ws) +
+                                                        kCounterStep * chain), 1u) + 1u;
+    __syncthreads();
+    return Place<VEC>::template make<REV>(A, chain, __builtin_amdgcn_readfirstlane(sh.ticket));
+  } else {
+    return Place<VEC>::template make<REV>(A, blockIdx.x, 0);
   }
 }
 
-// Pass 2: the state entering each chunk (REV: the gradient leaving it), by
-// walking the chunks' runs; written over the runs' S.
-template <bool REV>
-__global__ __launch_bounds__(64) void gscan_carry_kernel(float* ws, int nc, int C,
-                                                         const float* init, float* final_out,
-                                                         float* carry) {
-  const int ncb = (C + 63) / 64, b = blockIdx.x / ncb;
-  const int c = (blockIdx.x - b * ncb) * 64 + threadIdx.x;
-  if (c >= C) return;
-  float h = init ? init[(size_t)b * C + c] : 0.f;
-  for (int q = 0; q < nc; ++q) {
-    const int i = REV ? nc - 1 - q : q;
-    float* w = ws + ((size_t)b * nc + i) * 3 * C + c;
-    const Run r{w[0], w[C], w[2 * (size_t)C]};
-    w[2 * (size_t)C] = h;
-    if (carry) carry[((size_t)b * nc + i) * C + c] = h;
-    h = apply(r, h);
+// From each thread's run (own) to the state that enters its tokens. start: the
+// state that enters the first chunk. Also returns the state that enters the
+// chunk and, in the wave at the end of the chunk, the state that leaves it.
+// CHAIN: the sequence has more than one chunk.
+template <int VEC, bool REV, bool CHAIN>
+__device__ __forceinline__ void enter_states(const GScanArgs& A, const Place<VEC>& p, Shared& sh,
+                                             const Run (&own)[VEC], const float* start,
+                                             float (&mine)[VEC], float (&chunk_in)[VEC],
+                                             float (&chunk_out)[VEC]) {
+  const int lane = threadIdx.x & 63;
+  const int ord = REV ? kWaves - 1 - p.wave : p.wave;  // position along the scan
+  const int l0 = lane * VEC;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    sh.run[0][ord][l0 + j] = own[j].G;
+    sh.run[1][ord][l0 + j] = own[j].P;
+    sh.run[2][ord][l0 + j] = own[j].S;
   }
-  if (final_out) final_out[(size_t)b * C + c] = h;
-}
+  __syncthreads();
+  Run before[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) before[j] = identity();
+  for (int w = 0; w < ord; ++w) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      before[j] = join(before[j], Run{sh.run[0][w][l0 + j], sh.run[1][w][l0 + j],
+                                      sh.run[2][w][l0 + j]});
+  }
+  const bool last = ord == kWaves - 1;
+  Run total[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) total[j] = join(before[j], own[j]);  // used by the last wave
 
-// Pass 3: the outputs of each chunk from the state entering it.
-template <typename T, int VEC>
-__global__ __launch_bounds__(kTh) void gscan_out_kernel(GScanArgs A) {
-  typedef Lay<VEC> L;
-  __shared__ float sh[3][8][kCh];
-  const Place<VEC> p(A);
-  const T* x = static_cast<const T*>(A.x);
-  const T* f = static_cast<const T*>(A.f);
-  const T* o = static_cast<const T*>(A.o);
-  T* y = static_cast<T*>(A.y);
-  float k[L::TPT][VEC], xv[L::TPT][VEC];
-  Run own[VEC], excl[VEC], total[VEC];
+  if constexpr (!CHAIN) {
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) own[j] = identity();
+    for (int j = 0; j < VEC; ++j)
+      chunk_in[j] = start && p.on ? start[(size_t)p.b * A.C + p.c + j] : 0.f;
+  } else {
+    const Board bd(A, p.nc);
+    const int g = p.step / kGroup, i = p.step % kGroup;
+    const size_t row0 = (size_t)p.b * p.nc + g * kGroup;  // runs in the order of the scan
+    if (last && p.on && i + 1 < kGroup && p.step + 1 < p.nc) {
 #pragma unroll
-  for (int i = 0; i < L::TPT; ++i) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) k[i][j] = xv[i][j] = 0.f;
-    if (p.on && p.t0 + i < p.len) {
-      const size_t off = ((size_t)p.b * A.T + p.t0 + i) * A.ld + p.c;
-      const auto xr = load_raw<T, VEC>(x + off);
-      const auto fr = load_raw<T, VEC>(f + off);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        k[i][j] = gate_of(to_f32(fr[j]));
-        xv[i][j] = to_f32(xr[j]);
-        const float g = neg(k[i][j]) ? 1.f + k[i][j] : k[i][j];
-        own[j].G = __builtin_fmaf(g, 1.f - own[j].G, own[j].G);
-        own[j].P *= forget_of(k[i][j]);
-        own[j].S = step(k[i][j], xv[i][j], own[j].S);
-      }
+      for (int j = 0; j < VEC; ++j)
+        post(bd.runs + (row0 + i) * A.C + p.c + j,
+             word(canonical(total[j].S), canonical(factor(total[j]))));
     }
-  }
-  chunk_runs<VEC, false>(own, excl, total, sh);
-  if (!p.on) return;
-  const float* w = static_cast<const float*>(A.ws) + p.cw * 3 * A.C + p.c;
-  float h[VEC];
+    // wave w collects the runs of chunks w and w + 8 of the group; the first
+    // wave also the entering state
+    if (p.on) {
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) h[j] = apply(excl[j], w[2 * (size_t)A.C + j]);
+      for (int h = 0; h < kGroup / kWaves; ++h) {
+        const int q = h * kWaves + ord;
+        if (q < i) {
+          uint64_t v[VEC];
 #pragma unroll
-  for (int i = 0; i < L::TPT; ++i) {
-    if (p.t0 + i >= A.T) continue;
-    float v[VEC];
+          for (int j = 0; j < VEC; ++j) v[j] = peek(bd.runs + (row0 + q) * A.C + p.c + j);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] = 0.f;
-    if (p.t0 + i < p.len) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v[j] = h[j] = step(k[i][j], xv[i][j], h[j]);
-      if (o) {
-        const auto orow = load_raw<T, VEC>(o + ((size_t)p.b * A.T + p.t0 + i) * A.ld + p.c);
+          for (int j = 0; j < VEC; ++j) {
+            while (v[j] == kUnset) {
+              __builtin_amdgcn_s_sleep(1);
+              v[j] = peek(bd.runs + (row0 + q) * A.C + p.c + j);
+            }
+            sh.prev[q][l0 + j] = make_float2(__uint_as_float((uint32_t)(v[j] >> 32)),
+                                             __uint_as_float((uint32_t)v[j]));
+          }
+        }
+      }
+      if (last) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          const float ov = to_f32(orow[j]);
-          v[j] *= ov * sigm(ov);
+          if (g == 0) {
+            sh.enter[l0 + j] = start ? start[(size_t)p.b * A.C + p.c + j] : 0.f;
+          } else {
+            const uint64_t* e = bd.enter + ((size_t)p.b * bd.ng + g) * A.C + p.c + j;
+            uint64_t v = peek(e);
+            while (v == kUnset) {
+              __builtin_amdgcn_s_sleep(1);
+              v = peek(e);
+            }
+            sh.enter[l0 + j] = __uint_as_float((uint32_t)v);
+          }
         }
       }
     }
-    store_raw<T, VEC>(y + ((size_t)p.b * A.T + p.t0 + i) * A.C + p.c, v);
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) chunk_in[j] = p.on ? sh.enter[l0 + j] : 0.f;
+    if (p.on) {
+      for (int q = 0; q < i; ++q) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float2 r = sh.prev[q][l0 + j];
+          chunk_in[j] = r.y + decay(r.x, chunk_in[j]);
+        }
+      }
+    }
+    if (last && p.on && i + 1 == kGroup && p.step + 1 < p.nc) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        post(bd.enter + ((size_t)p.b * bd.ng + g + 1) * A.C + p.c + j,
+             word(apply(total[j], chunk_in[j]), 0.f));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    mine[j] = apply(before[j], chunk_in[j]);
+    chunk_out[j] = apply(total[j], chunk_in[j]);
+  }
+}
+
+// ---------------------------------------------------------------- forward
+
+// The chunk's rows of a tensor as a buffer, and the offset of this thread's
+// first token in it.
+template <typename T>
+__device__ __forceinline__ BufRes chunk_buffer(const void* t, size_t row, int64_t ld, int rows,
+                                               int C) {
+  return make_rsrc(static_cast<const T*>(t) + row * ld,
+                   rows > 0 ? ((uint64_t)(rows - 1) * ld + C) * sizeof(T) : 0);
+}
+
+template <typename T, int VEC, bool CHAIN, bool GATED>
+__global__ __launch_bounds__(kTh) void gscan_kernel(GScanArgs A) {
+  __shared__ Shared sh;
+  const Place<VEC> p = take_place<VEC, false, CHAIN>(A, sh);
+  const int t1 = p.chunk * kChunk, rows = min(kChunk, A.T - t1);  // the chunk's rows
+  const size_t row = (size_t)p.b * A.T + t1;
+  const int w0 = p.t0 - t1;                                     // this thread's first row
+  const int live = min(max(p.len - p.t0, 0), kTpt);             // its tokens in use
+  const BufRes rx = chunk_buffer<T>(A.x, row, A.ld, rows, A.C);
+  const BufRes rf = chunk_buffer<T>(A.f, row, A.ld, rows, A.C);
+  const BufRes ro = chunk_buffer<T>(GATED ? A.o : A.x, row, A.ld, rows, A.C);
+  const BufRes ry = chunk_buffer<T>(A.y, row, A.C, rows, A.C);
+  const uint32_t pitch = (uint32_t)A.ld * sizeof(T), ypitch = A.C * (uint32_t)sizeof(T);
+  const uint32_t col = p.on ? p.c * (uint32_t)sizeof(T) : kOOB;
+  uint32_t xr[kTpt], fr[kTpt], gr[kTpt];
+#pragma unroll
+  for (int i = 0; i < kTpt; ++i) {
+    const uint32_t off = i < live ? col : kOOB, r = (w0 + i) * pitch;
+    fr[i] = load_bits<T, VEC>(rf, off, r);
+    xr[i] = load_bits<T, VEC>(rx, off, r);
+    gr[i] = 0;
+    if constexpr (GATED) gr[i] = load_bits<T, VEC>(ro, off, r);
+  }
+  float k[kTpt][VEC];
+  Run own[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) own[j] = identity();
+#pragma unroll
+  for (int i = 0; i < kTpt; ++i) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      // past the length: f = 1 (and x reads as 0)
+      k[i][j] = i < live ? gate_of(channel<T, VEC>(fr[i], j)) : 0.f;
+      extend(own[j], k[i][j]);
+      own[j].S = step(k[i][j], channel<T, VEC>(xr[i], j), own[j].S);
+    }
+  }
+  float h[VEC], cin[VEC], cout[VEC];
+  enter_states<VEC, false, CHAIN>(A, p, sh, own, A.h_init, h, cin, cout);
+  if (p.on && A.carry && threadIdx.x < 64) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) A.carry[p.cw * A.C + p.c + j] = cin[j];
+  }
+  if (p.on && A.h_final && p.step == p.nc - 1 && threadIdx.x >= kTh - 64) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) A.h_final[(size_t)p.b * A.C + p.c + j] = cout[j];
+  }
+#pragma unroll
+  for (int i = 0; i < kTpt; ++i) {
+    float v[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      h[j] = step(k[i][j], channel<T, VEC>(xr[i], j), h[j]);
+      v[j] = h[j];
+      if constexpr (GATED) {
+        const float ov = channel<T, VEC>(gr[i], j);
+        v[j] *= ov * sigm(ov);
+      }
+      v[j] = i < live ? v[j] : 0.f;
+    }
+    store_bits<T, VEC>(ry, w0 + i < rows ? col : kOOB, (w0 + i) * ypitch, v);
   }
 }
 
 // ---------------------------------------------------------------- backward
 
-// The gradient that reaches h_t from y_t, dy silu(gate), for one row.
-template <typename T, int VEC>
-__device__ __forceinline__ void dh_of(const T* dy, const T* o, float* u) {
-  const auto dr = load_raw<T, VEC>(dy);
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) u[j] = to_f32(dr[j]);
-  if (o) {
-    const auto orow = load_raw<T, VEC>(o);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float ov = to_f32(orow[j]);
-      u[j] *= ov * sigm(ov);
-    }
-  }
-}
-
 // Walking back, c = f_t e_t is the gradient that leaves token t for the state
-// before it: c <- f (u + c).
-template <typename T, int VEC>
-__global__ __launch_bounds__(kTh) void gscan_bwd_runs_kernel(GScanArgs A) {
-  typedef Lay<VEC> L;
-  __shared__ float sh[3][8][kCh];
-  const Place<VEC> p(A);
-  const T* f = static_cast<const T*>(A.f);
-  const T* o = static_cast<const T*>(A.o);
-  const T* dy = static_cast<const T*>(A.dy);
-  Run own[VEC], excl[VEC], total[VEC];
+// before it: c <- f (u + c), u = dy silu(gate). The states come from the
+// forward's carry and the runs of the chunk's waves.
+template <typename T, int VEC, bool CHAIN, bool GATED>
+__global__ __launch_bounds__(kTh) void gscan_bwd_kernel(GScanArgs A) {
+  __shared__ Shared sh;
+  const Place<VEC> p = take_place<VEC, true, CHAIN>(A, sh);
+  const int t1 = p.chunk * kChunk, rows = min(kChunk, A.T - t1);
+  const size_t row = (size_t)p.b * A.T + t1;
+  const int w0 = p.t0 - t1;
+  const int live = min(max(p.len - p.t0, 0), kTpt);
+  const BufRes rx = chunk_buffer<T>(A.x, row, A.ld, rows, A.C);
+  const BufRes rf = chunk_buffer<T>(A.f, row, A.ld, rows, A.C);
+  const BufRes ro = chunk_buffer<T>(GATED ? A.o : A.x, row, A.ld, rows, A.C);
+  const BufRes rd = chunk_buffer<T>(A.dy, row, A.C, rows, A.C);
+  const BufRes sx = chunk_buffer<T>(A.dx, row, A.ldd, rows, A.C);
+  const BufRes sf = chunk_buffer<T>(A.df, row, A.ldd, rows, A.C);
+  const BufRes so = chunk_buffer<T>(GATED ? A.d_o : A.dx, row, A.ldd, rows, A.C);
+  constexpr uint32_t ES = sizeof(T);
+  const uint32_t pitch = (uint32_t)A.ld * ES, dpitch = (uint32_t)A.ldd * ES;
+  const uint32_t col = p.on ? p.c * ES : kOOB;
+  uint32_t xr[kTpt], fr[kTpt], gr[kTpt], dr[kTpt];
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) own[j] = identity();
-#pragma unroll
-  for (int i = L::TPT - 1; i >= 0; --i) {
-    if (p.on && p.t0 + i < p.len) {
-      const size_t row = (size_t)p.b * A.T + p.t0 + i;
-      const auto fr = load_raw<T, VEC>(f + row * A.ld + p.c);
-      float u[VEC];
-      dh_of<T, VEC>(dy + row * A.C + p.c, o ? o + row * A.ld + p.c : nullptr, u);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float k = gate_of(to_f32(fr[j]));
-        const float g = neg(k) ? 1.f + k : k;
-        own[j].G = __builtin_fmaf(g, 1.f - own[j].G, own[j].G);
-        own[j].P *= forget_of(k);
-        own[j].S = decay(k, u[j] + own[j].S);
-      }
-    }
+  for (int i = 0; i < kTpt; ++i) {
+    const uint32_t off = i < live ? col : kOOB, r = (w0 + i) * pitch;
+    fr[i] = load_bits<T, VEC>(rf, off, r);
+    dr[i] = load_bits<T, VEC>(rd, off, (w0 + i) * A.C * ES);
+    gr[i] = 0;
+    if constexpr (GATED) gr[i] = load_bits<T, VEC>(ro, off, r);
+    xr[i] = load_bits<T, VEC>(rx, off, r);
   }
-  chunk_runs<VEC, true>(own, excl, total, sh);
-  if (p.on && threadIdx.x < L::LC) {
-    float* w = static_cast<float*>(A.ws) + p.cw * 3 * A.C + p.c;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      w[j] = total[j].G;
-      w[A.C + j] = total[j].P;
-      w[2 * (size_t)A.C + j] = total[j].S;
-    }
-  }
-}
-
-template <typename T, int VEC>
-__global__ __launch_bounds__(kTh) void gscan_bwd_out_kernel(GScanArgs A) {
-  typedef Lay<VEC> L;
-  __shared__ float sh[3][8][kCh];
-  const Place<VEC> p(A);
-  const T* x = static_cast<const T*>(A.x);
-  const T* f = static_cast<const T*>(A.f);
-  const T* o = static_cast<const T*>(A.o);
-  const T* dy = static_cast<const T*>(A.dy);
-  T* dx = static_cast<T*>(A.dx);
-  T* df = static_cast<T*>(A.df);
-  T* d_o = static_cast<T*>(A.d_o);
-  float k[L::TPT][VEC], xv[L::TPT][VEC], u[L::TPT][VEC];
-  Run fw[VEC], bw[VEC], fex[VEC], bex[VEC], total[VEC];
+  float k[kTpt][VEC], e[kTpt][VEC];
+  Run fw[VEC], bw[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; ++j) fw[j] = bw[j] = identity();
 #pragma unroll
-  for (int i = 0; i < L::TPT; ++i) {
+  for (int i = 0; i < kTpt; ++i) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) k[i][j] = xv[i][j] = u[i][j] = 0.f;
-    if (p.on && p.t0 + i < p.len) {
-      const size_t row = (size_t)p.b * A.T + p.t0 + i;
-      const auto xr = load_raw<T, VEC>(x + row * A.ld + p.c);
-      const auto fr = load_raw<T, VEC>(f + row * A.ld + p.c);
-      dh_of<T, VEC>(dy + row * A.C + p.c, o ? o + row * A.ld + p.c : nullptr, u[i]);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        k[i][j] = gate_of(to_f32(fr[j]));
-        xv[i][j] = to_f32(xr[j]);
-        const float g = neg(k[i][j]) ? 1.f + k[i][j] : k[i][j];
-        fw[j].G = __builtin_fmaf(g, 1.f - fw[j].G, fw[j].G);
-        fw[j].P *= forget_of(k[i][j]);
-        fw[j].S = step(k[i][j], xv[i][j], fw[j].S);
+    for (int j = 0; j < VEC; ++j) {
+      k[i][j] = i < live ? gate_of(channel<T, VEC>(fr[i], j)) : 0.f;
+      e[i][j] = channel<T, VEC>(dr[i], j);
+      if constexpr (GATED) {
+        const float ov = channel<T, VEC>(gr[i], j);
+        e[i][j] *= ov * sigm(ov);
       }
+      extend(fw[j], k[i][j]);
+      fw[j].S = step(k[i][j], channel<T, VEC>(xr[i], j), fw[j].S);
     }
   }
 #pragma unroll
@@ -409,62 +444,87 @@ __global__ __launch_bounds__(kTh) void gscan_bwd_out_kernel(GScanArgs A) {
     bw[j].P = fw[j].P;
   }
 #pragma unroll
-  for (int i = L::TPT - 1; i >= 0; --i)
+  for (int i = kTpt - 1; i >= 0; --i)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) bw[j].S = decay(k[i][j], u[i][j] + bw[j].S);
-  chunk_runs<VEC, false>(fw, fex, total, sh);
-  chunk_runs<VEC, true>(bw, bex, total, sh);
-  if (!p.on) return;
-  const float* w = static_cast<const float*>(A.ws) + p.cw * 3 * A.C + p.c;
-  float h[VEC], c[VEC];
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    h[j] = apply(fex[j], A.carry_in[p.cw * A.C + p.c + j]);
-    c[j] = apply(bex[j], w[2 * (size_t)A.C + j]);
+    for (int j = 0; j < VEC; ++j) bw[j].S = decay(k[i][j], e[i][j] + bw[j].S);
+  float h[VEC], c[VEC], cin[VEC], cout[VEC];
+  GScanArgs F = A;  // the forward's state entering the chunk, as a sequence of one chunk
+  {
+    Place<VEC> q = p;
+    q.b = 0;
+    q.on = p.on;
+    enter_states<VEC, false, false>(F, q, sh, fw, A.carry_in + p.cw * A.C, h, cin, cout);
+    __syncthreads();  // the runs in LDS are no longer read
   }
-  // e_t backwards: u becomes e
+  enter_states<VEC, true, CHAIN>(A, p, sh, bw, A.dh_final, c, cin, cout);
+  if (p.on && A.dh_init && p.step == p.nc - 1 && threadIdx.x < 64) {
 #pragma unroll
-  for (int i = L::TPT - 1; i >= 0; --i) {
-    if (p.t0 + i < p.len) {
+    for (int j = 0; j < VEC; ++j) A.dh_init[(size_t)p.b * A.C + p.c + j] = cout[j];
+  }
+  // e_t from the last token back
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        u[i][j] += c[j];
-        c[j] = decay(k[i][j], u[i][j]);
-      }
+  for (int i = kTpt - 1; i >= 0; --i) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      e[i][j] += c[j];
+      c[j] = decay(k[i][j], e[i][j]);
     }
   }
 #pragma unroll
-  for (int i = 0; i < L::TPT; ++i) {
-    if (p.t0 + i >= A.T) continue;
-    const size_t row = (size_t)p.b * A.T + p.t0 + i;
+  for (int i = 0; i < kTpt; ++i) {
     float vx[VEC], vf[VEC], vo[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) vx[j] = vf[j] = vo[j] = 0.f;
-    if (p.t0 + i < p.len) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float kk = k[i][j], a = fabsf(kk), e = u[i][j];
-        vx[j] = inject(kk, e);
-        vf[j] = __builtin_fmaf(-a, a, a) * e * (h[j] - xv[i][j]);
-        h[j] = step(kk, xv[i][j], h[j]);
-      }
-      if (o) {
-        const auto orow = load_raw<T, VEC>(o + row * A.ld + p.c);
-        const auto dr = load_raw<T, VEC>(dy + row * A.C + p.c);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float ov = to_f32(orow[j]), sg = sigm(ov);
-          vo[j] = to_f32(dr[j]) * h[j] * (sg * __builtin_fmaf(ov, 1.f - sg, 1.f));
-        }
+    for (int j = 0; j < VEC; ++j) {
+      const float kk = k[i][j], a = fabsf(kk), xv = channel<T, VEC>(xr[i], j);
+      vx[j] = i < live ? inject(kk, e[i][j]) : 0.f;
+      vf[j] = i < live ? __builtin_fmaf(-a, a, a) * e[i][j] * (h[j] - xv) : 0.f;
+      h[j] = step(kk, xv, h[j]);
+      vo[j] = 0.f;
+      if constexpr (GATED) {
+        const float ov = channel<T, VEC>(gr[i], j), sg = sigm(ov);
+        vo[j] = channel<T, VEC>(dr[i], j) * h[j] * (sg * __builtin_fmaf(ov, 1.f - sg, 1.f));
+        vo[j] = i < live ? vo[j] : 0.f;
       }
     }
-    store_raw<T, VEC>(dx + row * A.ldd + p.c, vx);
-    store_raw<T, VEC>(df + row * A.ldd + p.c, vf);
-    if (o) store_raw<T, VEC>(d_o + row * A.ldd + p.c, vo);
+    const uint32_t off = w0 + i < rows ? col : kOOB, r = (w0 + i) * dpitch;
+    store_bits<T, VEC>(sx, off, r, vx);
+    store_bits<T, VEC>(sf, off, r, vf);
+    if constexpr (GATED) store_bits<T, VEC>(so, off, r, vo);
   }
 }
 
+// The workspace before a chained kernel: nothing published.
+__global__ __launch_bounds__(256) void gscan_unset_kernel(uint4* ws, size_t n) {
+  for (size_t q = (size_t)blockIdx.x * 256 + threadIdx.x; q < n; q += (size_t)gridDim.x * 256)
+    ws[q] = make_uint4(~0u, ~0u, ~0u, ~0u);
+}
+
 // ---------------------------------------------------------------- one token
+
+template <typename T, int VEC> struct Raw {
+  typedef T t __attribute__((ext_vector_type(VEC)));
+};
+template <typename T> struct Raw<T, 1> {
+  struct t {
+    T v;
+    __device__ T operator[](int) const { return v; }
+  };
+};
+template <typename T, int VEC>
+__device__ __forceinline__ typename Raw<T, VEC>::t load_raw(const T* p) {
+  return *reinterpret_cast<const typename Raw<T, VEC>::t*>(p);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_raw(T* p, const float* v) {
+  if constexpr (VEC == 1) {
+    p[0] = from_f32<T>(v[0]);
+  } else {
+    typename Raw<T, VEC>::t r;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) r[j] = from_f32<T>(v[j]);
+    *reinterpret_cast<typename Raw<T, VEC>::t*>(p) = r;
+  }
+}
 
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void gscan_step_kernel(const T* __restrict__ x,
@@ -499,42 +559,40 @@ __global__ __launch_bounds__(256) void gscan_step_kernel(const T* __restrict__ x
 
 // ---------------------------------------------------------------- launch
 
-// 16-byte accesses need rows that start on 16 bytes and whole groups of channels.
-template <typename T>
-bool rows_aligned(int C, int64_t ld, int64_t ldd) {
-  constexpr int V = 16 / (int)sizeof(T);
-  return C % V == 0 && ld % V == 0 && ldd % V == 0;
+// bf16 rows are taken two channels (4 bytes) per lane where every row starts on
+// a pair and has whole pairs; fp32 rows one channel (also 4 bytes) per lane.
+bool in_pairs(int C, int64_t ld, int64_t ldd) { return C % 2 == 0 && ld % 2 == 0 && ldd % 2 == 0; }
+
+unsigned units(const GScanArgs& A, int vec) {
+  return (unsigned)((A.C + 64 * vec - 1) / (64 * vec)) * (unsigned)gscan_chunks(A.T) *
+         (unsigned)A.Bt;
 }
 
-template <typename T, int VEC>
-hipError_t fwd_t(const GScanArgs& A, hipStream_t s) {
-  const int nc = gscan_chunks(A.T);
-  const unsigned ncb = (unsigned)((A.C + kCh - 1) / kCh);
-  const dim3 grid(ncb * (unsigned)nc * (unsigned)A.Bt);
+// BWD: the backward's kernel.
+template <typename T, int VEC, bool BWD>
+hipError_t go(const GScanArgs& A, hipStream_t s) {
   hipEvent_t e0, e1;
-  prof_kernel("gated_scan_runs", &e0, &e1);
-  hipExtLaunchKernelGGL((gscan_runs_kernel<T, VEC>), grid, dim3(kTh), 0, s, e0, e1, 0, A);
-  prof_kernel("gated_scan_carry", &e0, &e1);
-  hipExtLaunchKernelGGL(gscan_carry_kernel<false>, dim3(ncb * (unsigned)A.Bt), dim3(64), 0, s,
-                        e0, e1, 0, (float*)A.ws, nc, A.C, A.h_init, A.h_final, A.carry);
-  prof_kernel("gated_scan", &e0, &e1);
-  hipExtLaunchKernelGGL((gscan_out_kernel<T, VEC>), grid, dim3(kTh), 0, s, e0, e1, 0, A);
-  return hipGetLastError();
-}
-
-template <typename T, int VEC>
-hipError_t bwd_t(const GScanArgs& A, hipStream_t s) {
-  const int nc = gscan_chunks(A.T);
-  const unsigned ncb = (unsigned)((A.C + kCh - 1) / kCh);
-  const dim3 grid(ncb * (unsigned)nc * (unsigned)A.Bt);
-  hipEvent_t e0, e1;
-  prof_kernel("gated_scan_bwd_runs", &e0, &e1);
-  hipExtLaunchKernelGGL((gscan_bwd_runs_kernel<T, VEC>), grid, dim3(kTh), 0, s, e0, e1, 0, A);
-  prof_kernel("gated_scan_bwd_carry", &e0, &e1);
-  hipExtLaunchKernelGGL(gscan_carry_kernel<true>, dim3(ncb * (unsigned)A.Bt), dim3(64), 0, s,
-                        e0, e1, 0, (float*)A.ws, nc, A.C, A.dh_final, A.dh_init, (float*)nullptr);
-  prof_kernel("gated_scan_bwd", &e0, &e1);
-  hipExtLaunchKernelGGL((gscan_bwd_out_kernel<T, VEC>), grid, dim3(kTh), 0, s, e0, e1, 0, A);
+  const bool chain = gscan_chunks(A.T) > 1;
+  if (chain) {
+    prof_kernel("gated_scan_unset", &e0, &e1);
+    const size_t n = gscan_ws_bytes(A.Bt, A.T, A.C) / 16;
+    const unsigned blocks = (unsigned)std::min<size_t>((n + 255) / 256, 2048);
+    hipExtLaunchKernelGGL(gscan_unset_kernel, dim3(blocks), dim3(256), 0, s, e0, e1, 0,
+                          (uint4*)A.ws, n);
+  }
+  prof_kernel(BWD ? "gated_scan_bwd" : "gated_scan", &e0, &e1);
+  const dim3 grid(units(A, VEC));
+  auto run = [&](auto chained, auto gated) {
+    constexpr bool CH = decltype(chained)::value, GA = decltype(gated)::value;
+    if constexpr (BWD)
+      hipExtLaunchKernelGGL((gscan_bwd_kernel<T, VEC, CH, GA>), grid, dim3(kTh), 0, s, e0, e1, 0, A);
+    else
+      hipExtLaunchKernelGGL((gscan_kernel<T, VEC, CH, GA>), grid, dim3(kTh), 0, s, e0, e1, 0, A);
+  };
+  const std::true_type yes{};
+  const std::false_type no{};
+  if (chain) A.o ? run(yes, yes) : run(yes, no);
+  else A.o ? run(no, yes) : run(no, no);
   return hipGetLastError();
 }
 
@@ -543,23 +601,23 @@ hipError_t bwd_t(const GScanArgs& A, hipStream_t s) {
 int gscan_chunks(int T) { return (T + kChunk - 1) / kChunk; }
 
 int64_t gscan_blocks(int64_t Bt, int64_t T, int64_t C) {
-  return Bt * ((T + kChunk - 1) / kChunk) * ((C + kCh - 1) / kCh);
+  return Bt * ((T + kChunk - 1) / kChunk) * ((C + 63) / 64);
 }
 
 size_t gscan_ws_bytes(int Bt, int T, int C) {
-  return sizeof(float) * 3 * (size_t)Bt * gscan_chunks(T) * C;
+  const size_t nc = gscan_chunks(T), ng = (nc + kGroup - 1) / kGroup;
+  if (nc <= 1) return 0;
+  return (counter_bytes(Bt, C) + sizeof(uint64_t) * (size_t)Bt * (nc + ng) * C + 15) / 16 * 16;
 }
 
 hipError_t launch_gscan(bool is_bf16, const GScanArgs& a, hipStream_t s) {
-  if (is_bf16)
-    return rows_aligned<bf16>(a.C, a.ld, 0) ? fwd_t<bf16, 8>(a, s) : fwd_t<bf16, 1>(a, s);
-  return rows_aligned<float>(a.C, a.ld, 0) ? fwd_t<float, 4>(a, s) : fwd_t<float, 1>(a, s);
+  if (!is_bf16) return go<float, 1, false>(a, s);
+  return in_pairs(a.C, a.ld, 0) ? go<bf16, 2, false>(a, s) : go<bf16, 1, false>(a, s);
 }
 
 hipError_t launch_gscan_backward(bool is_bf16, const GScanArgs& a, hipStream_t s) {
-  if (is_bf16)
-    return rows_aligned<bf16>(a.C, a.ld, a.ldd) ? bwd_t<bf16, 8>(a, s) : bwd_t<bf16, 1>(a, s);
-  return rows_aligned<float>(a.C, a.ld, a.ldd) ? bwd_t<float, 4>(a, s) : bwd_t<float, 1>(a, s);
+  if (!is_bf16) return go<float, 1, true>(a, s);
+  return in_pairs(a.C, a.ld, a.ldd) ? go<bf16, 2, true>(a, s) : go<bf16, 1, true>(a, s);
 }
 
 hipError_t launch_gscan_step(bool is_bf16, const void* x, const void* f, const void* o, int64_t ld,
@@ -575,10 +633,10 @@ hipError_t launch_gscan_step(bool is_bf16, const void* x, const void* f, const v
                           (const T*)x, (const T*)f, (const T*)o, ld, h_prev, h, (T*)y, Bt, C);
   };
   if (is_bf16) {
-    if (rows_aligned<bf16>(C, ld, 0)) go(bf16(), std::integral_constant<int, 4>());
+    if (C % 4 == 0 && ld % 4 == 0) go(bf16(), std::integral_constant<int, 4>());
     else go(bf16(), std::integral_constant<int, 1>());
   } else {
-    if (rows_aligned<float>(C, ld, 0)) go(0.f, std::integral_constant<int, 4>());
+    if (C % 4 == 0 && ld % 4 == 0) go(0.f, std::integral_constant<int, 4>());
     else go(0.f, std::integral_constant<int, 1>());
   }
   return hipGetLastError();

@@ -14,6 +14,7 @@ namespace {
 
 // A grid's threads are counted in 32 bits.
 constexpr int64_t kMaxThreads = int64_t(1) << 32;
+constexpr int64_t kMaxLd = int64_t(1) << 22;
 
 swimba_status read_layer_dims(const swimba_dims* dims, Dims& d) {
   const swimba_status st = read_dims(dims, d);
@@ -37,7 +38,9 @@ swimba_status check_gscan(const Dims& d, int64_t ld, int64_t ldd) {
   if (ld < d.HP || ldd < d.HP)
     return fail(SWIMBA_ERR_DIMS, "a row stride is smaller than nheads * headdim = %lld",
                 (long long)d.HP);
-  if (ld > INT32_MAX || ldd > INT32_MAX) return fail(SWIMBA_ERR_DIMS, "row stride too large");
+  // a chunk's 128 rows are addressed through one buffer
+  if (ld >= kMaxLd || ldd >= kMaxLd)
+    return fail(SWIMBA_ERR_DIMS, "row strides must be below 2^22 elements");
   if (gscan_blocks(d.Bt, d.T, d.HP) * 512 >= kMaxThreads || d.Bt * d.HP >= kMaxThreads - 256)
     return fail(SWIMBA_ERR_DIMS, "too many chunks of tokens and channels for one launch");
   return SWIMBA_OK;
@@ -237,8 +240,8 @@ swimba_status swimba_gated_step(const swimba_dims* dims, const void* x, const vo
   swimba_status st = read_layer_dims(dims, d);
   if (st != SWIMBA_OK) return st;
   if (d.T != 1) return fail(SWIMBA_ERR_DIMS, "gated_step takes one token: seqlen must be 1");
-  if (ld < d.HP || ld > INT32_MAX)
-    return fail(SWIMBA_ERR_DIMS, "the row stride must lie in [nheads * headdim, 2^31)");
+  if (ld < d.HP || ld >= kMaxLd)
+    return fail(SWIMBA_ERR_DIMS, "the row stride must lie in [nheads * headdim, 2^22)");
   if (d.Bt * d.HP >= kMaxThreads - 256) return fail(SWIMBA_ERR_DIMS, "too many channels for one launch");
   if (d.Bt == 0) return SWIMBA_OK;
   REQUIRE_PTR(x);

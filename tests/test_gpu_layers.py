@@ -275,7 +275,8 @@ def scan_bounds(g):
 
 
 SCAN_SHAPES = [(1, 1, 1), (2, 1, 64), (1, 2, 8), (3, 5, 24), (2, 255, 64), (1, 256, 72),
-               (2, 257, 40), (1, 700, 128), (2, 513, 65), (1, 1500, 33), (5, 31, 200)]
+               (2, 257, 40), (1, 700, 128), (2, 513, 65), (1, 1500, 33), (5, 31, 200), (2, 2048, 8),
+               (1, 2049, 10), (1, 4300, 5)]
 
 
 @pytest.mark.parametrize("Bt,T,C", SCAN_SHAPES)

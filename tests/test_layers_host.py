@@ -127,14 +127,16 @@ def test_norm_refusals():
 
 def test_scan_refusals():
     lib()
-    d = dims()
+    d = dims(seqlen=300)
     need = sl.layer_workspace_size(d, sl.LAYER_GATED_SCAN)
-    assert need > 0 and sl.lib().swimba_gated_scan_carry_size(ref(d)) == 2 * 1 * 192 * 4
+    assert need > 0 and sl.lib().swimba_gated_scan_carry_size(ref(d)) == 2 * 3 * 192 * 4
+    # a sequence of one chunk needs no workspace
+    assert sl.layer_workspace_size(dims(seqlen=128), sl.LAYER_GATED_SCAN) == 0
     for kw in ("x", "f", "y"):
         assert scan(d, **{kw: None}) == -1, kw
     for kw in ("x", "f", "o", "lens", "h0", "y", "h", "carry", "ws"):
         assert scan(d, **{kw: MISALIGNED}) == -5, kw
-    assert scan(d, ld=191) == -2 and scan(d, ld=-1) == -2 and scan(d, ld=1 << 31) == -2
+    assert scan(d, ld=191) == -2 and scan(d, ld=-1) == -2 and scan(d, ld=1 << 22) == -2
     assert scan(d, nb=need - 1) == -4 and scan(d, ws=None, nb=0) == -4
     assert scan(dims(batch=0), x=None, f=None, y=None) == 0
     assert scan(dims(batch=1 << 24, seqlen=1), ld=192) == -2  # more workgroups than a launch has
@@ -146,13 +148,13 @@ def test_scan_refusals():
         assert scan_b(d, **{kw: MISALIGNED}) == -5, kw
     assert scan_b(d, ld=100) == -2 and scan_b(d, ldd=100) == -2
     assert scan_b(d, nb=need - 1) == -4
-    assert step(d) == -2 and "seqlen must be 1" in err()
+    assert step(dims()) == -2 and "seqlen must be 1" in err()
     d1 = dims(seqlen=1)
     for kw in ("x", "f", "hp", "h", "y"):
         assert step(d1, **{kw: None}) == -1, kw
     for kw in ("x", "f", "o", "hp", "h", "y"):
         assert step(d1, **{kw: MISALIGNED}) == -5, kw
-    assert step(d1, ld=8) == -2 and step(d1, ld=1 << 31) == -2
+    assert step(d1, ld=8) == -2 and step(d1, ld=1 << 22) == -2
     assert step(dims(batch=0, seqlen=1), x=None) == 0
 
 
