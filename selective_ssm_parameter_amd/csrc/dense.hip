@@ -32,6 +32,7 @@ namespace swimba {
 
 namespace {
 
+// BM x BN tiles by WM x WN waves.
 template <int BM_, int BN_, int WM_, int WN_>
 struct Cfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
@@ -64,7 +65,7 @@ constexpr int kBK = 32;
 template <typename T, class C, Mode MODE, bool SPLIT>
 struct DLay {
   static constexpr int ES = sizeof(T), EPC = 16 / ES;
-  static constexpr int NS = SPLIT ? 3 : 4;  // LDS stages, NS - 1 steps in flight
+  static constexpr int NS = SPLIT ? 3 : 4;
   static constexpr bool ACOL = MODE == kTN, BCOL = !is_gated(MODE);
   // tile in LDS: rows of CPR 16-byte chunks
   static constexpr int AROWS = ACOL ? kBK : C::BM, ACPR = (ACOL ? C::BM : kBK) / EPC;
@@ -76,16 +77,34 @@ struct DLay {
   static_assert(AB % (1024 * C::NW) == 0 && BB % (1024 * C::NW) == 0, "whole copies per wave");
 };
 
-// sigmoid(g), and Phi(g) from erfc, which keeps its relative precision for
-// negative g (1 + erf would cancel)
 __device__ __forceinline__ float sigm(float g) {
   return __builtin_amdgcn_rcpf(1.f + __expf(-g));
 }
-__device__ __forceinline__ float normal_cdf(float g) {
-  return 0.5f * erfcf(g * -0.70710678118654752f);
+// e = exp(-g^2 / 2) and Phi(g), from the upper tail Q(|g|) = e erfcx(|g| / sqrt 2) / 2,
+// so that it keeps its relative precision for negative g. erfcx (e^(x^2) erfc x)
+// is a polynomial of degree 9 in t = 1 / (1 + 0.3 x) without constant term,
+// fitted for this file by reweighted least squares on 0 <= x <= 10: relative
+// error 2e-8, 4.4e-7 evaluated in fp32. (The library's erfcf took 30 us more
+// of a 16384 x 2048 projection of 768.)
+__device__ __forceinline__ float normal_cdf(float g, float& e) {
+  const float a = fabsf(g);
+  e = __builtin_amdgcn_exp2f(-0.72134752044f * g * g);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.21213203436f, a, 1.f));
+  float c = -0.12952312601577864f;
+  c = __builtin_fmaf(c, t, 0.4855643722941682f);
+  c = __builtin_fmaf(c, t, -0.5122806874687891f);
+  c = __builtin_fmaf(c, t, 0.5477232538943848f);
+  c = __builtin_fmaf(c, t, -0.09465315028525317f);
+  c = __builtin_fmaf(c, t, 0.21492718641342054f);
+  c = __builtin_fmaf(c, t, 0.14833885369157157f);
+  c = __builtin_fmaf(c, t, 0.17071527585634538f);
+  c = __builtin_fmaf(c, t, 0.16918800203758264f);
+  const float tail = 0.5f * c * t * e;
+  return g > 0.f ? 1.f - tail : tail;
 }
 __device__ __forceinline__ float act_of(int act, float g) {
-  return g * (act == SWIMBA_ACT_SILU ? sigm(g) : normal_cdf(g));
+  float e;
+  return g * (act == SWIMBA_ACT_SILU ? sigm(g) : normal_cdf(g, e));
 }
 // act(g) and act'(g)
 __device__ __forceinline__ void act_grad(int act, float g, float& v, float& d) {
@@ -94,9 +113,10 @@ __device__ __forceinline__ void act_grad(int act, float g, float& v, float& d) {
     v = g * s;
     d = s * (1.f + g * (1.f - s));
   } else {
-    const float phi = normal_cdf(g);
+    float e;
+    const float phi = normal_cdf(g, e);
     v = g * phi;
-    d = phi + g * 0.39894228040143268f * __expf(-0.5f * g * g);
+    d = __builtin_fmaf(g * 0.39894228040143268f, e, phi);
   }
 }
 
@@ -392,6 +412,110 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   }
 }
 
+// The gated projection of at most 64 tokens (decode batches), bound by
+// streaming w_in from HBM once: a workgroup owns 16 columns of h, its waves
+// split k, and the weights go straight into registers as matrix-core operands,
+// in bursts of kBurst k steps of 16 rows of g and of u (each row's part of a
+// burst is one run of 512 bytes), the next burst requested before the products
+// of this one. The tokens' rows, read by every workgroup, come from L2. The
+// waves' partial products are added in LDS in wave order.
+// MT: tiles of 16 tokens; KW: waves per workgroup (more where few columns would
+// leave CUs without a workgroup).
+template <typename T, int MT, int KW>
+__global__ __launch_bounds__(64 * KW) void gated_skinny_kernel(DenseArgs A) {
+  typedef typename Vec<T>::x8 F;
+  constexpr int kBurst = 16 / (int)sizeof(T);
+  constexpr uint32_t ES = sizeof(T);
+  __shared__ floatx4 part[KW][2][MT][64];
+  const int lane = lane_id(), g = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int s0 = blockIdx.x * 16;
+  const int nsteps = (A.K + 31) / 32, per = (nsteps + KW - 1) / KW;
+  const int k0 = wave * per * 32, k1 = min(A.K, k0 + per * 32);  // this wave's k
+  const BufRes rW = make_rsrc(A.b, (uint64_t)2 * A.S * A.K * ES);
+  const BufRes rX = make_rsrc(A.a, (uint64_t)A.R * A.K * ES);
+  const uint32_t wg = s0 + c < A.S ? (uint32_t)(s0 + c) * A.K * ES : kOOB;
+  const uint32_t wu = s0 + c < A.S ? (uint32_t)(A.S + s0 + c) * A.K * ES : kOOB;
+  uint32_t xo[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+    xo[i] = 16 * i + c < A.R ? (uint32_t)(16 * i + c) * A.K * ES : kOOB;
+  struct Burst {
+    F w[2][kBurst], x[MT][kBurst];
+  };
+  auto load = [&](Burst& b, int k) {
+#pragma unroll
+    for (int q = 0; q < kBurst; ++q) {
+      const int kk = k + 32 * q + 8 * g;
+      const bool ok = kk < k1;
+      b.w[0][q] = load8_buf<T>(rW, ok && wg != kOOB ? wg + kk * ES : kOOB);
+      b.w[1][q] = load8_buf<T>(rW, ok && wu != kOOB ? wu + kk * ES : kOOB);
+    }
+#pragma unroll
+    for (int q = 0; q < kBurst; ++q) {
+      const int kk = k + 32 * q + 8 * g;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        b.x[i][q] = load8_buf<T>(rX, kk < k1 && xo[i] != kOOB ? xo[i] + kk * ES : kOOB);
+    }
+  };
+  floatx4 acc[2][MT];
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[q][i] = floatx4{0.f, 0.f, 0.f, 0.f};
+  auto mul = [&](const Burst& b) {
+#pragma unroll
+    for (int q = 0; q < kBurst; ++q)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        acc[0][i] = mma16(b.w[0][q], b.x[i][q], acc[0][i]);
+        acc[1][i] = mma16(b.w[1][q], b.x[i][q], acc[1][i]);
+      }
+  };
+  constexpr int KB = 32 * kBurst;
+  Burst b0, b1;
+  load(b0, k0);
+  for (int k = k0; k < k1; k += 2 * KB) {
+    load(b1, k + KB);  // (bursts past k1 read zeros)
+    __builtin_amdgcn_sched_barrier(0);
+    mul(b0);
+    load(b0, k + 2 * KB);
+    __builtin_amdgcn_sched_barrier(0);
+    mul(b1);
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) part[wave][q][i][lane] = acc[q][i];
+  __syncthreads();
+  // lane (g, c) of tile i: columns s0 + 4 g .. + 3 of token 16 i + c
+  for (int i = wave; i < MT; i += KW) {
+    const int m = 16 * i + c, col = s0 + 4 * g;
+    if (m >= A.R || col >= A.S) continue;
+    floatx4 v = part[0][0][i][lane], u = part[0][1][i][lane];
+#pragma unroll
+    for (int w = 1; w < KW; ++w) {
+      v = v + part[w][0][i][lane];
+      u = u + part[w][1][i][lane];
+    }
+    typename Vec<T>::x4 og, ou, oh;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      og[q] = from_f32<T>(v[q]);
+      ou[q] = from_f32<T>(u[q]);
+      oh[q] = from_f32<T>(act_of(A.act, v[q]) * u[q]);
+    }
+    typedef typename Vec<T>::x4 V4;
+    *reinterpret_cast<V4*>(static_cast<T*>(A.out) + (size_t)m * A.S + col) = oh;
+    if (A.z) {
+      T* z = static_cast<T*>(A.z) + (size_t)m * 2 * A.S + col;
+      *reinterpret_cast<V4*>(z) = og;
+      *reinterpret_cast<V4*>(z + A.S) = ou;
+    }
+  }
+}
+
 // out = the splits' partial products added in split order.
 __global__ __launch_bounds__(256) void dense_sum_kernel(const float* __restrict__ part, int splits,
                                                         size_t n4, float* __restrict__ out) {
@@ -414,34 +538,85 @@ hipError_t go(const char* name, const DenseArgs& A, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The tile (256, 128 or 64 rows) for an R x S product: the largest that still
-// gives most of the 256 CUs a workgroup. fp32 stages of 256 rows do not fit LDS.
-int tile_of(bool is_bf16, int64_t R, int64_t S, int64_t copies = 1) {
-  auto units = [&](int64_t t) { return (R + t - 1) / t * ((S + t - 1) / t) * copies; };
-  if (is_bf16 && units(256) >= 192) return 256;
-  return units(128) >= 192 ? 128 : 64;
+// Tile and number of k runs of a product, by an estimate of its time in us from
+// what the tiles measured: workgroups the chip holds at once, time per k step of
+// those that share a CU, and the rest of a tile (first copies, epilogue, stores).
+// bf16 at 256 rows 0.90 us a step and 12 us a tile (32768 x 8192 x 2048: 16
+// rounds, 1081 us); 128 rows, two tiles per CU, 1439 us for the same product;
+// 64 rows are for products that would leave most CUs without a tile. fp32
+// stages of 256 rows do not fit LDS.
+struct TileCost {
+  int tile, slots;
+  double step, rest;
+};
+constexpr TileCost kBf16Tiles[] = {{256, 256, 0.90, 12}, {128, 512, 0.62, 8}, {64, 1024, 0.40, 5}};
+constexpr TileCost kF32Tiles[] = {{128, 256, 1.8, 8}, {64, 512, 1.0, 5}};
+
+struct Plan {
+  int tile, splits;
+};
+// cols: columns of the product per column of a tile's width (the gated tile of
+// 64 rows is 128 wide). most: the largest number of k runs; their partial sums
+// are written, read and summed at about 4 TB/s.
+Plan plan(bool is_bf16, bool split, bool gated, int64_t R, int64_t S, int64_t K, int64_t most) {
+  Plan best{64, 1};
+  double tbest = 1e30;
+  const TileCost* c = is_bf16 ? kBf16Tiles : kF32Tiles;
+  const int nt = is_bf16 ? 3 : 2;
+  const double steps = (double)((K + kBK - 1) / kBK) * (split ? 1.9 : 1.0);
+  for (int i = 0; i < nt; ++i) {
+    const int64_t tr = c[i].tile, ts = gated && tr == 64 ? 128 : tr;
+    const int64_t units = (R + tr - 1) / tr * ((S + ts - 1) / ts);
+    for (int64_t n = 1; n <= most; ++n) {
+      const int64_t slots = ts != tr ? c[i].slots * 3 / 4 : c[i].slots;
+      const double rounds = (double)((units * n + slots - 1) / slots);
+      double t = rounds * (steps / n * c[i].step + c[i].rest);
+      if (n > 1) t += 4 + (double)(n + 1) * R * S * 4e-6 / 4;
+      if (t < tbest) {
+        tbest = t;
+        best = Plan{(int)tr, (int)n};
+      }
+      if (units * n > 4 * c[i].slots) break;  // more runs only add partial sums
+    }
+  }
+  return best;
 }
 
-// The k runs of a weight gradient: at least 512 tokens each, as many as bring
-// the product near 256 workgroups; and every run's operand rows below 2 GiB.
-void tn_plan(bool is_bf16, int M, int R, int S, int& tile, int& splits, int& ksplit) {
-  const int64_t most = std::max<int64_t>(1, M / 512);
-  tile = tile_of(is_bf16, R, S, std::min<int64_t>(most, 16));
-  const int64_t units = (int64_t)((R + tile - 1) / tile) * ((S + tile - 1) / tile);
-  int64_t n = std::min(most, (256 + units - 1) / units);
+// The k runs of a weight gradient: at least 256 tokens each, 64 at most, and
+// every run's operand rows below 2 GiB.
+void tn_plan(bool is_bf16, bool split, int M, int R, int S, int& tile, int& splits, int& ksplit) {
+  const Plan p = plan(is_bf16, split, false, R, S, M,
+                      std::max<int64_t>(1, std::min<int64_t>(64, M / 256)));
+  tile = p.tile;
   const int64_t row = (int64_t)(R > S ? R : S) * (is_bf16 ? 2 : 4);
-  n = std::max<int64_t>(n, (M * row + (int64_t(1) << 30) - 1) >> 30);
+  const int64_t n = std::max<int64_t>(p.splits, (M * row + (int64_t(1) << 30) - 1) >> 30);
   ksplit = (int)(((M + n - 1) / n + kBK - 1) / kBK * kBK);
   splits = (M + ksplit - 1) / ksplit;
 }
 
 template <typename T, Mode MODE>
 hipError_t go_gated(const char* name, const DenseArgs& A, hipStream_t s) {
-  const int tile = tile_of(sizeof(T) == 2, A.R, 2 * (int64_t)A.S);
+  const int tile = plan(sizeof(T) == 2, false, true, A.R, 2 * (int64_t)A.S, A.K, 1).tile;
   if constexpr (sizeof(T) == 2)
     if (tile == 256) return go<T, Big, MODE, T>(name, A, s);
   if (tile == 128) return go<T, Mid, MODE, T>(name, A, s);
   return go<T, Small, MODE, T>(name, A, s);
+}
+
+constexpr int kSkinnyTokens = 64;
+
+template <typename T, int MT>
+hipError_t go_skinny(const DenseArgs& A, hipStream_t s) {
+  const int units = (A.S + 15) / 16;
+  hipEvent_t e0, e1;
+  prof_kernel("gated_project", &e0, &e1);
+  if (units >= 192 || MT == 4)
+    hipExtLaunchKernelGGL((gated_skinny_kernel<T, MT, 4>), dim3((unsigned)units), dim3(256), 0, s,
+                          e0, e1, 0, A);
+  else
+    hipExtLaunchKernelGGL((gated_skinny_kernel<T, MT, 8>), dim3((unsigned)units), dim3(512), 0, s,
+                          e0, e1, 0, A);
+  return hipGetLastError();
 }
 
 template <typename T, Mode MODE, typename TO, bool SPLIT>
@@ -458,6 +633,9 @@ hipError_t launch_gated_project(bool is_bf16, int M, int D, int F, int act, cons
                                 const void* w_in, void* z, void* h, hipStream_t s) {
   DenseArgs A{};
   A.a = x; A.b = w_in; A.out = h; A.z = z; A.R = M; A.S = F; A.K = D; A.act = act;
+  if (M <= 16) return is_bf16 ? go_skinny<bf16, 1>(A, s) : go_skinny<float, 1>(A, s);
+  if (M <= 32) return is_bf16 ? go_skinny<bf16, 2>(A, s) : go_skinny<float, 2>(A, s);
+  if (M <= kSkinnyTokens) return is_bf16 ? go_skinny<bf16, 4>(A, s) : go_skinny<float, 4>(A, s);
   return is_bf16 ? go_gated<bf16, kGated>("gated_project", A, s)
                  : go_gated<float, kGated>("gated_project", A, s);
 }
@@ -478,15 +656,15 @@ hipError_t launch_dense_nn(bool is_bf16, const char* name, int M, int K, int S, 
                            const void* a_lo, const void* b, void* out, hipStream_t s) {
   DenseArgs A{};
   A.a = a; A.a_lo = a_lo; A.b = b; A.out = out; A.R = M; A.S = S; A.K = K;
-  const int tile = tile_of(is_bf16, M, S);
+  const int tile = plan(is_bf16, a_lo != nullptr, false, M, S, K, 1).tile;
   if (!is_bf16) return go_tile<float, kNN, float, false>(tile, name, A, s);
   return a_lo ? go_tile<bf16, kNN, float, true>(tile, name, A, s)
               : go_tile<bf16, kNN, bf16, false>(tile, name, A, s);
 }
 
-size_t dense_tn_ws_bytes(bool is_bf16, int M, int R, int S) {
+size_t dense_tn_ws_bytes(bool is_bf16, bool split, int M, int R, int S) {
   int tile, splits, ksplit;
-  tn_plan(is_bf16, M, R, S, tile, splits, ksplit);
+  tn_plan(is_bf16, split, M, R, S, tile, splits, ksplit);
   return splits > 1 ? sizeof(float) * (size_t)splits * R * S : 0;
 }
 
@@ -495,7 +673,7 @@ hipError_t launch_dense_tn(bool is_bf16, const char* name, int M, int R, int S, 
   DenseArgs A{};
   A.a = a; A.a_lo = a_lo; A.b = b; A.R = R; A.S = S; A.K = M;
   int tile;
-  tn_plan(is_bf16, M, R, S, tile, A.splits, A.ksplit);
+  tn_plan(is_bf16, a_lo != nullptr, M, R, S, tile, A.splits, A.ksplit);
   A.out = A.splits > 1 ? ws : (void*)out;
   hipError_t e;
   if (!is_bf16) e = go_tile<float, kTN, float, false>(tile, name, A, s);

@@ -71,8 +71,8 @@ hipError_t launch_gated_dz(bool is_bf16, int M, int D, int F, int act, const voi
 hipError_t launch_dense_nn(bool is_bf16, const char* name, int M, int K, int S, const void* a,
                            const void* a_lo, const void* b, void* out, hipStream_t s);
 // out [R, S] (float32) = (a + a_lo)^T b over M rows: a, a_lo [M, R] (a_lo may
-// be null), b [M, S].
-size_t dense_tn_ws_bytes(bool is_bf16, int M, int R, int S);
+// be null; split: it is given), b [M, S].
+size_t dense_tn_ws_bytes(bool is_bf16, bool split, int M, int R, int S);
 hipError_t launch_dense_tn(bool is_bf16, const char* name, int M, int R, int S, const void* a,
                            const void* a_lo, const void* b, float* out, void* ws, hipStream_t s);
 

@@ -80,9 +80,9 @@ size_t layer_ws(const Dims& d, int32_t call) {
       return gscan_ws_bytes((int)d.Bt, (int)d.T, (int)d.HP);
     case SWIMBA_LAYER_GATED_PROJECT_BACKWARD:
       return gated_bwd_dz_bytes(d) +
-             dense_tn_ws_bytes(d.bf16, (int)d.M, (int)(2 * d.HP), (int)d.D);
+             dense_tn_ws_bytes(d.bf16, d.bf16, (int)d.M, (int)(2 * d.HP), (int)d.D);
     case SWIMBA_LAYER_OUTPUT_PROJECT_BACKWARD:
-      return dense_tn_ws_bytes(d.bf16, (int)d.M, (int)d.D, (int)d.HP);
+      return dense_tn_ws_bytes(d.bf16, false, (int)d.M, (int)d.D, (int)d.HP);
     default: return 0;
   }
 }
