@@ -4,8 +4,8 @@
 //   e_t = dy silu(gate) + f_{t+1} e_{t+1},  dx = g e,  dforget = f g e (h_{t-1} - x),
 //   dgate = dy h silu'(gate).
 // A run of tokens maps the state that enters it to P h + S, with P the product
-// of its f, and runs are composed: thread (16 tokens of 2 channels, walked in
-// registers), wave (128 channels), workgroup (8 waves, a chunk of 128 tokens),
+// of its f, and runs are composed: thread (16 tokens of a channel, walked in
+// registers), wave (64 channels), workgroup (8 waves, a chunk of 128 tokens),
 // sequence. Bound by HBM: each tensor is read once, by one kernel. A chunk's
 // workgroup publishes its run, then waits for what precedes it: the runs of the
 // earlier chunks of its group of 16, and the state that enters the group, which
@@ -17,7 +17,7 @@
 // channels (its chain); its chunk is the next number of the chain's counter, so
 // that it only ever waits for workgroups that took an earlier number of the
 // same chain and hence already run: every wait ends. (One counter for all
-// workgroups cost about 115 ns each: 65536 tokens x 2048 channels took 957 us.)
+// workgroups was no slower, but would need all of them in one order.)
 //
 // The steps keep their relative precision where f is near 1 (a memory of many
 // tokens) and near 0 (a reset): with small = min(f, g) = t / (1 + t), t =
@@ -43,31 +43,24 @@ constexpr int kChunk = kTpt * kWaves;  // tokens per workgroup
 constexpr int kGroup = 16;          // chunks per group
 constexpr uint64_t kUnset = ~0ull;
 
-// One access of VEC channels (2 or 4 bytes) at byte offset off of a row that
-// starts `row` bytes into a buffer: with off = kOOB a load reads zeros and a
-// store is dropped.
-template <typename T, int VEC>
+// One channel of a row that starts `row` bytes into a buffer, at byte offset
+// off: with off = kOOB a load reads zeros and a store is dropped.
+template <typename T>
 __device__ __forceinline__ uint32_t load_bits(BufRes r, uint32_t off, uint32_t row) {
-  if constexpr (sizeof(T) * VEC == 4) return __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0);
+  if constexpr (sizeof(T) == 4) return __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0);
   else return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, row, 0);
 }
-template <typename T, int VEC>
-__device__ __forceinline__ float channel(uint32_t bits, int j) {
-  if constexpr (sizeof(T) == 4) return __uint_as_float(bits);
-  else return __uint_as_float(j == 0 ? bits << 16 : bits & 0xFFFF0000u);
+template <typename T>
+__device__ __forceinline__ float value(uint32_t bits) {
+  return __uint_as_float(sizeof(T) == 4 ? bits : bits << 16);
 }
-template <typename T, int VEC>
-__device__ __forceinline__ void store_bits(BufRes r, uint32_t off, uint32_t row, const float* v) {
-  if constexpr (sizeof(T) == 4) {
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), r, off, row, 0);
-  } else if constexpr (VEC == 2) {
-    typedef T T2 __attribute__((ext_vector_type(2)));
-    const T2 t = {from_f32<T>(v[0]), from_f32<T>(v[1])};
-    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, t), r, off, row, 0);
-  } else {
-    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, from_f32<T>(v[0])), r, off, row,
+template <typename T>
+__device__ __forceinline__ void store_one(BufRes r, uint32_t off, uint32_t row, float v) {
+  if constexpr (sizeof(T) == 4)
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, off, row, 0);
+  else
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, from_f32<T>(v)), r, off, row,
                                           0);
-  }
 }
 
 // small = min(f, 1 - f) with the sign of the logit: + where g = 1 - f is small.
@@ -112,47 +105,44 @@ __device__ __forceinline__ void extend(Run& r, float k) {
   r.P = decay(k, r.P);
 }
 
-__device__ __forceinline__ int seq_len(const int32_t* lens, int b, int T) {
-  if (!lens) return T;
-  const int n = lens[b];
-  return n < 0 ? 0 : (n > T ? T : n);
-}
-
 // ---------------------------------------------------------------- chunks
 
 struct Shared {
-  float run[3][kWaves][128];           // each wave's run
-  float2 prev[kGroup][128];            // the earlier runs of the group: factor, S
-  float enter[128];                    // the state that enters the group
+  float run[3][kWaves][64];    // each wave's run
+  float2 prev[kGroup][64];     // the earlier runs of the group: factor, S
+  float enter[64];             // the state that enters the group
   uint32_t ticket;
 };
 
-// A workgroup's chain (sequence and block of channels) and chunk, and the tokens
-// of this thread. REV: the chain runs from the last chunk.
-template <int VEC>
+// A workgroup's chain (sequence and block of 64 channels) and chunk, and the
+// tokens of this thread. The chain is the chunks up to the sequence's length
+// (one at least), REV: from the last of them; the chunks past it take the
+// numbers after the chain's and only write zeros. All but c and on are uniform
+// in a wave, and said to be: buffers are built from them.
 struct Place {
-  int b, chunk, c, t0, len;  // c: first channel; t0: first token within the sequence
-  int step, nc, wave;        // position along the direction of the scan
+  int b, chunk, c, t0, len;  // c: channel; t0: first token within the sequence
+  int step, nc, wave;        // position along the scan, chunks of the chain
   size_t cw;                 // row of the chunk among all sequences' chunks
-  bool on;
-  template <bool REV>
-  static __device__ Place make(const GScanArgs& A, unsigned chain, int step) {
-    Place p;
-    const unsigned ncb = (A.C + 64 * VEC - 1) / (64 * VEC);
-    p.nc = (A.T + kChunk - 1) / kChunk;
-    // uniform, and said to be: buffers are built from them
-    p.b = __builtin_amdgcn_readfirstlane(chain / ncb);
-    p.step = step;
-    p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    p.chunk = REV ? p.nc - 1 - p.step : p.step;
-    p.cw = (size_t)p.b * p.nc + p.chunk;
-    p.c = (chain - p.b * ncb) * 64 * VEC + (threadIdx.x & 63) * VEC;
-    p.t0 = p.chunk * kChunk + p.wave * kTpt;
-    p.len = __builtin_amdgcn_readfirstlane(seq_len(A.lens, p.b, A.T));
-    p.on = p.c < A.C;
-    return p;
-  }
+  bool on, dead;             // dead: a chunk past the chain
 };
+template <bool REV>
+__device__ __forceinline__ Place place_of(const GScanArgs& A, unsigned chain, int step) {
+  Place p;
+  const unsigned ncb = (A.C + 63) / 64;
+  p.b = __builtin_amdgcn_readfirstlane(chain / ncb);
+  p.len = A.T;
+  if (A.lens) p.len = __builtin_amdgcn_readfirstlane(min(max(A.lens[p.b], 0), A.T));
+  p.nc = max(1, (p.len + kChunk - 1) / kChunk);
+  p.step = step;
+  p.dead = step >= p.nc;
+  p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  p.chunk = REV && !p.dead ? p.nc - 1 - p.step : p.step;
+  p.cw = (size_t)p.b * ((A.T + kChunk - 1) / kChunk) + p.chunk;
+  p.c = (chain - p.b * ncb) * 64 + (threadIdx.x & 63);
+  p.t0 = p.chunk * kChunk + p.wave * kTpt;
+  p.on = p.c < A.C;
+  return p;
+}
 
 __device__ __forceinline__ uint64_t word(float lo, float hi) {
   return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo);
@@ -166,156 +156,118 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* p) {
 __device__ __forceinline__ void post(uint64_t* p, uint64_t v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+__device__ __forceinline__ uint64_t wait_for(const uint64_t* p) {
+  uint64_t v = peek(p);
+  while (v == kUnset) {
+    __builtin_amdgcn_s_sleep(1);
+    v = peek(p);
+  }
+  return v;
+}
 
 // The workspace: a counter per chain, 128 bytes apart; a word per chunk and
 // channel (the chunk's run: S, factor); a word per group and channel (the state
 // entering it). All of it starts as all ones.
 constexpr size_t kCounterStep = 128;
 size_t __host__ __device__ inline counter_bytes(int Bt, int C) {
-  return kCounterStep * (size_t)Bt * ((C + 63) / 64);  // the most chains there are
+  return kCounterStep * (size_t)Bt * ((C + 63) / 64);
 }
 struct Board {
   uint64_t *runs, *enter;
-  int ng;  // groups per sequence
-  __device__ Board(const GScanArgs& A, int nc) {
+  int nc, ng;  // chunks and groups per sequence
+  __device__ explicit Board(const GScanArgs& A) {
+    nc = (A.T + kChunk - 1) / kChunk;
+    ng = (nc + kGroup - 1) / kGroup;
     runs = reinterpret_cast<uint64_t*>(static_cast<char*>(A.ws) + counter_bytes(A.Bt, A.C));
     enter = runs + (size_t)A.Bt * nc * A.C;
-    ng = (nc + kGroup - 1) / kGroup;
   }
 };
 
 // The workgroup's place: its chain from its index, its chunk from the chain's
 // counter.
-template <int VEC, bool REV, bool CHAIN>
-__device__ __forceinline__ Place<VEC> take_place(const GScanArgs& A, Shared& sh) {
+template <bool REV, bool CHAIN>
+__device__ __forceinline__ Place take_place(const GScanArgs& A, Shared& sh) {
   if constexpr (CHAIN) {
-    const unsigned chains = (unsigned)A.Bt * ((A.C + 64 * VEC - 1) / (64 * VEC));
+    const unsigned chains = (unsigned)A.Bt * ((A.C + 63) / 64);
     const unsigned chain = blockIdx.x % chains;
     if (threadIdx.x == 0)
       sh.ticket = atomicAdd(reinterpret_cast<uint32_t*>(static_cast<char*>(A.ws) +
                                                         kCounterStep * chain), 1u) + 1u;
     __syncthreads();
-    return Place<VEC>::template make<REV>(A, chain, __builtin_amdgcn_readfirstlane(sh.ticket));
+    return place_of<REV>(A, chain, __builtin_amdgcn_readfirstlane(sh.ticket));
   } else {
-    return Place<VEC>::template make<REV>(A, blockIdx.x, 0);
+    return place_of<REV>(A, blockIdx.x, 0);
   }
 }
 
-// From each thread's run (own) to the state that enters its tokens. start: the
-// state that enters the first chunk. Also returns the state that enters the
-// chunk and, in the wave at the end of the chunk, the state that leaves it.
-// CHAIN: the sequence has more than one chunk.
-template <int VEC, bool REV, bool CHAIN>
-__device__ __forceinline__ void enter_states(const GScanArgs& A, const Place<VEC>& p, Shared& sh,
-                                             const Run (&own)[VEC], const float* start,
-                                             float (&mine)[VEC], float (&chunk_in)[VEC],
-                                             float (&chunk_out)[VEC]) {
-  const int lane = threadIdx.x & 63;
-  const int ord = REV ? kWaves - 1 - p.wave : p.wave;  // position along the scan
-  const int l0 = lane * VEC;
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    sh.run[0][ord][l0 + j] = own[j].G;
-    sh.run[1][ord][l0 + j] = own[j].P;
-    sh.run[2][ord][l0 + j] = own[j].S;
-  }
-  __syncthreads();
-  Run before[VEC];
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) before[j] = identity();
-  for (int w = 0; w < ord; ++w) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j)
-      before[j] = join(before[j], Run{sh.run[0][w][l0 + j], sh.run[1][w][l0 + j],
-                                      sh.run[2][w][l0 + j]});
-  }
-  const bool last = ord == kWaves - 1;
-  Run total[VEC];
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) total[j] = join(before[j], own[j]);  // used by the last wave
+// The state that enters this thread's tokens, the one that enters the chunk,
+// and in the wave at the end of the chunk the one that leaves it.
+struct States {
+  float mine, in, out;
+};
 
-  if constexpr (!CHAIN) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j)
-      chunk_in[j] = start && p.on ? start[(size_t)p.b * A.C + p.c + j] : 0.f;
-  } else {
-    const Board bd(A, p.nc);
+// What the waves before this one (in the order of the scan) do to the chunk's
+// state. Every thread of the workgroup calls it.
+template <bool REV>
+__device__ __forceinline__ Run waves_before(const Place& p, Shared& sh, const Run& own) {
+  const int lane = threadIdx.x & 63, ord = REV ? kWaves - 1 - p.wave : p.wave;
+  sh.run[0][ord][lane] = own.G;
+  sh.run[1][ord][lane] = own.P;
+  sh.run[2][ord][lane] = own.S;
+  __syncthreads();
+  Run r = identity();
+  for (int w = 0; w < ord; ++w)
+    r = join(r, Run{sh.run[0][w][lane], sh.run[1][w][lane], sh.run[2][w][lane]});
+  return r;
+}
+
+// From each thread's run to its states. start: the state that enters the first
+// chunk, or null. CHAIN: sequences have more than one chunk.
+template <bool REV, bool CHAIN>
+__device__ __forceinline__ States enter_states(const GScanArgs& A, const Place& p, Shared& sh,
+                                               const Run& own, const float* start) {
+  const int lane = threadIdx.x & 63, ord = REV ? kWaves - 1 - p.wave : p.wave;
+  const Run before = waves_before<REV>(p, sh, own);
+  const bool last = ord == kWaves - 1;
+  const Run total = join(before, own);  // of the chunk, in the last wave
+  const float first = start && p.on ? start[(size_t)p.b * A.C + p.c] : 0.f;
+  States st;
+  st.in = first;
+  if constexpr (CHAIN) {
+    const Board bd(A);
     const int g = p.step / kGroup, i = p.step % kGroup;
-    const size_t row0 = (size_t)p.b * p.nc + g * kGroup;  // runs in the order of the scan
-    if (last && p.on && i + 1 < kGroup && p.step + 1 < p.nc) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        post(bd.runs + (row0 + i) * A.C + p.c + j,
-             word(canonical(total[j].S), canonical(factor(total[j]))));
-    }
-    // wave w collects the runs of chunks w and w + 8 of the group; the first
-    // wave also the entering state
+    const uint64_t* runs = bd.runs + ((size_t)p.b * bd.nc + g * kGroup) * A.C + p.c;
+    uint64_t* enter = bd.enter + ((size_t)p.b * bd.ng + g) * A.C + p.c;
     if (p.on) {
-#pragma unroll
-      for (int h = 0; h < kGroup / kWaves; ++h) {
-        const int q = h * kWaves + ord;
-        if (q < i) {
-          uint64_t v[VEC];
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) v[j] = peek(bd.runs + (row0 + q) * A.C + p.c + j);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            while (v[j] == kUnset) {
-              __builtin_amdgcn_s_sleep(1);
-              v[j] = peek(bd.runs + (row0 + q) * A.C + p.c + j);
-            }
-            sh.prev[q][l0 + j] = make_float2(__uint_as_float((uint32_t)(v[j] >> 32)),
-                                             __uint_as_float((uint32_t)v[j]));
-          }
-        }
+      if (last && i + 1 < kGroup && p.step + 1 < p.nc)
+        post(const_cast<uint64_t*>(runs) + (size_t)i * A.C,
+             word(canonical(total.S), canonical(factor(total))));
+      // wave w collects the runs of chunks w and w + 8 of the group, the last
+      // wave also the entering state
+      for (int q = ord; q < i; q += kWaves) {
+        const uint64_t v = wait_for(runs + (size_t)q * A.C);
+        sh.prev[q][lane] = make_float2(__uint_as_float((uint32_t)(v >> 32)),
+                                       __uint_as_float((uint32_t)v));
       }
-      if (last) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          if (g == 0) {
-            sh.enter[l0 + j] = start ? start[(size_t)p.b * A.C + p.c + j] : 0.f;
-          } else {
-            const uint64_t* e = bd.enter + ((size_t)p.b * bd.ng + g) * A.C + p.c + j;
-            uint64_t v = peek(e);
-            while (v == kUnset) {
-              __builtin_amdgcn_s_sleep(1);
-              v = peek(e);
-            }
-            sh.enter[l0 + j] = __uint_as_float((uint32_t)v);
-          }
-        }
-      }
+      if (last) sh.enter[lane] = g == 0 ? first : __uint_as_float((uint32_t)wait_for(enter));
     }
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) chunk_in[j] = p.on ? sh.enter[l0 + j] : 0.f;
     if (p.on) {
+      st.in = sh.enter[lane];
       for (int q = 0; q < i; ++q) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float2 r = sh.prev[q][l0 + j];
-          chunk_in[j] = r.y + decay(r.x, chunk_in[j]);
-        }
+        const float2 r = sh.prev[q][lane];
+        st.in = r.y + decay(r.x, st.in);
       }
-    }
-    if (last && p.on && i + 1 == kGroup && p.step + 1 < p.nc) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        post(bd.enter + ((size_t)p.b * bd.ng + g + 1) * A.C + p.c + j,
-             word(apply(total[j], chunk_in[j]), 0.f));
+      if (last && i + 1 == kGroup && p.step + 1 < p.nc)
+        post(enter + A.C, word(apply(total, st.in), 0.f));
     }
   }
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    mine[j] = apply(before[j], chunk_in[j]);
-    chunk_out[j] = apply(total[j], chunk_in[j]);
-  }
+  st.mine = apply(before, st.in);
+  st.out = apply(total, st.in);
+  return st;
 }
 
-// ---------------------------------------------------------------- forward
-
-// The chunk's rows of a tensor as a buffer, and the offset of this thread's
-// first token in it.
+// The chunk's rows of a tensor as a buffer.
 template <typename T>
 __device__ __forceinline__ BufRes chunk_buffer(const void* t, size_t row, int64_t ld, int rows,
                                                int C) {
@@ -323,67 +275,60 @@ __device__ __forceinline__ BufRes chunk_buffer(const void* t, size_t row, int64_
                    rows > 0 ? ((uint64_t)(rows - 1) * ld + C) * sizeof(T) : 0);
 }
 
-template <typename T, int VEC, bool CHAIN, bool GATED>
+// ---------------------------------------------------------------- forward
+
+template <typename T, bool CHAIN, bool GATED>
 __global__ __launch_bounds__(kTh) void gscan_kernel(GScanArgs A) {
+  constexpr uint32_t ES = sizeof(T);
   __shared__ Shared sh;
-  const Place<VEC> p = take_place<VEC, false, CHAIN>(A, sh);
+  const Place p = take_place<false, CHAIN>(A, sh);
   const int t1 = p.chunk * kChunk, rows = min(kChunk, A.T - t1);  // the chunk's rows
   const size_t row = (size_t)p.b * A.T + t1;
-  const int w0 = p.t0 - t1;                                     // this thread's first row
-  const int live = min(max(p.len - p.t0, 0), kTpt);             // its tokens in use
+  const int w0 = p.t0 - t1;                          // this thread's first row
+  const int live = min(max(p.len - p.t0, 0), kTpt);  // its tokens in use
   const BufRes rx = chunk_buffer<T>(A.x, row, A.ld, rows, A.C);
   const BufRes rf = chunk_buffer<T>(A.f, row, A.ld, rows, A.C);
   const BufRes ro = chunk_buffer<T>(GATED ? A.o : A.x, row, A.ld, rows, A.C);
   const BufRes ry = chunk_buffer<T>(A.y, row, A.C, rows, A.C);
-  const uint32_t pitch = (uint32_t)A.ld * sizeof(T), ypitch = A.C * (uint32_t)sizeof(T);
-  const uint32_t col = p.on ? p.c * (uint32_t)sizeof(T) : kOOB;
+  const uint32_t pitch = (uint32_t)A.ld * ES, ypitch = A.C * ES;
+  const uint32_t col = p.on ? p.c * ES : kOOB;
+  if (p.dead) {
+#pragma unroll
+    for (int i = 0; i < kTpt; ++i)
+      store_one<T>(ry, w0 + i < rows ? col : kOOB, (w0 + i) * ypitch, 0.f);
+    return;
+  }
   uint32_t xr[kTpt], fr[kTpt], gr[kTpt];
 #pragma unroll
   for (int i = 0; i < kTpt; ++i) {
     const uint32_t off = i < live ? col : kOOB, r = (w0 + i) * pitch;
-    fr[i] = load_bits<T, VEC>(rf, off, r);
-    xr[i] = load_bits<T, VEC>(rx, off, r);
-    gr[i] = 0;
-    if constexpr (GATED) gr[i] = load_bits<T, VEC>(ro, off, r);
+    fr[i] = load_bits<T>(rf, off, r);
+    xr[i] = load_bits<T>(rx, off, r);
+    if constexpr (GATED) gr[i] = load_bits<T>(ro, off, r);
   }
-  float k[kTpt][VEC];
-  Run own[VEC];
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) own[j] = identity();
+  float k[kTpt];
+  Run own = identity();
 #pragma unroll
   for (int i = 0; i < kTpt; ++i) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      // past the length: f = 1 (and x reads as 0)
-      k[i][j] = i < live ? gate_of(channel<T, VEC>(fr[i], j)) : 0.f;
-      extend(own[j], k[i][j]);
-      own[j].S = step(k[i][j], channel<T, VEC>(xr[i], j), own[j].S);
-    }
+    // past the length: f = 1 (and x reads as 0)
+    k[i] = i < live ? gate_of(value<T>(fr[i])) : 0.f;
+    extend(own, k[i]);
+    own.S = step(k[i], value<T>(xr[i]), own.S);
   }
-  float h[VEC], cin[VEC], cout[VEC];
-  enter_states<VEC, false, CHAIN>(A, p, sh, own, A.h_init, h, cin, cout);
-  if (p.on && A.carry && threadIdx.x < 64) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) A.carry[p.cw * A.C + p.c + j] = cin[j];
-  }
-  if (p.on && A.h_final && p.step == p.nc - 1 && threadIdx.x >= kTh - 64) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) A.h_final[(size_t)p.b * A.C + p.c + j] = cout[j];
-  }
+  const States st = enter_states<false, CHAIN>(A, p, sh, own, A.h_init);
+  if (p.on && A.carry && p.wave == 0) A.carry[p.cw * A.C + p.c] = st.in;
+  if (p.on && A.h_final && p.step == p.nc - 1 && p.wave == kWaves - 1)
+    A.h_final[(size_t)p.b * A.C + p.c] = st.out;
+  float h = st.mine;
 #pragma unroll
   for (int i = 0; i < kTpt; ++i) {
-    float v[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      h[j] = step(k[i][j], channel<T, VEC>(xr[i], j), h[j]);
-      v[j] = h[j];
-      if constexpr (GATED) {
-        const float ov = channel<T, VEC>(gr[i], j);
-        v[j] *= ov * sigm(ov);
-      }
-      v[j] = i < live ? v[j] : 0.f;
+    h = step(k[i], value<T>(xr[i]), h);
+    float v = h;
+    if constexpr (GATED) {
+      const float ov = value<T>(gr[i]);
+      v *= ov * sigm(ov);
     }
-    store_bits<T, VEC>(ry, w0 + i < rows ? col : kOOB, (w0 + i) * ypitch, v);
+    store_one<T>(ry, w0 + i < rows ? col : kOOB, (w0 + i) * ypitch, i < live ? v : 0.f);
   }
 }
 
@@ -392,10 +337,11 @@ __global__ __launch_bounds__(kTh) void gscan_kernel(GScanArgs A) {
 // Walking back, c = f_t e_t is the gradient that leaves token t for the state
 // before it: c <- f (u + c), u = dy silu(gate). The states come from the
 // forward's carry and the runs of the chunk's waves.
-template <typename T, int VEC, bool CHAIN, bool GATED>
+template <typename T, bool CHAIN, bool GATED>
 __global__ __launch_bounds__(kTh) void gscan_bwd_kernel(GScanArgs A) {
+  constexpr uint32_t ES = sizeof(T);
   __shared__ Shared sh;
-  const Place<VEC> p = take_place<VEC, true, CHAIN>(A, sh);
+  const Place p = take_place<true, CHAIN>(A, sh);
   const int t1 = p.chunk * kChunk, rows = min(kChunk, A.T - t1);
   const size_t row = (size_t)p.b * A.T + t1;
   const int w0 = p.t0 - t1;
@@ -407,89 +353,70 @@ __global__ __launch_bounds__(kTh) void gscan_bwd_kernel(GScanArgs A) {
   const BufRes sx = chunk_buffer<T>(A.dx, row, A.ldd, rows, A.C);
   const BufRes sf = chunk_buffer<T>(A.df, row, A.ldd, rows, A.C);
   const BufRes so = chunk_buffer<T>(GATED ? A.d_o : A.dx, row, A.ldd, rows, A.C);
-  constexpr uint32_t ES = sizeof(T);
   const uint32_t pitch = (uint32_t)A.ld * ES, dpitch = (uint32_t)A.ldd * ES;
   const uint32_t col = p.on ? p.c * ES : kOOB;
+  if (p.dead) {
+#pragma unroll
+    for (int i = 0; i < kTpt; ++i) {
+      const uint32_t off = w0 + i < rows ? col : kOOB, r = (w0 + i) * dpitch;
+      store_one<T>(sx, off, r, 0.f);
+      store_one<T>(sf, off, r, 0.f);
+      if constexpr (GATED) store_one<T>(so, off, r, 0.f);
+    }
+    return;
+  }
   uint32_t xr[kTpt], fr[kTpt], gr[kTpt], dr[kTpt];
 #pragma unroll
   for (int i = 0; i < kTpt; ++i) {
     const uint32_t off = i < live ? col : kOOB, r = (w0 + i) * pitch;
-    fr[i] = load_bits<T, VEC>(rf, off, r);
-    dr[i] = load_bits<T, VEC>(rd, off, (w0 + i) * A.C * ES);
-    gr[i] = 0;
-    if constexpr (GATED) gr[i] = load_bits<T, VEC>(ro, off, r);
-    xr[i] = load_bits<T, VEC>(rx, off, r);
+    fr[i] = load_bits<T>(rf, off, r);
+    dr[i] = load_bits<T>(rd, off, (w0 + i) * A.C * ES);
+    if constexpr (GATED) gr[i] = load_bits<T>(ro, off, r);
+    xr[i] = load_bits<T>(rx, off, r);
   }
-  float k[kTpt][VEC], e[kTpt][VEC];
-  Run fw[VEC], bw[VEC];
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) fw[j] = bw[j] = identity();
+  float k[kTpt], e[kTpt];
+  Run fw = identity();
 #pragma unroll
   for (int i = 0; i < kTpt; ++i) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      k[i][j] = i < live ? gate_of(channel<T, VEC>(fr[i], j)) : 0.f;
-      e[i][j] = channel<T, VEC>(dr[i], j);
-      if constexpr (GATED) {
-        const float ov = channel<T, VEC>(gr[i], j);
-        e[i][j] *= ov * sigm(ov);
-      }
-      extend(fw[j], k[i][j]);
-      fw[j].S = step(k[i][j], channel<T, VEC>(xr[i], j), fw[j].S);
+    k[i] = i < live ? gate_of(value<T>(fr[i])) : 0.f;
+    e[i] = value<T>(dr[i]);
+    if constexpr (GATED) {
+      const float ov = value<T>(gr[i]);
+      e[i] *= ov * sigm(ov);
     }
+    extend(fw, k[i]);
+    fw.S = step(k[i], value<T>(xr[i]), fw.S);
   }
+  Run bw = fw;
+  bw.S = 0.f;
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    bw[j].G = fw[j].G;
-    bw[j].P = fw[j].P;
-  }
-#pragma unroll
-  for (int i = kTpt - 1; i >= 0; --i)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) bw[j].S = decay(k[i][j], e[i][j] + bw[j].S);
-  float h[VEC], c[VEC], cin[VEC], cout[VEC];
-  GScanArgs F = A;  // the forward's state entering the chunk, as a sequence of one chunk
-  {
-    Place<VEC> q = p;
-    q.b = 0;
-    q.on = p.on;
-    enter_states<VEC, false, false>(F, q, sh, fw, A.carry_in + p.cw * A.C, h, cin, cout);
-    __syncthreads();  // the runs in LDS are no longer read
-  }
-  enter_states<VEC, true, CHAIN>(A, p, sh, bw, A.dh_final, c, cin, cout);
-  if (p.on && A.dh_init && p.step == p.nc - 1 && threadIdx.x < 64) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) A.dh_init[(size_t)p.b * A.C + p.c + j] = cout[j];
-  }
+  for (int i = kTpt - 1; i >= 0; --i) bw.S = decay(k[i], e[i] + bw.S);
+  const Run fbefore = waves_before<false>(p, sh, fw);
+  float h = p.on ? apply(fbefore, A.carry_in[p.cw * A.C + p.c]) : 0.f;
+  __syncthreads();  // the runs in LDS are no longer read
+  const States st = enter_states<true, CHAIN>(A, p, sh, bw, A.dh_final);
+  if (p.on && A.dh_init && p.step == p.nc - 1 && p.wave == 0)
+    A.dh_init[(size_t)p.b * A.C + p.c] = st.out;
   // e_t from the last token back
+  float c = st.mine;
 #pragma unroll
   for (int i = kTpt - 1; i >= 0; --i) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      e[i][j] += c[j];
-      c[j] = decay(k[i][j], e[i][j]);
-    }
+    e[i] += c;
+    c = decay(k[i], e[i]);
   }
 #pragma unroll
   for (int i = 0; i < kTpt; ++i) {
-    float vx[VEC], vf[VEC], vo[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float kk = k[i][j], a = fabsf(kk), xv = channel<T, VEC>(xr[i], j);
-      vx[j] = i < live ? inject(kk, e[i][j]) : 0.f;
-      vf[j] = i < live ? __builtin_fmaf(-a, a, a) * e[i][j] * (h[j] - xv) : 0.f;
-      h[j] = step(kk, xv, h[j]);
-      vo[j] = 0.f;
-      if constexpr (GATED) {
-        const float ov = channel<T, VEC>(gr[i], j), sg = sigm(ov);
-        vo[j] = channel<T, VEC>(dr[i], j) * h[j] * (sg * __builtin_fmaf(ov, 1.f - sg, 1.f));
-        vo[j] = i < live ? vo[j] : 0.f;
-      }
-    }
+    const float kk = k[i], a = fabsf(kk), xv = value<T>(xr[i]);
     const uint32_t off = w0 + i < rows ? col : kOOB, r = (w0 + i) * dpitch;
-    store_bits<T, VEC>(sx, off, r, vx);
-    store_bits<T, VEC>(sf, off, r, vf);
-    if constexpr (GATED) store_bits<T, VEC>(so, off, r, vo);
+    const bool in = i < live;
+    store_one<T>(sx, off, r, in ? inject(kk, e[i]) : 0.f);
+    store_one<T>(sf, off, r, in ? __builtin_fmaf(-a, a, a) * e[i] * (h - xv) : 0.f);
+    h = step(kk, xv, h);
+    if constexpr (GATED) {
+      const float ov = value<T>(gr[i]), sg = sigm(ov);
+      const float vo = value<T>(dr[i]) * h * (sg * __builtin_fmaf(ov, 1.f - sg, 1.f));
+      store_one<T>(so, off, r, in ? vo : 0.f);
+    }
   }
 }
 
@@ -559,17 +486,11 @@ __global__ __launch_bounds__(256) void gscan_step_kernel(const T* __restrict__ x
 
 // ---------------------------------------------------------------- launch
 
-// bf16 rows are taken two channels (4 bytes) per lane where every row starts on
-// a pair and has whole pairs; fp32 rows one channel (also 4 bytes) per lane.
-bool in_pairs(int C, int64_t ld, int64_t ldd) { return C % 2 == 0 && ld % 2 == 0 && ldd % 2 == 0; }
-
-unsigned units(const GScanArgs& A, int vec) {
-  return (unsigned)((A.C + 64 * vec - 1) / (64 * vec)) * (unsigned)gscan_chunks(A.T) *
-         (unsigned)A.Bt;
-}
-
+// One channel per lane for both types: pairs of bf16 channels (4-byte accesses)
+// needed 121 and 234 registers against 84 and 129 and were 3 % and 15 % slower
+// (65536 x 2048 forward, padded 8 x 2048 x 1536 training step).
 // BWD: the backward's kernel.
-template <typename T, int VEC, bool BWD>
+template <typename T, bool BWD>
 hipError_t go(const GScanArgs& A, hipStream_t s) {
   hipEvent_t e0, e1;
   const bool chain = gscan_chunks(A.T) > 1;
@@ -581,13 +502,13 @@ hipError_t go(const GScanArgs& A, hipStream_t s) {
                           (uint4*)A.ws, n);
   }
   prof_kernel(BWD ? "gated_scan_bwd" : "gated_scan", &e0, &e1);
-  const dim3 grid(units(A, VEC));
+  const dim3 grid((unsigned)gscan_blocks(A.Bt, A.T, A.C));
   auto run = [&](auto chained, auto gated) {
     constexpr bool CH = decltype(chained)::value, GA = decltype(gated)::value;
     if constexpr (BWD)
-      hipExtLaunchKernelGGL((gscan_bwd_kernel<T, VEC, CH, GA>), grid, dim3(kTh), 0, s, e0, e1, 0, A);
+      hipExtLaunchKernelGGL((gscan_bwd_kernel<T, CH, GA>), grid, dim3(kTh), 0, s, e0, e1, 0, A);
     else
-      hipExtLaunchKernelGGL((gscan_kernel<T, VEC, CH, GA>), grid, dim3(kTh), 0, s, e0, e1, 0, A);
+      hipExtLaunchKernelGGL((gscan_kernel<T, CH, GA>), grid, dim3(kTh), 0, s, e0, e1, 0, A);
   };
   const std::true_type yes{};
   const std::false_type no{};
@@ -611,13 +532,11 @@ size_t gscan_ws_bytes(int Bt, int T, int C) {
 }
 
 hipError_t launch_gscan(bool is_bf16, const GScanArgs& a, hipStream_t s) {
-  if (!is_bf16) return go<float, 1, false>(a, s);
-  return in_pairs(a.C, a.ld, 0) ? go<bf16, 2, false>(a, s) : go<bf16, 1, false>(a, s);
+  return is_bf16 ? go<bf16, false>(a, s) : go<float, false>(a, s);
 }
 
 hipError_t launch_gscan_backward(bool is_bf16, const GScanArgs& a, hipStream_t s) {
-  if (!is_bf16) return go<float, 1, true>(a, s);
-  return in_pairs(a.C, a.ld, a.ldd) ? go<bf16, 2, true>(a, s) : go<bf16, 1, true>(a, s);
+  return is_bf16 ? go<bf16, true>(a, s) : go<float, true>(a, s);
 }
 
 hipError_t launch_gscan_step(bool is_bf16, const void* x, const void* f, const void* o, int64_t ld,

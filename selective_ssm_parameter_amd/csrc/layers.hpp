@@ -26,6 +26,7 @@ struct NormBwdArgs {
 };
 constexpr int kNormMaxD = 32768;  // a row is held in the registers of 1024 threads
 int norm_bwd_parts(int M, int D);
+int64_t norm_fwd_threads(int64_t M, int D);  // of the forward's launch
 hipError_t launch_norm_fwd(bool is_bf16, const NormFwdArgs& a, hipStream_t s);
 hipError_t launch_norm_bwd(bool is_bf16, bool dy_f32, const NormBwdArgs& a, hipStream_t s);
 

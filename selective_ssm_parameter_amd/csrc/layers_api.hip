@@ -29,7 +29,7 @@ swimba_status check_norm(const Dims& d) {
   if (d.D > kNormMaxD)
     return fail(SWIMBA_ERR_UNSUPPORTED, "d_model %lld: the layer norm holds a row of at most %d",
                 (long long)d.D, kNormMaxD);
-  if (d.M * (d.D <= 2048 ? 64 : (d.D <= 8192 ? 256 : 1024)) >= kMaxThreads - 1024)
+  if (norm_fwd_threads(d.M, (int)d.D) >= kMaxThreads)
     return fail(SWIMBA_ERR_DIMS, "too many rows of this width for one launch");
   return SWIMBA_OK;
 }

@@ -4,12 +4,16 @@
 // mean(s), var = mean((s - mu)^2), y = (s - mu) (var + eps)^(-1/2) w + b.
 // Backward, per row, with xh = (s - mu) rstd and g = dy w: dx = dres + rstd
 // (g - mean(g) - xh mean(g xh)); over the rows dw = sum dy xh, db = sum dy.
-// Both are bound by HBM: a row is read once, held in registers (32 elements
-// per thread at most) and written once; the variance is a second pass over
-// the registers, so that an offset common to the row does not cancel. The
-// weight gradients stay in registers over all rows that a workgroup takes,
-// one partial row per workgroup goes to the workspace, and a second kernel
-// adds the partial rows in order.
+// Both are bound by HBM: a row is read once, held in registers and written
+// once; the variance is a second pass over the registers, so that an offset
+// common to the row does not cancel. A row takes 4 to 1024 threads, 8 elements
+// each in the forward (one 16-byte access of bf16; 32768 x 2048: 91 us with 256
+// threads a row, 102 with 64) and 16 in the backward, whose weight gradients
+// stay in registers over all rows that a workgroup takes, with the next row's
+// loads in flight; one partial row per workgroup goes to the workspace, and a
+// second kernel adds the partial rows in order.
+#include <algorithm>
+
 #include "common.hpp"
 #include "layers.hpp"
 
@@ -50,16 +54,16 @@ __device__ __forceinline__ void storev(T* p, const float* v) {
   }
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+// Sum over the NT threads of a row, in a butterfly within a wave.
+template <int NT>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  for (int off = (NT < 64 ? NT : 64) / 2; off > 0; off >>= 1) v += __shfl_xor(v, off);
   return v;
 }
-
-// Sum over the NT threads of a row (NT = 64: one wave; else the workgroup).
 template <int NT>
 __device__ __forceinline__ float row_sum(float v, float* red) {
-  v = wave_sum(v);
+  v = lanes_sum<NT>(v);
   if constexpr (NT > 64) {
     __syncthreads();  // the previous sum has been read
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
@@ -71,11 +75,12 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return v;
 }
 
-// Rows per workgroup of the forward and the backward.
+// Threads and rows per workgroup.
 template <int NT>
 struct RowCfg {
-  static constexpr int TH = NT < 256 ? 256 : NT;  // threads per workgroup
+  static constexpr int TH = NT <= 64 ? 256 : NT;
   static constexpr int RP = TH / NT;
+  static constexpr int NW = NT < 64 ? 1 : NT / 64;  // waves per row
 };
 
 template <typename T, int VEC, int NT, int EPT>
@@ -83,10 +88,10 @@ __global__ __launch_bounds__(RowCfg<NT>::TH) void norm_fwd_kernel(
     const T* x, const T* residual, const T* __restrict__ weight, const T* __restrict__ bias,
     float eps, T* sum, T* y, float* __restrict__ mean, float* __restrict__ rstd, int M, int D) {
   constexpr int VPT = EPT / VEC;
-  __shared__ float red[NT / 64];
+  __shared__ float red[RowCfg<NT>::NW];
   const int tid = threadIdx.x % NT;
   const int m = blockIdx.x * RowCfg<NT>::RP + threadIdx.x / NT;
-  if (m >= M) return;  // whole waves, and whole workgroups where they share a row
+  if (m >= M) return;  // all threads of the row, and of the workgroup where a row has it alone
   const size_t base = (size_t)m * D;
   float v[VPT][VEC];
 #pragma unroll
@@ -160,8 +165,8 @@ __global__ __launch_bounds__(RowCfg<NT>::TH) void norm_bwd_kernel(
     const T* __restrict__ s, const T* __restrict__ weight, const float* __restrict__ mean,
     const float* __restrict__ rstd, const TG* dy, const float* dres, float* dx,
     float* __restrict__ part, int M, int D) {
-  constexpr int VPT = EPT / VEC, RP = RowCfg<NT>::RP, TH = RowCfg<NT>::TH;
-  __shared__ float red[2 * (NT / 64)];
+  constexpr int VPT = EPT / VEC, RP = RowCfg<NT>::RP, TH = RowCfg<NT>::TH, NW = RowCfg<NT>::NW;
+  __shared__ float red[2 * NW];
   extern __shared__ float acc_sh[];  // [2][D] where several rows share the workgroup
   const int tid = threadIdx.x % NT, sub = threadIdx.x / NT;
   float w[VPT][VEC], dw[VPT][VEC], db[VPT][VEC];
@@ -173,20 +178,34 @@ __global__ __launch_bounds__(RowCfg<NT>::TH) void norm_bwd_kernel(
     if (c < D) loadv<T, VEC>(weight + c, w[i]);
   }
   const float inv = 1.f / (float)D;
-  for (int m = blockIdx.x * RP + sub; m < M; m += gridDim.x * RP) {
+  struct Row {
+    float s[VPT][VEC], g[VPT][VEC], r[VPT][VEC], mu, rs;
+  };
+  auto load = [&](Row& q, int m) {
     const size_t base = (size_t)m * D;
-    float xh[VPT][VEC], g[VPT][VEC];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * NT + tid) * VEC;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) xh[i][j] = g[i][j] = 0.f;
+      for (int j = 0; j < VEC; ++j) q.s[i][j] = q.g[i][j] = q.r[i][j] = 0.f;
       if (c < D) {
-        loadv<T, VEC>(s + base + c, xh[i]);
-        loadv<TG, VEC>(dy + base + c, g[i]);
+        loadv<T, VEC>(s + base + c, q.s[i]);
+        loadv<TG, VEC>(dy + base + c, q.g[i]);
+        if (dres) loadv<float, VEC>(dres + base + c, q.r[i]);
       }
     }
-    const float mu = mean[m], rs = rstd[m];
+    q.mu = mean[m];
+    q.rs = rstd[m];
+  };
+  const int step = gridDim.x * RP;
+  int m = blockIdx.x * RP + sub;
+  // 1024 threads have 128 registers each: no room for the next row
+  constexpr bool AHEAD = NT < 1024;
+  Row cur, nxt;
+  if (AHEAD && m < M) load(cur, m);
+  for (; m < M; m += step) {
+    if constexpr (!AHEAD) load(cur, m);
+    else if (m + step < M) load(nxt, m + step);
     float sg = 0.f, sx = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -194,17 +213,17 @@ __global__ __launch_bounds__(RowCfg<NT>::TH) void norm_bwd_kernel(
       if (c < D) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          xh[i][j] = (xh[i][j] - mu) * rs;
-          dw[i][j] += g[i][j] * xh[i][j];
-          db[i][j] += g[i][j];
-          g[i][j] *= w[i][j];
-          sg += g[i][j];
-          sx += g[i][j] * xh[i][j];
+          cur.s[i][j] = (cur.s[i][j] - cur.mu) * cur.rs;
+          dw[i][j] += cur.g[i][j] * cur.s[i][j];
+          db[i][j] += cur.g[i][j];
+          cur.g[i][j] *= w[i][j];
+          sg += cur.g[i][j];
+          sx += cur.g[i][j] * cur.s[i][j];
         }
       }
     }
-    sg = wave_sum(sg);
-    sx = wave_sum(sx);
+    sg = lanes_sum<NT>(sg);
+    sx = lanes_sum<NT>(sx);
     if constexpr (NT > 64) {
       __syncthreads();  // the previous row's sums have been read
       if ((threadIdx.x & 63) == 0) {
@@ -214,41 +233,53 @@ __global__ __launch_bounds__(RowCfg<NT>::TH) void norm_bwd_kernel(
       __syncthreads();
       sg = sx = 0.f;
 #pragma unroll
-      for (int q = 0; q < NT / 64; ++q) {
+      for (int q = 0; q < NW; ++q) {
         sg += red[2 * q];
         sx += red[2 * q + 1];
       }
     }
     const float mg = sg * inv, mx = sx * inv;
+    const size_t base = (size_t)m * D;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * NT + tid) * VEC;
       if (c < D) {
-        float r[VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) r[j] = 0.f;
-        if (dres) loadv<float, VEC>(dres + base + c, r);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) r[j] += rs * (g[i][j] - mg - xh[i][j] * mx);
-        storev<float, VEC>(dx + base + c, r);
+        for (int j = 0; j < VEC; ++j)
+          cur.r[i][j] += cur.rs * (cur.g[i][j] - mg - cur.s[i][j] * mx);
+        storev<float, VEC>(dx + base + c, cur.r[i]);
       }
     }
+    if constexpr (AHEAD) cur = nxt;
   }
-  // one partial row of dw and of db per workgroup: the row groups in order
+  // one partial row of dw and of db per workgroup: the rows of a wave in a
+  // butterfly, then the waves (or the rows of wider groups) in order
+#pragma unroll
+  for (int off = NT; off < 64; off *= 2) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        dw[i][j] += __shfl_xor(dw[i][j], off);
+        db[i][j] += __shfl_xor(db[i][j], off);
+      }
+  }
   float* pw = part + (size_t)blockIdx.x * 2 * D;
   if constexpr (RP == 1) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * NT + tid) * VEC;
       if (c < D) {
-        storev<float, VEC>(pw + c, dw[i]);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) pw[D + c + j] = db[i][j];
+        for (int j = 0; j < VEC; ++j) {
+          pw[c + j] = dw[i][j];
+          pw[D + c + j] = db[i][j];
+        }
       }
     }
   } else {
-    for (int r = 0; r < RP; ++r) {
-      if (sub == r) {
+    for (int r = 0; r < TH / 64; ++r) {
+      if ((int)(threadIdx.x >> 6) == r && (threadIdx.x & 63) < NT) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
           const int c = (i * NT + tid) * VEC;
@@ -267,24 +298,26 @@ __global__ __launch_bounds__(RowCfg<NT>::TH) void norm_bwd_kernel(
   }
 }
 
-// dw and db: the np partial rows added in a fixed order (8 interleaved sums
+// dw and db: the np partial rows added in a fixed order (32 interleaved sums
 // per column, joined in order).
-__global__ __launch_bounds__(256) void norm_dw_kernel(const float* __restrict__ part, int np,
-                                                      int D, float* __restrict__ dw,
-                                                      float* __restrict__ db) {
-  __shared__ float sh[8][32];
+constexpr int kDwSums = 32;
+__global__ __launch_bounds__(32 * kDwSums) void norm_dw_kernel(const float* __restrict__ part,
+                                                               int np, int D,
+                                                               float* __restrict__ dw,
+                                                               float* __restrict__ db) {
+  __shared__ float sh[kDwSums][32];
   const int cl = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + cl;  // column of [dw | db]
   float a = 0.f;
   if (c < 2 * D) {
 #pragma unroll 8
-    for (int p = grp; p < np; p += 8) a += part[(size_t)p * 2 * D + c];
+    for (int p = grp; p < np; p += kDwSums) a += part[(size_t)p * 2 * D + c];
   }
   sh[grp][cl] = a;
   __syncthreads();
   if (grp == 0 && c < 2 * D) {
 #pragma unroll
-    for (int q = 1; q < 8; ++q) a += sh[q][cl];
+    for (int q = 1; q < kDwSums; ++q) a += sh[q][cl];
     if (c < D) dw[c] = a;
     else if (db) db[c - D] = a;
   }
@@ -313,48 +346,61 @@ hipError_t bwd_cfg(const NormBwdArgs& a, hipStream_t s) {
                         (const T*)a.s, (const T*)a.weight, a.mean, a.rstd, (const TG*)a.dy, a.dres,
                         a.dx, a.part, a.M, a.D);
   prof_kernel("layer_norm_dw", &e0, &e1);
-  hipExtLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((2 * a.D + 31) / 32)), dim3(256), 0, s, e0,
-                        e1, 0, a.part, np, a.D, a.dw, a.db);
+  hipExtLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((2 * a.D + 31) / 32)),
+                        dim3(32 * kDwSums), 0, s, e0, e1, 0, a.part, np, a.D, a.dw, a.db);
   return hipGetLastError();
 }
 
-// Threads per row: one wave up to 64 x 32 elements, then a workgroup of 256
-// or 1024.
-int row_threads(int D) { return D <= 2048 ? 64 : (D <= 8192 ? 256 : 1024); }
+// Threads per row for E elements each; 1024 threads then take up to 32 each.
+int row_threads(int D, int E) {
+  for (int nt : {4, 16, 64, 128, 256, 512})
+    if (D <= nt * E) return nt;
+  return 1024;
+}
 
-#define SWIMBA_NORM_CFG(CALL)                                   \
-  const int nt = row_threads(a.D), ept = (a.D + nt - 1) / nt;   \
-  if (nt == 64) {                                               \
-    if (ept <= 8) return CALL(64, 8);                           \
-    if (ept <= 16) return CALL(64, 16);                         \
-    return CALL(64, 32);                                        \
-  }                                                             \
-  if (nt == 256) {                                              \
-    if (ept <= 16) return CALL(256, 16);                        \
-    return CALL(256, 32);                                       \
-  }                                                             \
-  if (ept <= 16) return CALL(1024, 16);                         \
+// CALL(threads, elements per thread) for E elements per thread.
+#define SWIMBA_NORM_CFG(E, CALL)             \
+  switch (row_threads(a.D, E)) {             \
+    case 4: return CALL(4, E);               \
+    case 16: return CALL(16, E);             \
+    case 64: return CALL(64, E);             \
+    case 128: return CALL(128, E);           \
+    case 256: return CALL(256, E);           \
+    case 512: return CALL(512, E);           \
+    default: break;                          \
+  }                                          \
+  if (a.D <= 8192) return CALL(1024, 8);     \
+  if (a.D <= 16384) return CALL(1024, 16);   \
   return CALL(1024, 32)
+
+constexpr int kFwdE = 8, kBwdE = 16;
 
 template <typename T, int VEC>
 hipError_t fwd_t(const NormFwdArgs& a, hipStream_t s) {
 #define CALL(NT, EPT) fwd_cfg<T, VEC, NT, EPT>(a, s)
-  SWIMBA_NORM_CFG(CALL);
+  SWIMBA_NORM_CFG(kFwdE, CALL);
 #undef CALL
 }
 template <typename T, typename TG, int VEC>
 hipError_t bwd_t(const NormBwdArgs& a, hipStream_t s) {
 #define CALL(NT, EPT) bwd_cfg<T, TG, VEC, NT, EPT>(a, s)
-  SWIMBA_NORM_CFG(CALL);
+  SWIMBA_NORM_CFG(kBwdE, CALL);
 #undef CALL
 }
 
 }  // namespace
 
+// Workgroups of the backward, each with one partial row: as many as the chip
+// holds at once (8 waves per CU), or fewer with at least four rows each.
 int norm_bwd_parts(int M, int D) {
-  const int rp = row_threads(D) == 64 ? 4 : 1;
-  const int wgs = (M + rp - 1) / rp;
-  return wgs < 512 ? wgs : 512;
+  const int nt = row_threads(D, kBwdE), th = nt <= 64 ? 256 : nt, rp = th / nt;
+  const int64_t wgs = (M + 4 * rp - 1) / (4 * rp);
+  return (int)std::min<int64_t>(std::max<int64_t>(wgs, 1), 256 * 512 / th);
+}
+
+int64_t norm_fwd_threads(int64_t M, int D) {
+  const int nt = row_threads(D, kFwdE), th = nt <= 64 ? 256 : nt, rp = th / nt;
+  return (M + rp - 1) / rp * th;
 }
 
 hipError_t launch_norm_fwd(bool is_bf16, const NormFwdArgs& a, hipStream_t s) {

@@ -78,56 +78,61 @@ def gated_scan_carry(dims, device="cuda") -> torch.Tensor:
     return torch.empty(max(n // 4, 4), dtype=torch.float32, device=device)
 
 
-def _ptrs(*tensors):
-    """Device pointers of contiguous tensors on the current device (None stays None)."""
-    cur, out = torch.cuda.current_device() if torch.cuda.is_initialized() else -1, []
+# A decode step is a few microseconds on the GPU, so the marshalling below asks
+# torch for no more than it needs.
+
+def _device():
+    """The current device's index (-1 before CUDA is initialised)."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+
+
+def _refuse(t, dev):
+    if t.get_device() != dev:
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    raise ValueError("tensors passed to the Swimba library must be contiguous")
+
+
+def _ptrs(dev, *tensors):
+    """Device pointers of contiguous tensors on device dev (None stays None)."""
+    out = []
     for t in tensors:
         if t is None:
             out.append(None)
-            continue
-        if not t.is_contiguous():
-            raise ValueError("tensors passed to the Swimba library must be contiguous")
-        if t.get_device() != cur:
-            _wrong_device(t, cur)
-        out.append(t.data_ptr())
+        elif t.get_device() == dev and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            _refuse(t, dev)
     return out
 
 
-def _wrong_device(t, cur):
-    raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
-
-
-def _rows(*tensors):
+def _rows(dev, *tensors):
     """Pointers of [M, C] tensors whose rows are equally far apart, and that distance."""
-    cur = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
-    ld, ptrs = None, []
+    ld, ptrs, single = None, [], False
     for t in tensors:
         if t is None:
             ptrs.append(None)
             continue
-        if t.dim() != 2:
+        stride = t.stride()
+        if len(stride) != 2:
             t = t.view(-1, t.shape[-1])
-        rows, cols = t.shape
-        step, unit = t.stride()
-        if unit != 1 and cols > 1:
-            raise ValueError("rows of the gated scan must have unit stride along the channels")
-        if rows <= 1:
-            step = max(step, cols) if ld is None else ld
+            stride = t.stride()
         if ld is None:
-            ld = step
-        elif step != ld:
+            rows, cols = t.shape
+            single = rows <= 1
+            ld = max(stride[0], cols) if single else stride[0]
+        elif stride[0] != ld and not single:
             raise ValueError("the gated scan's tensors must have one row stride")
-        if t.get_device() != cur:
-            _wrong_device(t, cur)
+        if stride[1] != 1 and t.shape[1] > 1:
+            raise ValueError("rows of the gated scan must have unit stride along the channels")
+        if t.get_device() != dev:
+            _refuse(t, dev)
         ptrs.append(t.data_ptr())
     return ptrs, ld
 
 
-def _stream(stream):
+def _stream(stream, dev):
     if stream is None:
-        # the current stream's handle without a Stream object: a decode step is
-        # a few microseconds on the GPU
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -140,58 +145,66 @@ def _ws(ws, ws_bytes):
 
 def swimba_layer_norm(dims, x, residual, weight, bias, eps, sum, y, mean=None, rstd=None,
                       stream=None):
-    px, pr, pw, pb, ps, py, pm, pq = _ptrs(x, residual, weight, bias, sum, y, mean, rstd)
+    dev = _device()
+    px, pr, pw, pb, ps, py, pm, pq = _ptrs(dev, x, residual, weight, bias, sum, y, mean, rstd)
     _check(lib().swimba_layer_norm(ctypes.byref(dims), px, pr, pw, pb, eps, ps, py, pm, pq,
-                                   _stream(stream)))
+                                   _stream(stream, dev)))
 
 
 def swimba_layer_norm_backward(dims, s, weight, mean, rstd, dy, dres, dx, dweight, dbias, ws,
                                ws_bytes=None, stream=None):
+    dev = _device()
     if dy is not None and dy.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"dy of {dy.dtype}: bfloat16 or float32")
     dy_dtype = sb.BF16 if dy is not None and dy.dtype == torch.bfloat16 else sb.F32
-    p = _ptrs(s, weight, mean, rstd, dy, dres, dx, dweight, dbias, ws)
+    p = _ptrs(dev, s, weight, mean, rstd, dy, dres, dx, dweight, dbias, ws)
     _check(lib().swimba_layer_norm_backward(ctypes.byref(dims), *p[:5], dy_dtype, *p[5:],
-                                            _ws(ws, ws_bytes), _stream(stream)))
+                                            _ws(ws, ws_bytes), _stream(stream, dev)))
 
 
 def swimba_gated_scan(dims, x, forget, gate, seq_lens, h_init, y, h_final, carry, ws,
                       ws_bytes=None, stream=None):
-    rows, ld = _rows(x, forget, gate)
-    p = _ptrs(seq_lens, h_init, y, h_final, carry, ws)
+    dev = _device()
+    rows, ld = _rows(dev, x, forget, gate)
+    p = _ptrs(dev, seq_lens, h_init, y, h_final, carry, ws)
     _check(lib().swimba_gated_scan(ctypes.byref(dims), *rows, ld, *p, _ws(ws, ws_bytes),
-                                   _stream(stream)))
+                                   _stream(stream, dev)))
 
 
 def swimba_gated_scan_backward(dims, x, forget, gate, seq_lens, carry, dy, dh_final, dx, dforget,
                                dgate, dh_init, ws, ws_bytes=None, stream=None):
-    rows, ld = _rows(x, forget, gate)
-    drows, ldd = _rows(dx, dforget, dgate if gate is not None else None)
-    p = _ptrs(seq_lens, carry, dy, dh_final, dh_init, ws)
+    dev = _device()
+    rows, ld = _rows(dev, x, forget, gate)
+    drows, ldd = _rows(dev, dx, dforget, dgate if gate is not None else None)
+    p = _ptrs(dev, seq_lens, carry, dy, dh_final, dh_init, ws)
     _check(lib().swimba_gated_scan_backward(ctypes.byref(dims), *rows, ld, *p[:4], *drows, ldd,
-                                            *p[4:], _ws(ws, ws_bytes), _stream(stream)))
+                                            *p[4:], _ws(ws, ws_bytes), _stream(stream, dev)))
 
 
 def swimba_gated_step(dims, x, forget, gate, h_prev, h, y, stream=None):
-    rows, ld = _rows(x, forget, gate)
-    _check(lib().swimba_gated_step(ctypes.byref(dims), *rows, ld, *_ptrs(h_prev, h, y),
-                                   _stream(stream)))
+    dev = _device()
+    rows, ld = _rows(dev, x, forget, gate)
+    _check(lib().swimba_gated_step(ctypes.byref(dims), *rows, ld, *_ptrs(dev, h_prev, h, y),
+                                   _stream(stream, dev)))
 
 
 def swimba_gated_project(dims, x, w_in, act, z, h, stream=None):
-    px, pw, pz, ph = _ptrs(x, w_in, z, h)
-    _check(lib().swimba_gated_project(ctypes.byref(dims), px, pw, act, pz, ph, _stream(stream)))
+    dev = _device()
+    px, pw, pz, ph = _ptrs(dev, x, w_in, z, h)
+    _check(lib().swimba_gated_project(ctypes.byref(dims), px, pw, act, pz, ph, _stream(stream, dev)))
 
 
 def swimba_gated_project_backward(dims, x, w_in, dh, act, dx, dw_in, ws, ws_bytes=None,
                                   stream=None):
-    px, pw, pd, pdx, pdw, pws = _ptrs(x, w_in, dh, dx, dw_in, ws)
+    dev = _device()
+    px, pw, pd, pdx, pdw, pws = _ptrs(dev, x, w_in, dh, dx, dw_in, ws)
     _check(lib().swimba_gated_project_backward(ctypes.byref(dims), px, pw, pd, act, pdx, pdw, pws,
-                                               _ws(ws, ws_bytes), _stream(stream)))
+                                               _ws(ws, ws_bytes), _stream(stream, dev)))
 
 
 def swimba_output_project_backward(dims, y, w_out, dout, dy, dw_out, ws, ws_bytes=None,
                                    stream=None):
+    dev = _device()
     _check(lib().swimba_output_project_backward(
-        ctypes.byref(dims), *_ptrs(y, w_out, dout, dy, dw_out, ws), _ws(ws, ws_bytes),
-        _stream(stream)))
+        ctypes.byref(dims), *_ptrs(dev, y, w_out, dout, dy, dw_out, ws), _ws(ws, ws_bytes),
+        _stream(stream, dev)))

@@ -91,7 +91,8 @@ def norm_tols(src, w, b, want, mean, rstd, dt):
     return ty, ROW * ma[:, 0], tr
 
 
-NORM_SHAPES = [(1, 1), (3, 8), (5, 63), (257, 64), (64, 512), (33, 768), (7, 1000), (9, 2048),
+NORM_SHAPES = [(1, 1), (300, 7), (3, 8), (70, 16), (1029, 24), (130, 100), (67, 128), (18, 129),
+               (40, 384), (5, 63), (257, 64), (64, 512), (33, 768), (7, 1000), (9, 2048),
                (130, 2056), (4, 4100), (3, 8192), (2, 8200), (2, 9001), (2, 32768), (1, 32767)]
 
 
@@ -169,9 +170,10 @@ def test_layer_norm_backward(M, D, dtype, dy_f32):
         if use_res:
             tol = tol + 2 * U * np.abs(keep)
         check("dx", dx, want, tol)
-        # rows of a workgroup one after the other, then 4 row groups, then 512
-        # partial rows as 8 sums of 64 and their join
-        n = M / 512 / (4 if D <= 2048 else 1) + 2 + 4 + 64 + 8
+        # a thread's rows one after the other (64 of M = 16384 at most, with 256
+        # workgroups or more), 4 steps within a wave, 4 waves, then up to 512
+        # partial rows as 32 sums of 16 and their join
+        n = max(4, M / 256) + 2 + 4 + 4 + 16 + 32
         ady = np.abs(host(dy))
         check("dw", dw, wdw, (ady * (exh + n * U * xh)).sum(0))
         if use_res:

@@ -112,7 +112,7 @@ def test_norm_refusals():
     for eps in (-1e-6, float("nan"), float("inf")):
         assert norm(d, eps=eps) == -2
     assert norm(dims(d=32769)) == -3
-    assert norm(dims(batch=1 << 13, seqlen=1 << 14, d=8)) == -2  # 2^27 rows
+    assert norm(dims(batch=1 << 13, seqlen=1 << 13, d=512)) == -2  # 2^26 rows of a wave each
     assert norm(dims(seqlen=0), x=None, w=None, y=None) == 0
     need = sl.layer_workspace_size(d, sl.LAYER_NORM_BACKWARD)
     assert need > 0
@@ -202,12 +202,16 @@ def test_workspace_of_invalid_dims():
 def test_binding_checks_row_strides():
     lib()
     wide = torch.zeros(4, 30)
-    (a, b, c), ld = sl._rows(wide[:, :8], wide[:, 8:16], None)
+    (a, b, c), ld = sl._rows(-1, wide[:, :8], wide[:, 8:16], None)
     assert ld == 30 and b - a == 32 and c is None
     with pytest.raises(ValueError, match="one row stride"):
-        sl._rows(wide[:, :8], torch.zeros(4, 8))
+        sl._rows(-1, wide[:, :8], torch.zeros(4, 8))
     with pytest.raises(ValueError, match="unit stride"):
-        sl._rows(torch.zeros(8, 4).t())
+        sl._rows(-1, torch.zeros(8, 4).t())
+    with pytest.raises(ValueError, match="contiguous"):
+        sl._ptrs(-1, wide[:, :8])
+    with pytest.raises(ValueError, match="current device"):
+        sl._ptrs(0, wide)
     with pytest.raises(ValueError, match="bfloat16 or float32"):
         sl.swimba_layer_norm_backward(dims(), None, None, None, None,
                                       torch.zeros(2, dtype=torch.float16), None, None, None, None,
