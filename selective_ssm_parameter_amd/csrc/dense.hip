@@ -40,6 +40,7 @@ struct Cfg {
   static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
 };
 typedef Cfg<256, 256, 2, 4> Big;
+typedef Cfg<256, 192, 2, 4> Wide;  // not for gated products
 typedef Cfg<128, 128, 2, 2> Mid;
 typedef Cfg<64, 128, 2, 2> Small;   // gated products (32 columns of g and of u per wave)
 typedef Cfg<64, 64, 2, 2> Small64;  // the others
@@ -72,10 +73,53 @@ struct DLay {
   static constexpr int BROWS = BCOL ? kBK : C::BN, BCPR = (BCOL ? C::BN : kBK) / EPC;
   static constexpr int AB = AROWS * ACPR * 16, BB = BROWS * BCPR * 16, STAGE = AB * (SPLIT ? 2 : 1) + BB;
   static constexpr int BOFF = STAGE - BB;  // a (, a_lo), b
-  static constexpr int MA = AB / 1024 / C::NW, MB = BB / 1024 / C::NW;  // copies per wave
+  static constexpr int NA = AB / 1024, NB = BB / 1024;  // copies of 64 chunks
+  static constexpr int MA = (NA + C::NW - 1) / C::NW, MB = (NB + C::NW - 1) / C::NW;  // per wave
   static constexpr int CPW = MA * (SPLIT ? 2 : 1) + MB;
-  static_assert(AB % (1024 * C::NW) == 0 && BB % (1024 * C::NW) == 0, "whole copies per wave");
+  static_assert(AB % 1024 == 0 && BB % 1024 == 0, "whole copies");
 };
+
+// Copy m of a wave among n: where the copies do not divide by the waves, the
+// waves past the last one repeat an earlier copy (the same bytes to the same
+// place), so that every wave waits for the same count.
+template <int NCOPY, int NW>
+__device__ __forceinline__ int copy_of(int m, int wave) {
+  const int i = wave + NW * m;
+  return NCOPY % NW == 0 || i < NCOPY ? i : i - NCOPY;
+}
+
+// XOR swizzle of the 16-byte chunks of a columns tile's row r. Rows of 24
+// chunks keep it within aligned groups of 8.
+template <typename T, int CPR>
+__device__ __forceinline__ int swz_col(int r) {
+  if constexpr (CPR % 16 == 0 || CPR < 16) return swz_tr<T, CPR>(r);
+  else return swz_tr<T, 8>(r);
+}
+// load_kmajor (lds_tiles.hpp) for such a tile
+template <typename T, int CPR>
+__device__ __forceinline__ typename Vec<T>::x8 load_col(const unsigned char* tile, int col0,
+                                                        int lane) {
+  if constexpr (CPR % 16 == 0 || CPR < 16) {
+    return load_kmajor<T, CPR>(tile, 0, col0, lane);
+  } else {
+    static_assert(sizeof(T) == 2, "24 chunks of 8 elements");
+    typedef short s4 __attribute__((__vector_size__(8)));
+    const int g = lane >> 4, c = lane & 15;
+    typename Vec<T>::x8 v;
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const int r = 8 * g + 4 * hh + (c >> 2), col = col0 + 4 * (c & 3);
+      const unsigned char* p =
+          tile + (r * CPR + ((col >> 3) ^ swz_col<T, CPR>(r))) * 16 + 8 * ((col >> 2) & 1);
+      const typename Vec<T>::x4 w4 = __builtin_bit_cast(
+          typename Vec<T>::x4,
+          __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)(p)));
+#pragma unroll
+      for (int m = 0; m < 4; ++m) v[4 * hh + m] = w4[m];
+    }
+    return v;
+  }
+}
 
 __device__ __forceinline__ float sigm(float g) {
   return __builtin_amdgcn_rcpf(1.f + __expf(-g));
@@ -201,10 +245,10 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   }
 #pragma unroll
   for (int m = 0; m < MA; ++m) {
-    const int slot = 64 * (wave + NW * m) + lane;
+    const int slot = 64 * copy_of<L::NA, NW>(m, wave) + lane;
     const int r = slot / L::ACPR, pc = slot % L::ACPR;
     if constexpr (L::ACOL) {
-      const int col = r0 + (pc ^ swz_tr<T, L::ACPR>(r)) * EPC;
+      const int col = r0 + (pc ^ swz_col<T, L::ACPR>(r)) * EPC;
       aoff[m] = col < A.R ? ((uint32_t)r * A.R + col) * ES : kOOB;
       akc[m] = r;
     } else {
@@ -214,10 +258,10 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   }
 #pragma unroll
   for (int m = 0; m < MB; ++m) {
-    const int slot = 64 * (wave + NW * m) + lane;
+    const int slot = 64 * copy_of<L::NB, NW>(m, wave) + lane;
     const int r = slot / L::BCPR, pc = slot % L::BCPR;
     if constexpr (L::BCOL) {
-      const int col = s0 + (pc ^ swz_tr<T, L::BCPR>(r)) * EPC;
+      const int col = s0 + (pc ^ swz_col<T, L::BCPR>(r)) * EPC;
       boff[m] = col < A.S ? ((uint32_t)r * A.S + col) * ES : kOOB;
       bkc[m] = r;
     } else {
@@ -237,19 +281,19 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
     for (int m = 0; m < MA; ++m) {
       const uint32_t off = k0 + akc[m] < K && aoff[m] != kOOB ? aoff[m] + kt * astep : kOOB;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rA, (__attribute__((address_space(3))) void*)(st + 1024 * (wave + NW * m)), 16, off, 0, 0,
-          0);
+          rA, (__attribute__((address_space(3))) void*)(st + 1024 * copy_of<L::NA, NW>(m, wave)), 16,
+          off, 0, 0, 0);
       if constexpr (SPLIT)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rL, (__attribute__((address_space(3))) void*)(st + L::AB + 1024 * (wave + NW * m)), 16,
-            off, 0, 0, 0);
+            rL, (__attribute__((address_space(3))) void*)(st + L::AB + 1024 * copy_of<L::NA, NW>(m, wave)),
+            16, off, 0, 0, 0);
     }
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
       const uint32_t off = k0 + bkc[m] < K && boff[m] != kOOB ? boff[m] + kt * bstep : kOOB;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rB, (__attribute__((address_space(3))) void*)(st + L::BOFF + 1024 * (wave + NW * m)), 16,
-          off, 0, 0, 0);
+          rB, (__attribute__((address_space(3))) void*)(st + L::BOFF + 1024 * copy_of<L::NB, NW>(m, wave)),
+          16, off, 0, 0, 0);
     }
   };
 
@@ -260,7 +304,7 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   auto afrag = [&](const unsigned char* st, int i) -> F {
     const int row = wm * TM * 16 + 16 * i;
     if constexpr (L::ACOL) {
-      return load_kmajor<T, L::ACPR>(st, 0, row, lane);
+      return load_col<T, L::ACPR>(st, row, lane);
     } else {
       const int r = row + c;
       if constexpr (ES == 2)
@@ -272,7 +316,7 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   };
   auto bfrag = [&](const unsigned char* st, int j) -> F {
     if constexpr (L::BCOL) {
-      return load_kmajor<T, L::BCPR>(st + L::BOFF, 0, wn * TN * 16 + 16 * j, lane);
+      return load_col<T, L::BCPR>(st + L::BOFF, wn * TN * 16 + 16 * j, lane);
     } else {
       const int r = wn * TN * 16 + 32 * (j >> 1) + 8 * (c >> 2) + 4 * (j & 1) + (c & 3);
       if constexpr (ES == 2)
@@ -546,35 +590,39 @@ hipError_t go(const char* name, const DenseArgs& A, hipStream_t s) {
 // 64 rows are for products that would leave most CUs without a tile. fp32
 // stages of 256 rows do not fit LDS.
 struct TileCost {
-  int tile, slots;
+  int rows, cols, slots;
   double step, rest;
 };
-constexpr TileCost kBf16Tiles[] = {{256, 256, 0.90, 12}, {128, 512, 0.62, 8}, {64, 1024, 0.40, 5}};
-constexpr TileCost kF32Tiles[] = {{128, 256, 1.8, 8}, {64, 512, 1.0, 5}};
+constexpr TileCost kBf16Tiles[] = {{256, 256, 256, 0.90, 12},
+                                   {256, 192, 256, 0.72, 10},
+                                   {128, 128, 512, 0.62, 8},
+                                   {64, 64, 1024, 0.40, 5}};
+constexpr TileCost kBf16Gated[] = {{256, 256, 256, 0.90, 12},
+                                   {128, 128, 512, 0.62, 8},
+                                   {64, 128, 768, 0.53, 5}};
+constexpr TileCost kF32Tiles[] = {{128, 128, 256, 1.8, 8}, {64, 64, 512, 1.0, 5}};
+constexpr TileCost kF32Gated[] = {{128, 128, 256, 1.8, 8}, {64, 128, 256, 1.0, 5}};
 
 struct Plan {
-  int tile, splits;
+  int tile, splits;  // tile: rows * 1000 + columns
 };
-// cols: columns of the product per column of a tile's width (the gated tile of
-// 64 rows is 128 wide). most: the largest number of k runs; their partial sums
+// most: the largest number of k runs; their partial sums
 // are written, read and summed at about 4 TB/s.
 Plan plan(bool is_bf16, bool split, bool gated, int64_t R, int64_t S, int64_t K, int64_t most) {
-  Plan best{64, 1};
+  Plan best{0, 1};
   double tbest = 1e30;
-  const TileCost* c = is_bf16 ? kBf16Tiles : kF32Tiles;
-  const int nt = is_bf16 ? 3 : 2;
+  const TileCost* c = is_bf16 ? (gated ? kBf16Gated : kBf16Tiles) : (gated ? kF32Gated : kF32Tiles);
+  const int nt = is_bf16 ? (gated ? 3 : 4) : 2;
   const double steps = (double)((K + kBK - 1) / kBK) * (split ? 1.9 : 1.0);
   for (int i = 0; i < nt; ++i) {
-    const int64_t tr = c[i].tile, ts = gated && tr == 64 ? 128 : tr;
-    const int64_t units = (R + tr - 1) / tr * ((S + ts - 1) / ts);
+    const int64_t units = (R + c[i].rows - 1) / c[i].rows * ((S + c[i].cols - 1) / c[i].cols);
     for (int64_t n = 1; n <= most; ++n) {
-      const int64_t slots = ts != tr ? c[i].slots * 3 / 4 : c[i].slots;
-      const double rounds = (double)((units * n + slots - 1) / slots);
+      const double rounds = (double)((units * n + c[i].slots - 1) / c[i].slots);
       double t = rounds * (steps / n * c[i].step + c[i].rest);
       if (n > 1) t += 4 + (double)(n + 1) * R * S * 4e-6 / 4;
       if (t < tbest) {
         tbest = t;
-        best = Plan{(int)tr, (int)n};
+        best = Plan{c[i].rows * 1000 + c[i].cols, (int)n};
       }
       if (units * n > 4 * c[i].slots) break;  // more runs only add partial sums
     }
@@ -598,8 +646,8 @@ template <typename T, Mode MODE>
 hipError_t go_gated(const char* name, const DenseArgs& A, hipStream_t s) {
   const int tile = plan(sizeof(T) == 2, false, true, A.R, 2 * (int64_t)A.S, A.K, 1).tile;
   if constexpr (sizeof(T) == 2)
-    if (tile == 256) return go<T, Big, MODE, T>(name, A, s);
-  if (tile == 128) return go<T, Mid, MODE, T>(name, A, s);
+    if (tile == 256256) return go<T, Big, MODE, T>(name, A, s);
+  if (tile == 128128) return go<T, Mid, MODE, T>(name, A, s);
   return go<T, Small, MODE, T>(name, A, s);
 }
 
@@ -621,9 +669,11 @@ hipError_t go_skinny(const DenseArgs& A, hipStream_t s) {
 
 template <typename T, Mode MODE, typename TO, bool SPLIT>
 hipError_t go_tile(int tile, const char* name, const DenseArgs& A, hipStream_t s) {
-  if constexpr (sizeof(T) == 2)
-    if (tile == 256) return go<T, Big, MODE, TO, SPLIT>(name, A, s);
-  if (tile == 128) return go<T, Mid, MODE, TO, SPLIT>(name, A, s);
+  if constexpr (sizeof(T) == 2) {
+    if (tile == 256256) return go<T, Big, MODE, TO, SPLIT>(name, A, s);
+    if (tile == 256192) return go<T, Wide, MODE, TO, SPLIT>(name, A, s);
+  }
+  if (tile == 128128) return go<T, Mid, MODE, TO, SPLIT>(name, A, s);
   return go<T, Small64, MODE, TO, SPLIT>(name, A, s);
 }
 

@@ -277,22 +277,22 @@ __device__ __forceinline__ BufRes chunk_buffer(const void* t, size_t row, int64_
 
 // ---------------------------------------------------------------- forward
 
-template <typename T, bool CHAIN, bool GATED>
-__global__ __launch_bounds__(kTh) void gscan_kernel(GScanArgs A) {
+// FULL: all of the chunk's tokens are in use (no selects on the token).
+template <typename T, bool CHAIN, bool GATED, bool FULL>
+__device__ __forceinline__ void gscan_chunk(const GScanArgs& A, const Place& p, Shared& sh) {
   constexpr uint32_t ES = sizeof(T);
-  __shared__ Shared sh;
-  const Place p = take_place<false, CHAIN>(A, sh);
-  const int t1 = p.chunk * kChunk, rows = min(kChunk, A.T - t1);  // the chunk's rows
+  const int t1 = p.chunk * kChunk;
+  const int rows = FULL ? kChunk : min(kChunk, A.T - t1);  // the chunk's rows
   const size_t row = (size_t)p.b * A.T + t1;
   const int w0 = p.t0 - t1;                          // this thread's first row
-  const int live = min(max(p.len - p.t0, 0), kTpt);  // its tokens in use
+  const int live = FULL ? kTpt : min(max(p.len - p.t0, 0), kTpt);  // its tokens in use
   const BufRes rx = chunk_buffer<T>(A.x, row, A.ld, rows, A.C);
   const BufRes rf = chunk_buffer<T>(A.f, row, A.ld, rows, A.C);
   const BufRes ro = chunk_buffer<T>(GATED ? A.o : A.x, row, A.ld, rows, A.C);
   const BufRes ry = chunk_buffer<T>(A.y, row, A.C, rows, A.C);
   const uint32_t pitch = (uint32_t)A.ld * ES, ypitch = A.C * ES;
   const uint32_t col = p.on ? p.c * ES : kOOB;
-  if (p.dead) {
+  if (!FULL && p.dead) {
 #pragma unroll
     for (int i = 0; i < kTpt; ++i)
       store_one<T>(ry, w0 + i < rows ? col : kOOB, (w0 + i) * ypitch, 0.f);
@@ -310,8 +310,9 @@ __global__ __launch_bounds__(kTh) void gscan_kernel(GScanArgs A) {
   Run own = identity();
 #pragma unroll
   for (int i = 0; i < kTpt; ++i) {
-    // past the length: f = 1 (and x reads as 0)
-    k[i] = i < live ? gate_of(value<T>(fr[i])) : 0.f;
+    // past the length: f = 1 (the logit and x read as 0)
+    k[i] = gate_of(value<T>(fr[i]));
+    if constexpr (!FULL) k[i] *= i < live ? 1.f : 0.f;
     extend(own, k[i]);
     own.S = step(k[i], value<T>(xr[i]), own.S);
   }
@@ -332,20 +333,26 @@ __global__ __launch_bounds__(kTh) void gscan_kernel(GScanArgs A) {
   }
 }
 
+template <typename T, bool CHAIN, bool GATED>
+__global__ __launch_bounds__(kTh) void gscan_kernel(GScanArgs A) {
+  __shared__ Shared sh;
+  const Place p = take_place<false, CHAIN>(A, sh);
+  if ((p.chunk + 1) * (int64_t)kChunk <= p.len) gscan_chunk<T, CHAIN, GATED, true>(A, p, sh);
+  else gscan_chunk<T, CHAIN, GATED, false>(A, p, sh);
+}
+
 // ---------------------------------------------------------------- backward
 
 // Walking back, c = f_t e_t is the gradient that leaves token t for the state
 // before it: c <- f (u + c), u = dy silu(gate). The states come from the
 // forward's carry and the runs of the chunk's waves.
-template <typename T, bool CHAIN, bool GATED>
-__global__ __launch_bounds__(kTh) void gscan_bwd_kernel(GScanArgs A) {
+template <typename T, bool CHAIN, bool GATED, bool FULL>
+__device__ __forceinline__ void gscan_bwd_chunk(const GScanArgs& A, const Place& p, Shared& sh) {
   constexpr uint32_t ES = sizeof(T);
-  __shared__ Shared sh;
-  const Place p = take_place<true, CHAIN>(A, sh);
-  const int t1 = p.chunk * kChunk, rows = min(kChunk, A.T - t1);
+  const int t1 = p.chunk * kChunk, rows = FULL ? kChunk : min(kChunk, A.T - t1);
   const size_t row = (size_t)p.b * A.T + t1;
   const int w0 = p.t0 - t1;
-  const int live = min(max(p.len - p.t0, 0), kTpt);
+  const int live = FULL ? kTpt : min(max(p.len - p.t0, 0), kTpt);
   const BufRes rx = chunk_buffer<T>(A.x, row, A.ld, rows, A.C);
   const BufRes rf = chunk_buffer<T>(A.f, row, A.ld, rows, A.C);
   const BufRes ro = chunk_buffer<T>(GATED ? A.o : A.x, row, A.ld, rows, A.C);
@@ -355,7 +362,7 @@ __global__ __launch_bounds__(kTh) void gscan_bwd_kernel(GScanArgs A) {
   const BufRes so = chunk_buffer<T>(GATED ? A.d_o : A.dx, row, A.ldd, rows, A.C);
   const uint32_t pitch = (uint32_t)A.ld * ES, dpitch = (uint32_t)A.ldd * ES;
   const uint32_t col = p.on ? p.c * ES : kOOB;
-  if (p.dead) {
+  if (!FULL && p.dead) {
 #pragma unroll
     for (int i = 0; i < kTpt; ++i) {
       const uint32_t off = w0 + i < rows ? col : kOOB, r = (w0 + i) * dpitch;
@@ -378,7 +385,8 @@ __global__ __launch_bounds__(kTh) void gscan_bwd_kernel(GScanArgs A) {
   Run fw = identity();
 #pragma unroll
   for (int i = 0; i < kTpt; ++i) {
-    k[i] = i < live ? gate_of(value<T>(fr[i])) : 0.f;
+    k[i] = gate_of(value<T>(fr[i]));
+    if constexpr (!FULL) k[i] *= i < live ? 1.f : 0.f;
     e[i] = value<T>(dr[i]);
     if constexpr (GATED) {
       const float ov = value<T>(gr[i]);
@@ -418,6 +426,14 @@ __global__ __launch_bounds__(kTh) void gscan_bwd_kernel(GScanArgs A) {
       store_one<T>(so, off, r, in ? vo : 0.f);
     }
   }
+}
+
+template <typename T, bool CHAIN, bool GATED>
+__global__ __launch_bounds__(kTh, 4) void gscan_bwd_kernel(GScanArgs A) {
+  __shared__ Shared sh;
+  const Place p = take_place<true, CHAIN>(A, sh);
+  if ((p.chunk + 1) * (int64_t)kChunk <= p.len) gscan_bwd_chunk<T, CHAIN, GATED, true>(A, p, sh);
+  else gscan_bwd_chunk<T, CHAIN, GATED, false>(A, p, sh);
 }
 
 // The workspace before a chained kernel: nothing published.

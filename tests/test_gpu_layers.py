@@ -435,7 +435,7 @@ GEMM_SHAPES = [(1, 8, 8), (17, 2056, 40), (33, 264, 520), (64, 1032, 200), (65, 
                (129, 136, 72), (300, 520, 200), (1000, 64, 1032), (2049, 104, 136),
                (4100, 40, 264)]
 # shapes whose products take the 256-row tile
-BIG_SHAPES = [(6200, 512, 1032), (12400, 1032, 64)]
+BIG_SHAPES = [(6200, 512, 1032), (12400, 1032, 64), (16300, 744, 32), (8192, 384, 192)]
 
 
 @pytest.mark.parametrize("M,D,F", GEMM_SHAPES + BIG_SHAPES)
