@@ -88,36 +88,66 @@ __device__ __forceinline__ int copy_of(int m, int wave) {
   return NCOPY % NW == 0 || i < NCOPY ? i : i - NCOPY;
 }
 
-// XOR swizzle of the 16-byte chunks of a columns tile's row r. Rows of 24
-// chunks keep it within aligned groups of 8.
+// Fragments from LDS. The contraction index of element e in lane group g is
+// 8 g + e for 2-byte types and 4 g + e % 4 + 16 (e / 4) for fp32, for rows and
+// columns tiles alike.
+//
+// Rows tiles: chunk ch of row r lies at ch ^ swz_rows(r).
 template <typename T, int CPR>
-__device__ __forceinline__ int swz_col(int r) {
-  if constexpr (CPR % 16 == 0 || CPR < 16) return swz_tr<T, CPR>(r);
+__device__ __forceinline__ int swz_rows(int r) {
+  if constexpr (sizeof(T) == 2) return swz_row<T, CPR>(r);
+  else return r & 7;  // 8 chunks a row: 8 lanes reading one chunk of 8 rows take all of them
+}
+template <typename T, int CPR>
+__device__ __forceinline__ typename Vec<T>::x8 load_row(const unsigned char* tile, int r, int g) {
+  const unsigned char* row = tile + r * CPR * 16;
+  const int x = swz_rows<T, CPR>(r);
+  if constexpr (sizeof(T) == 2)
+    return load8<T>(reinterpret_cast<const T*>(row + 16 * (g ^ x)));
+  else
+    return load4x2<T>(reinterpret_cast<const T*>(row + 16 * (g ^ x)),
+                      reinterpret_cast<const T*>(row + 16 * ((g + 4) ^ x)));
+}
+// Columns tiles ([k][column]), 2-byte types: transposing reads, chunks swizzled
+// as swz_tr; rows of 24 chunks keep the swizzle within aligned groups of 8.
+// fp32 tiles are not swizzled: a lane reads N neighbouring columns of a row at
+// once, one for each of N matrix-core tiles, whose columns are then N apart
+// (tile n, index m: column col0 + N m + n).
+template <typename T, int CPR>
+__device__ __forceinline__ int swz_cols(int r) {
+  if constexpr (sizeof(T) == 4) return 0;
+  else if constexpr (CPR % 16 == 0 || CPR < 16) return swz_tr<T, CPR>(r);
   else return swz_tr<T, 8>(r);
 }
-// load_kmajor (lds_tiles.hpp) for such a tile
-template <typename T, int CPR>
-__device__ __forceinline__ typename Vec<T>::x8 load_col(const unsigned char* tile, int col0,
-                                                        int lane) {
-  if constexpr (CPR % 16 == 0 || CPR < 16) {
-    return load_kmajor<T, CPR>(tile, 0, col0, lane);
-  } else {
-    static_assert(sizeof(T) == 2, "24 chunks of 8 elements");
+template <typename T, int CPR, int N>
+__device__ __forceinline__ void load_cols(const unsigned char* tile, int col0, int lane,
+                                          typename Vec<T>::x8 (&f)[N]) {
+  const int g = lane >> 4, c = lane & 15;
+  if constexpr (sizeof(T) == 2) {
     typedef short s4 __attribute__((__vector_size__(8)));
-    const int g = lane >> 4, c = lane & 15;
-    typename Vec<T>::x8 v;
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const int r = 8 * g + 4 * hh + (c >> 2), col = col0 + 4 * (c & 3);
-      const unsigned char* p =
-          tile + (r * CPR + ((col >> 3) ^ swz_col<T, CPR>(r))) * 16 + 8 * ((col >> 2) & 1);
-      const typename Vec<T>::x4 w4 = __builtin_bit_cast(
-          typename Vec<T>::x4,
-          __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)(p)));
+    for (int n = 0; n < N; ++n) {
 #pragma unroll
-      for (int m = 0; m < 4; ++m) v[4 * hh + m] = w4[m];
+      for (int hh = 0; hh < 2; ++hh) {
+        const int r = 8 * g + 4 * hh + (c >> 2), col = col0 + 16 * n + 4 * (c & 3);
+        const unsigned char* p =
+            tile + (r * CPR + ((col >> 3) ^ swz_cols<T, CPR>(r))) * 16 + 8 * ((col >> 2) & 1);
+        const typename Vec<T>::x4 w4 = __builtin_bit_cast(
+            typename Vec<T>::x4,
+            __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)(p)));
+#pragma unroll
+        for (int m = 0; m < 4; ++m) f[n][4 * hh + m] = w4[m];
+      }
     }
-    return v;
+  } else {
+    typedef float FN __attribute__((ext_vector_type(N)));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int k = 4 * g + (e & 3) + 16 * (e >> 2);
+      const FN v = *reinterpret_cast<const FN*>(tile + k * CPR * 16 + (col0 + N * c) * 4);
+#pragma unroll
+      for (int n = 0; n < N; ++n) f[n][e] = v[n];
+    }
   }
 }
 
@@ -248,11 +278,11 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
     const int slot = 64 * copy_of<L::NA, NW>(m, wave) + lane;
     const int r = slot / L::ACPR, pc = slot % L::ACPR;
     if constexpr (L::ACOL) {
-      const int col = r0 + (pc ^ swz_col<T, L::ACPR>(r)) * EPC;
+      const int col = r0 + (pc ^ swz_cols<T, L::ACPR>(r)) * EPC;
       aoff[m] = col < A.R ? ((uint32_t)r * A.R + col) * ES : kOOB;
       akc[m] = r;
     } else {
-      akc[m] = (pc ^ swz_row<T, L::ACPR>(r)) * EPC;
+      akc[m] = (pc ^ swz_rows<T, L::ACPR>(r)) * EPC;
       aoff[m] = r < nrows ? ((uint32_t)r * A.K + akc[m]) * ES : kOOB;
     }
   }
@@ -261,13 +291,13 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
     const int slot = 64 * copy_of<L::NB, NW>(m, wave) + lane;
     const int r = slot / L::BCPR, pc = slot % L::BCPR;
     if constexpr (L::BCOL) {
-      const int col = s0 + (pc ^ swz_col<T, L::BCPR>(r)) * EPC;
+      const int col = s0 + (pc ^ swz_cols<T, L::BCPR>(r)) * EPC;
       boff[m] = col < A.S ? ((uint32_t)r * A.S + col) * ES : kOOB;
       bkc[m] = r;
     } else {
       // 64 tile rows are 32 columns of g and the same 32 of u
       const int col = s0 + (r >> 6) * 32 + (r & 31);
-      bkc[m] = (pc ^ swz_row<T, L::BCPR>(r)) * EPC;
+      bkc[m] = (pc ^ swz_rows<T, L::BCPR>(r)) * EPC;
       boff[m] = col < A.S
                     ? ((uint32_t)(((r >> 5) & 1 ? A.S : 0) + col) * A.K + bkc[m]) * ES
                     : kOOB;
@@ -297,33 +327,29 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
     }
   };
 
-  // ---- fragments. acc[i][j] holds, in lane (g, c), row 16 i + c and columns
-  // 16 j + 4 g .. + 3 of this wave's block (b is the matrix cores' A operand);
-  // the gated tile's columns are permuted within pairs of tiles so that a
-  // lane's 8 values of a pair are consecutive columns 8 g .. 8 g + 7.
-  auto afrag = [&](const unsigned char* st, int i) -> F {
-    const int row = wm * TM * 16 + 16 * i;
+  // ---- fragments. acc[i][j] holds, in lane (g, c), index c of row tile i and
+  // indexes 4 g .. + 3 of column tile j of this wave's block (b is the matrix
+  // cores' A operand). The gated tile's columns are permuted within pairs of
+  // tiles so that a lane's 8 values of a pair are consecutive columns
+  // 8 g .. 8 g + 7.
+  auto load_a = [&](const unsigned char* st, F (&f)[TM]) __attribute__((always_inline)) {
+    const int row = wm * TM * 16;
     if constexpr (L::ACOL) {
-      return load_col<T, L::ACPR>(st, row, lane);
+      load_cols<T, L::ACPR, TM>(st, row, lane, f);
     } else {
-      const int r = row + c;
-      if constexpr (ES == 2)
-        return load8<T>(reinterpret_cast<const T*>(
-            st + (r * L::ACPR + (g ^ swz_row<T, L::ACPR>(r))) * 16));
-      else
-        return load8<T>(reinterpret_cast<const T*>(st + r * L::ACPR * 16 + 32 * g));
+#pragma unroll
+      for (int i = 0; i < TM; ++i) f[i] = load_row<T, L::ACPR>(st, row + 16 * i + c, g);
     }
   };
-  auto bfrag = [&](const unsigned char* st, int j) -> F {
+  auto load_b = [&](const unsigned char* st, F (&f)[TN]) __attribute__((always_inline)) {
+    const int col = wn * TN * 16;
     if constexpr (L::BCOL) {
-      return load_col<T, L::BCPR>(st + L::BOFF, wn * TN * 16 + 16 * j, lane);
+      load_cols<T, L::BCPR, TN>(st + L::BOFF, col, lane, f);
     } else {
-      const int r = wn * TN * 16 + 32 * (j >> 1) + 8 * (c >> 2) + 4 * (j & 1) + (c & 3);
-      if constexpr (ES == 2)
-        return load8<T>(reinterpret_cast<const T*>(
-            st + L::BOFF + (r * L::BCPR + (g ^ swz_row<T, L::BCPR>(r))) * 16));
-      else
-        return load8<T>(reinterpret_cast<const T*>(st + L::BOFF + r * L::BCPR * 16 + 32 * g));
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        f[j] = load_row<T, L::BCPR>(
+            st + L::BOFF, col + 32 * (j >> 1) + 8 * (c >> 2) + 4 * (j & 1) + (c & 3), g);
     }
   };
 
@@ -332,19 +358,33 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+  // DEFER (the gated products on the largest tile): the products of a step's
+  // last row of fragments are issued after the reads of the next step (past its
+  // barrier), so that they cover the wait for those reads: 1 to 3 %.
+  constexpr bool DEFER = is_gated(MODE) && TM == 8;
+  F bd[DEFER ? TN : 1], ad = zero8<T>();
+  if constexpr (DEFER) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) bd[j] = zero8<T>();
+  }
   auto compute = [&](const unsigned char* st) {
     F bf[TN], af[TM];
+    load_b(st, bf);
+    load_a(st, af);
+    if constexpr (DEFER) {
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) bf[j] = bfrag(st, j);
+      for (int j = 0; j < TN; ++j) acc[TM - 1][j] = mma16(bd[j], ad, acc[TM - 1][j]);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) af[i] = afrag(st, i);
+      for (int j = 0; j < TN; ++j) bd[j] = bf[j];
+      ad = af[TM - 1];
+    }
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < (DEFER ? TM - 1 : TM); ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = mma16(bf[j], af[i], acc[i][j]);
     if constexpr (SPLIT) {
-#pragma unroll
-      for (int i = 0; i < TM; ++i) af[i] = afrag(st + L::AB, i);
+      load_a(st + L::AB, af);
 #pragma unroll
       for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -377,6 +417,10 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
       iter(kt + 1, stg1, stg0);
       iter(kt + 2, stg2, stg1);
     }
+  }
+  if constexpr (DEFER) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[TM - 1][j] = mma16(bd[j], ad, acc[TM - 1][j]);
   }
   wait_vm<0>();  // the copies past the end land before the workgroup's LDS is released
 
@@ -438,19 +482,35 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
       }
     }
   } else {
-    typedef typename Vec<TO>::x4 O4;
     TO* out = static_cast<TO*>(A.out) + (MODE == kTN ? (size_t)split * A.R * A.S : 0);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      const int r = wm * TM * 16 + 16 * i + c;
+      const int r = wm * TM * 16 + (ES == 4 && L::ACOL ? TM * c + i : 16 * i + c);
+      if (r >= nrows) continue;
+      TO* row = out + (size_t)(r0 + r) * A.S;
+      if constexpr (ES == 4) {
+        // index 4 g + q of the TN tiles: TN consecutive columns
+        typedef TO ON __attribute__((ext_vector_type(TN)));
 #pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const int col = s0 + wn * TN * 16 + 16 * j + 4 * g;
-        if (r >= nrows || col >= A.S) continue;
-        O4 o;
+        for (int q = 0; q < 4; ++q) {
+          const int col = s0 + wn * TN * 16 + TN * (4 * g + q);
+          if (col >= A.S) continue;
+          ON o;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = from_f32<TO>(acc[i][j][q]);
-        *reinterpret_cast<O4*>(out + (size_t)(r0 + r) * A.S + col) = o;
+          for (int j = 0; j < TN; ++j) o[j] = from_f32<TO>(acc[i][j][q]);
+          *reinterpret_cast<ON*>(row + col) = o;
+        }
+      } else {
+        typedef typename Vec<TO>::x4 O4;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const int col = s0 + wn * TN * 16 + 16 * j + 4 * g;
+          if (col >= A.S) continue;
+          O4 o;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) o[q] = from_f32<TO>(acc[i][j][q]);
+          *reinterpret_cast<O4*>(row + col) = o;
+        }
       }
     }
   }
