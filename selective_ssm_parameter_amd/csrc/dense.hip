@@ -57,7 +57,8 @@ struct DenseArgs {
   const void* dh;    // kGatedBwd
   int R, S, K;       // gated: S = F, the columns of h
   int act;
-  int splits;     // kTN: k is cut into this many runs of ksplit rows
+  int splits;     // kNN, kTN: k is cut into this many runs of ksplit, their
+                  // partial products [splits][R][S] float32 in out
   int ksplit;
 };
 
@@ -66,7 +67,9 @@ constexpr int kBK = 32;
 template <typename T, class C, Mode MODE, bool SPLIT>
 struct DLay {
   static constexpr int ES = sizeof(T), EPC = 16 / ES;
-  static constexpr int NS = SPLIT ? 3 : 4;
+  // (fp32 128 x 128 gated tiles: two stages, so that two workgroups share a CU,
+  // 114 against 90 TFLOP/s at 12000 x 320 x 512; no gain for columns tiles)
+  static constexpr int NS = SPLIT ? 3 : (is_gated(MODE) && ES == 4 && C::BM == 128 ? 2 : 4);
   static constexpr bool ACOL = MODE == kTN, BCOL = !is_gated(MODE);
   // tile in LDS: rows of CPR 16-byte chunks
   static constexpr int AROWS = ACOL ? kBK : C::BM, ACPR = (ACOL ? C::BM : kBK) / EPC;
@@ -223,12 +226,12 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   // an array per stage: copies into one are known not to touch the others
   __shared__ __align__(16) unsigned char stg0[L::STAGE];
   __shared__ __align__(16) unsigned char stg1[L::STAGE];
-  __shared__ __align__(16) unsigned char stg2[L::STAGE];
-  __shared__ __align__(16) unsigned char stg3[L::NS == 4 ? L::STAGE : 16];
+  __shared__ __align__(16) unsigned char stg2[L::NS > 2 ? L::STAGE : 16];
+  __shared__ __align__(16) unsigned char stg3[L::NS > 3 ? L::STAGE : 16];
 
   const int nr = (A.R + BM - 1) / BM, nc = (A.S + SN - 1) / SN;
   int tr, tc, split = 0;
-  if constexpr (MODE == kTN) {
+  if constexpr (!is_gated(MODE)) {
     // the splits of one unit follow each other
     if (!unit_of(nr, nc * A.splits, tr, tc)) return;
     split = tc % A.splits;
@@ -238,8 +241,8 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   }
   const int r0 = tr * BM, s0 = tc * SN;
   const int nrows = min(BM, A.R - r0);
-  const int kbeg = MODE == kTN ? split * A.ksplit : 0;
-  const int K = MODE == kTN ? min(A.ksplit, A.K - kbeg) : A.K;
+  const int kbeg = split * A.ksplit;
+  const int K = is_gated(MODE) ? A.K : min(A.ksplit, A.K - kbeg);
 
   const int lane = lane_id(), g = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -262,8 +265,9 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
     if constexpr (SPLIT) rL = make_rsrc(lp + (size_t)kbeg * A.R, (uint64_t)K * A.R * ES);
     astep = kBK * (uint32_t)A.R * ES;
   } else {
-    rA = make_rsrc(ap + (size_t)r0 * A.K, (uint64_t)nrows * A.K * ES);
-    if constexpr (SPLIT) rL = make_rsrc(lp + (size_t)r0 * A.K, (uint64_t)nrows * A.K * ES);
+    const uint64_t bytes = ((uint64_t)nrows * A.K - kbeg) * ES;
+    rA = make_rsrc(ap + (size_t)r0 * A.K + kbeg, bytes);
+    if constexpr (SPLIT) rL = make_rsrc(lp + (size_t)r0 * A.K + kbeg, bytes);
     astep = kBK * ES;
   }
   if constexpr (L::BCOL) {
@@ -402,8 +406,13 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
     compute(cur);
   };
   fetch(stg0, 0);
-  fetch(stg1, 1);
-  if constexpr (L::NS == 4) {
+  if constexpr (L::NS > 2) fetch(stg1, 1);
+  if constexpr (L::NS == 2) {
+    for (int kt = 0; kt < nks; kt += 2) {
+      iter(kt, stg0, stg1);
+      iter(kt + 1, stg1, stg0);
+    }
+  } else if constexpr (L::NS == 4) {
     fetch(stg2, 2);
     for (int kt = 0; kt < nks; kt += 4) {
       iter(kt, stg0, stg3);
@@ -482,7 +491,7 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
       }
     }
   } else {
-    TO* out = static_cast<TO*>(A.out) + (MODE == kTN ? (size_t)split * A.R * A.S : 0);
+    TO* out = static_cast<TO*>(A.out) + (size_t)split * A.R * A.S;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       const int r = wm * TM * 16 + (ES == 4 && L::ACOL ? TM * c + i : 16 * i + c);
@@ -621,12 +630,16 @@ __global__ __launch_bounds__(64 * KW) void gated_skinny_kernel(DenseArgs A) {
 }
 
 // out = the splits' partial products added in split order.
+template <typename TO>
 __global__ __launch_bounds__(256) void dense_sum_kernel(const float* __restrict__ part, int splits,
-                                                        size_t n4, float* __restrict__ out) {
+                                                        size_t n4, TO* __restrict__ out) {
   for (size_t q = (size_t)blockIdx.x * 256 + threadIdx.x; q < n4; q += (size_t)gridDim.x * 256) {
     floatx4 s = reinterpret_cast<const floatx4*>(part)[q];
     for (int p = 1; p < splits; ++p) s = s + reinterpret_cast<const floatx4*>(part)[p * n4 + q];
-    reinterpret_cast<floatx4*>(out)[q] = s;
+    typename Vec<TO>::x4 o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = from_f32<TO>(s[j]);
+    reinterpret_cast<typename Vec<TO>::x4*>(out)[q] = o;
   }
 }
 
@@ -634,7 +647,7 @@ template <typename T, class C, Mode MODE, typename TO, bool SPLIT = false>
 hipError_t go(const char* name, const DenseArgs& A, hipStream_t s) {
   constexpr int SN = is_gated(MODE) ? C::BN / 2 : C::BN;
   const int64_t units = (int64_t)((A.R + C::BM - 1) / C::BM) * ((A.S + SN - 1) / SN) *
-                        (MODE == kTN ? A.splits : 1);
+                        (is_gated(MODE) ? 1 : A.splits);
   hipEvent_t e0, e1;
   prof_kernel(name, &e0, &e1);
   hipExtLaunchKernelGGL((dense_kernel<T, C, MODE, TO, SPLIT>),
@@ -661,7 +674,7 @@ constexpr TileCost kBf16Gated[] = {{256, 256, 256, 0.90, 12},
                                    {128, 128, 512, 0.62, 8},
                                    {64, 128, 768, 0.53, 5}};
 constexpr TileCost kF32Tiles[] = {{128, 128, 256, 1.8, 8}, {64, 64, 512, 1.0, 5}};
-constexpr TileCost kF32Gated[] = {{128, 128, 256, 1.8, 8}, {64, 128, 256, 1.0, 5}};
+constexpr TileCost kF32Gated[] = {{128, 128, 512, 3.4, 8}, {64, 128, 256, 1.0, 5}};
 
 struct Plan {
   int tile, splits;  // tile: rows * 1000 + columns
@@ -690,16 +703,24 @@ Plan plan(bool is_bf16, bool split, bool gated, int64_t R, int64_t S, int64_t K,
   return best;
 }
 
-// The k runs of a weight gradient: at least 256 tokens each, 64 at most, and
-// every run's operand rows below 2 GiB.
-void tn_plan(bool is_bf16, bool split, int M, int R, int S, int& tile, int& splits, int& ksplit) {
-  const Plan p = plan(is_bf16, split, false, R, S, M,
-                      std::max<int64_t>(1, std::min<int64_t>(64, M / 256)));
-  tile = p.tile;
-  const int64_t row = (int64_t)(R > S ? R : S) * (is_bf16 ? 2 : 4);
-  const int64_t n = std::max<int64_t>(p.splits, (M * row + (int64_t(1) << 30) - 1) >> 30);
-  ksplit = (int)(((M + n - 1) / n + kBK - 1) / kBK * kBK);
-  splits = (M + ksplit - 1) / ksplit;
+// The k runs of a product, at least 256 long and 64 at most (for few tokens, or
+// a weight gradient of many tokens and few columns). Of a weight gradient every
+// run's operand rows also stay below 2 GiB.
+struct Runs {
+  int tile, splits, ksplit;
+};
+Runs runs_of(bool is_bf16, bool split, bool tn, int R, int S, int K) {
+  const Plan p = plan(is_bf16, split, false, R, S, K,
+                      std::max<int64_t>(1, std::min<int64_t>(64, K / 256)));
+  int64_t n = p.splits;
+  if (tn) {
+    const int64_t row = (int64_t)(R > S ? R : S) * (is_bf16 ? 2 : 4);
+    n = std::max<int64_t>(n, (K * row + (int64_t(1) << 30) - 1) >> 30);
+  }
+  Runs r{p.tile, 1, 0};
+  r.ksplit = (int)(((K + n - 1) / n + kBK - 1) / kBK * kBK);
+  r.splits = (K + r.ksplit - 1) / r.ksplit;
+  return r;
 }
 
 template <typename T, Mode MODE>
@@ -718,12 +739,18 @@ hipError_t go_skinny(const DenseArgs& A, hipStream_t s) {
   const int units = (A.S + 15) / 16;
   hipEvent_t e0, e1;
   prof_kernel("gated_project", &e0, &e1);
-  if (units >= 192 || MT == 4)
-    hipExtLaunchKernelGGL((gated_skinny_kernel<T, MT, 4>), dim3((unsigned)units), dim3(256), 0, s,
-                          e0, e1, 0, A);
-  else
-    hipExtLaunchKernelGGL((gated_skinny_kernel<T, MT, 8>), dim3((unsigned)units), dim3(512), 0, s,
-                          e0, e1, 0, A);
+  auto run = [&](auto kw) {
+    constexpr int KW = decltype(kw)::value;
+    hipExtLaunchKernelGGL((gated_skinny_kernel<T, MT, KW>), dim3((unsigned)units), dim3(64 * KW),
+                          0, s, e0, e1, 0, A);
+  };
+  // (8 waves leave 256 registers each, which more tiles of tokens do not fit)
+  if constexpr (MT == 1) {
+    if (units < 192) run(std::integral_constant<int, 8>());
+    else run(std::integral_constant<int, 4>());
+  } else {
+    run(std::integral_constant<int, 4>());
+  }
   return hipGetLastError();
 }
 
@@ -762,41 +789,58 @@ hipError_t launch_gated_dz(bool is_bf16, int M, int D, int F, int act, const voi
                  : go_gated<float, kGatedBwd>("gated_dz", A, s);
 }
 
-hipError_t launch_dense_nn(bool is_bf16, const char* name, int M, int K, int S, const void* a,
-                           const void* a_lo, const void* b, void* out, hipStream_t s) {
-  DenseArgs A{};
-  A.a = a; A.a_lo = a_lo; A.b = b; A.out = out; A.R = M; A.S = S; A.K = K;
-  const int tile = plan(is_bf16, a_lo != nullptr, false, M, S, K, 1).tile;
-  if (!is_bf16) return go_tile<float, kNN, float, false>(tile, name, A, s);
-  return a_lo ? go_tile<bf16, kNN, float, true>(tile, name, A, s)
-              : go_tile<bf16, kNN, bf16, false>(tile, name, A, s);
+size_t dense_ws_bytes(bool is_bf16, bool split, bool tn, int R, int S, int K) {
+  const Runs r = runs_of(is_bf16, split, tn, R, S, K);
+  return r.splits > 1 ? sizeof(float) * (size_t)r.splits * R * S : 0;
 }
 
-size_t dense_tn_ws_bytes(bool is_bf16, bool split, int M, int R, int S) {
-  int tile, splits, ksplit;
-  tn_plan(is_bf16, split, M, R, S, tile, splits, ksplit);
-  return splits > 1 ? sizeof(float) * (size_t)splits * R * S : 0;
+namespace {
+
+// The sum of a product's k runs (in ws) to out.
+template <typename TO>
+hipError_t sum_runs(const DenseArgs& A, const void* ws, void* out, hipStream_t s) {
+  hipEvent_t e0, e1;
+  prof_kernel("dense_sum", &e0, &e1);
+  const size_t n4 = (size_t)A.R * A.S / 4;
+  const unsigned blocks = (unsigned)std::min<size_t>((n4 + 255) / 256, 4096);
+  hipExtLaunchKernelGGL(dense_sum_kernel<TO>, dim3(blocks), dim3(256), 0, s, e0, e1, 0,
+                        (const float*)ws, A.splits, n4, (TO*)out);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_dense_nn(bool is_bf16, const char* name, int M, int K, int S, const void* a,
+                           const void* a_lo, const void* b, void* out, void* ws, hipStream_t s) {
+  DenseArgs A{};
+  A.a = a; A.a_lo = a_lo; A.b = b; A.R = M; A.S = S; A.K = K;
+  const Runs r = runs_of(is_bf16, a_lo != nullptr, false, M, S, K);
+  A.splits = r.splits;
+  A.ksplit = r.ksplit;
+  A.out = r.splits > 1 ? ws : out;
+  hipError_t e;
+  if (!is_bf16) e = go_tile<float, kNN, float, false>(r.tile, name, A, s);
+  else if (a_lo) e = go_tile<bf16, kNN, float, true>(r.tile, name, A, s);
+  else if (r.splits > 1) e = go_tile<bf16, kNN, float, false>(r.tile, name, A, s);
+  else e = go_tile<bf16, kNN, bf16, false>(r.tile, name, A, s);
+  if (e != hipSuccess || r.splits == 1) return e;
+  return is_bf16 && !a_lo ? sum_runs<bf16>(A, ws, out, s) : sum_runs<float>(A, ws, out, s);
 }
 
 hipError_t launch_dense_tn(bool is_bf16, const char* name, int M, int R, int S, const void* a,
                            const void* a_lo, const void* b, float* out, void* ws, hipStream_t s) {
   DenseArgs A{};
   A.a = a; A.a_lo = a_lo; A.b = b; A.R = R; A.S = S; A.K = M;
-  int tile;
-  tn_plan(is_bf16, a_lo != nullptr, M, R, S, tile, A.splits, A.ksplit);
-  A.out = A.splits > 1 ? ws : (void*)out;
+  const Runs r = runs_of(is_bf16, a_lo != nullptr, true, R, S, M);
+  A.splits = r.splits;
+  A.ksplit = r.ksplit;
+  A.out = r.splits > 1 ? ws : (void*)out;
   hipError_t e;
-  if (!is_bf16) e = go_tile<float, kTN, float, false>(tile, name, A, s);
-  else if (a_lo) e = go_tile<bf16, kTN, float, true>(tile, name, A, s);
-  else e = go_tile<bf16, kTN, float, false>(tile, name, A, s);
-  if (e != hipSuccess || A.splits == 1) return e;
-  hipEvent_t e0, e1;
-  prof_kernel("dense_sum", &e0, &e1);
-  const size_t n4 = (size_t)R * S / 4;
-  const unsigned blocks = (unsigned)std::min<size_t>((n4 + 255) / 256, 4096);
-  hipExtLaunchKernelGGL(dense_sum_kernel, dim3(blocks), dim3(256), 0, s, e0, e1, 0,
-                        (const float*)ws, A.splits, n4, out);
-  return hipGetLastError();
+  if (!is_bf16) e = go_tile<float, kTN, float, false>(r.tile, name, A, s);
+  else if (a_lo) e = go_tile<bf16, kTN, float, true>(r.tile, name, A, s);
+  else e = go_tile<bf16, kTN, float, false>(r.tile, name, A, s);
+  if (e != hipSuccess || r.splits == 1) return e;
+  return sum_runs<float>(A, ws, out, s);
 }
 
 }  // namespace swimba

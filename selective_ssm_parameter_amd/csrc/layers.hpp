@@ -67,13 +67,15 @@ hipError_t launch_gated_project(bool is_bf16, int M, int D, int F, int act, cons
 size_t gated_dz_bytes(bool is_bf16, int M, int F);
 hipError_t launch_gated_dz(bool is_bf16, int M, int D, int F, int act, const void* x,
                            const void* w_in, const void* dh, void* dz, hipStream_t s);
+// Partial sums of a product that runs its k in pieces (ws below): out [R, S] of
+// K terms; tn: a weight gradient; split: with a_lo.
+size_t dense_ws_bytes(bool is_bf16, bool split, bool tn, int R, int S, int K);
 // out [M, S] = a [M, K] b [K, S]; with a_lo (bf16 problems) a is a + a_lo and
 // out is float32, else out has the input type.
 hipError_t launch_dense_nn(bool is_bf16, const char* name, int M, int K, int S, const void* a,
-                           const void* a_lo, const void* b, void* out, hipStream_t s);
+                           const void* a_lo, const void* b, void* out, void* ws, hipStream_t s);
 // out [R, S] (float32) = (a + a_lo)^T b over M rows: a, a_lo [M, R] (a_lo may
-// be null; split: it is given), b [M, S].
-size_t dense_tn_ws_bytes(bool is_bf16, bool split, int M, int R, int S);
+// be null), b [M, S].
 hipError_t launch_dense_tn(bool is_bf16, const char* name, int M, int R, int S, const void* a,
                            const void* a_lo, const void* b, float* out, void* ws, hipStream_t s);
 

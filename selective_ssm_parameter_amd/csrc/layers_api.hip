@@ -3,6 +3,7 @@
 // launch; no HIP call is made on an invalid argument.
 #include "swimba_layers.h"
 
+#include <algorithm>
 #include <cmath>
 
 #include "api_common.hpp"
@@ -71,6 +72,7 @@ size_t gated_bwd_dz_bytes(const Dims& d) {
 
 size_t layer_ws(const Dims& d, int32_t call) {
   if (d.M == 0) return 0;
+  const int M = (int)d.M, D = (int)d.D, F = (int)d.HP;
   switch (call) {
     case SWIMBA_LAYER_NORM_BACKWARD:
       return d.D > kNormMaxD ? 0
@@ -78,11 +80,14 @@ size_t layer_ws(const Dims& d, int32_t call) {
     case SWIMBA_LAYER_GATED_SCAN:
     case SWIMBA_LAYER_GATED_SCAN_BACKWARD:
       return gscan_ws_bytes((int)d.Bt, (int)d.T, (int)d.HP);
+    // dz, and behind it the partial sums of dx, then those of dw_in
     case SWIMBA_LAYER_GATED_PROJECT_BACKWARD:
       return gated_bwd_dz_bytes(d) +
-             dense_tn_ws_bytes(d.bf16, d.bf16, (int)d.M, (int)(2 * d.HP), (int)d.D);
+             std::max(dense_ws_bytes(d.bf16, d.bf16, false, M, D, 2 * F),
+                      dense_ws_bytes(d.bf16, d.bf16, true, 2 * F, D, M));
     case SWIMBA_LAYER_OUTPUT_PROJECT_BACKWARD:
-      return dense_tn_ws_bytes(d.bf16, false, (int)d.M, (int)d.D, (int)d.HP);
+      return std::max(dense_ws_bytes(d.bf16, false, false, M, F, D),
+                      dense_ws_bytes(d.bf16, false, true, D, F, M));
     default: return 0;
   }
 }
@@ -293,13 +298,14 @@ swimba_status swimba_gated_project_backward(const swimba_dims* dims, const void*
     return st;
   const int M = (int)d.M, D = (int)d.D, F = (int)d.HP;
   unsigned char* w8 = static_cast<unsigned char*>(ws);
+  unsigned char* part = w8 + gated_bwd_dz_bytes(d);
   const void* lo = d.bf16 ? w8 + (size_t)M * 2 * F * 2 : nullptr;
   hipError_t e = launch_gated_dz(d.bf16, M, D, F, act, x, w_in, dh, ws, stream);
   if (e != hipSuccess) return hip_status(e, "gated_project_backward dz launch");
-  e = launch_dense_nn(d.bf16, "gated_dx", M, 2 * F, D, ws, lo, w_in, dx, stream);
+  e = launch_dense_nn(d.bf16, "gated_dx", M, 2 * F, D, ws, lo, w_in, dx, part, stream);
   if (e != hipSuccess) return hip_status(e, "gated_project_backward dx launch");
-  return hip_status(launch_dense_tn(d.bf16, "gated_dw", M, 2 * F, D, ws, lo, x, dw_in,
-                                    w8 + gated_bwd_dz_bytes(d), stream),
+  return hip_status(launch_dense_tn(d.bf16, "gated_dw", M, 2 * F, D, ws, lo, x, dw_in, part,
+                                    stream),
                     "gated_project_backward dw launch");
 }
 
@@ -322,7 +328,7 @@ swimba_status swimba_output_project_backward(const swimba_dims* dims, const void
   if ((st = check_ws(ws, ws_bytes, layer_ws(d, SWIMBA_LAYER_OUTPUT_PROJECT_BACKWARD))) != SWIMBA_OK)
     return st;
   const int M = (int)d.M, D = (int)d.D, F = (int)d.HP;
-  hipError_t e = launch_dense_nn(d.bf16, "output_project_dy", M, D, F, dout, nullptr, w_out, dy, stream);
+  hipError_t e = launch_dense_nn(d.bf16, "output_project_dy", M, D, F, dout, nullptr, w_out, dy, ws, stream);
   if (e != hipSuccess) return hip_status(e, "output_project_backward dy launch");
   return hip_status(launch_dense_tn(d.bf16, "output_project_dw", M, D, F, dout, nullptr, y, dw_out, ws,
                                     stream),

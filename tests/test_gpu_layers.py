@@ -431,6 +431,7 @@ def gemm_case(M, D, F, dtype, seed=0):
 
 
 GEMM_SHAPES = [(1, 8, 8), (17, 2056, 40), (33, 264, 520), (64, 1032, 200), (65, 72, 136),
+               (70, 1048, 1224),
                 (1, 64, 128), (3, 40, 24), (16, 96, 264), (127, 128, 128),
                (129, 136, 72), (300, 520, 200), (1000, 64, 1032), (2049, 104, 136),
                (4100, 40, 264)]
