@@ -438,6 +438,19 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
     static_assert(TN % 4 == 0, "a pair of g tiles and the pair of u tiles per wave");
     TO* h = static_cast<TO*>(A.out);
     TO* z = static_cast<TO*>(A.z);
+    // the gradients of h for this lane's rows, all requested before the first use
+    typename Vec<T>::x8 dv[MODE == kGatedBwd ? TM * (TN / 4) : 1];
+    if constexpr (MODE == kGatedBwd) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int jj = 0; jj < TN / 4; ++jj) {
+          const int r = min(wm * TM * 16 + 16 * i + c, nrows - 1);
+          const int col = min(s0 + (wn * (TN / 4) + jj) * 32 + 8 * g, A.S - 8);
+          dv[i * (TN / 4) + jj] =
+              load8<T>(static_cast<const T*>(A.dh) + (size_t)(r0 + r) * A.S + col);
+        }
+    }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       const int r = wm * TM * 16 + 16 * i + c;
@@ -447,13 +460,12 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
         if (r >= nrows || col >= A.S) continue;
         if constexpr (MODE == kGatedBwd) {
           const size_t row = (size_t)(r0 + r);
-          const typename Vec<T>::x8 dv = load8<T>(static_cast<const T*>(A.dh) + row * A.S + col);
           floatx8 dg, du;
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             float v, d;
             act_grad(A.act, acc[i][4 * jj + (q >> 2)][q & 3], v, d);
-            const float dd = to_f32(dv[q]);
+            const float dd = to_f32(dv[i * (TN / 4) + jj][q]);
             dg[q] = dd * acc[i][4 * jj + 2 + (q >> 2)][q & 3] * d;
             du[q] = dd * v;
           }
