@@ -44,6 +44,7 @@ typedef Cfg<256, 192, 2, 4> Wide;  // not for gated products
 typedef Cfg<128, 128, 2, 2> Mid;
 typedef Cfg<64, 128, 2, 2> Small;   // gated products (32 columns of g and of u per wave)
 typedef Cfg<64, 64, 2, 2> Small64;  // the others
+typedef Cfg<32, 64, 2, 2> Tiny;
 
 // kGated: h; kGatedBwd: the same product, dz in the epilogue
 enum Mode { kGated, kGatedBwd, kNN, kTN };
@@ -667,49 +668,56 @@ hipError_t go(const char* name, const DenseArgs& A, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Tile and number of k runs of a product, by an estimate of its time in us from
-// what the tiles measured: workgroups the chip holds at once, time per k step of
-// those that share a CU, and the rest of a tile (first copies, epilogue, stores).
-// bf16 at 256 rows 0.90 us a step and 12 us a tile (32768 x 8192 x 2048: 16
-// rounds, 1081 us); 128 rows, two tiles per CU, 1439 us for the same product;
-// 64 rows are for products that would leave most CUs without a tile. fp32
-// stages of 256 rows do not fit LDS.
+// Tile and number of k runs of a product, by an estimate of its time in us. A
+// tile's k step takes `alone` us by itself (its copies and LDS reads waited for)
+// and at least `busy` us per tile that shares the CU, of which there are up to
+// `most`; `rest` is what a tile adds (first copies, epilogue, stores). Fitted to
+// products of 999 x 1016 x 480 and 4096 x 1024 x 1024 with each tile and of
+// 32768 x 8192 x 2048. fp32 stages of 256 rows do not fit LDS.
 struct TileCost {
-  int rows, cols, slots;
-  double step, rest;
+  int rows, cols, most;
+  double busy, alone, rest;
 };
-constexpr TileCost kBf16Tiles[] = {{256, 256, 256, 0.90, 12},
-                                   {256, 192, 256, 0.72, 10},
-                                   {128, 128, 512, 0.62, 8},
-                                   {64, 64, 1024, 0.40, 5}};
-constexpr TileCost kBf16Gated[] = {{256, 256, 256, 0.90, 12},
-                                   {128, 128, 512, 0.62, 8},
-                                   {64, 128, 768, 0.53, 5}};
-constexpr TileCost kF32Tiles[] = {{128, 128, 256, 1.8, 8}, {64, 64, 512, 1.0, 5}};
-constexpr TileCost kF32Gated[] = {{128, 128, 512, 3.4, 8}, {64, 128, 256, 1.0, 5}};
+constexpr TileCost kBf16Tiles[] = {{256, 256, 1, 0.90, 0.90, 10},
+                                   {256, 192, 1, 0.72, 0.72, 9},
+                                   {128, 128, 2, 0.31, 0.35, 6},
+                                   {64, 64, 4, 0.16, 0.20, 4},
+                                   {32, 64, 6, 0.10, 0.20, 4}};
+constexpr TileCost kBf16Gated[] = {{256, 256, 1, 0.90, 0.90, 12},
+                                   {128, 128, 2, 0.31, 0.35, 7},
+                                   {64, 128, 3, 0.19, 0.22, 5}};
+constexpr TileCost kF32Tiles[] = {{128, 128, 1, 2.0, 2.0, 8},
+                                  {64, 64, 2, 0.52, 0.65, 6},
+                                  {32, 64, 3, 0.25, 0.40, 5}};
+constexpr TileCost kF32Gated[] = {{128, 128, 2, 1.8, 2.0, 8}, {64, 128, 1, 1.0, 1.0, 6}};
 
 struct Plan {
   int tile, splits;  // tile: rows * 1000 + columns
 };
-// most: the largest number of k runs; their partial sums
-// are written, read and summed at about 4 TB/s.
+// most: the largest number of k runs; their partial sums are written, read and
+// summed at about 4 TB/s by one more launch.
 Plan plan(bool is_bf16, bool split, bool gated, int64_t R, int64_t S, int64_t K, int64_t most) {
   Plan best{0, 1};
   double tbest = 1e30;
-  const TileCost* c = is_bf16 ? (gated ? kBf16Gated : kBf16Tiles) : (gated ? kF32Gated : kF32Tiles);
-  const int nt = is_bf16 ? (gated ? 3 : 4) : 2;
-  const double steps = (double)((K + kBK - 1) / kBK) * (split ? 1.9 : 1.0);
+  const TileCost* tiles =
+      is_bf16 ? (gated ? kBf16Gated : kBf16Tiles) : (gated ? kF32Gated : kF32Tiles);
+  const int nt = is_bf16 ? (gated ? 3 : 5) : (gated ? 2 : 3);
+  const double steps = (double)((K + kBK - 1) / kBK) * (split ? 1.8 : 1.0);
   for (int i = 0; i < nt; ++i) {
-    const int64_t units = (R + c[i].rows - 1) / c[i].rows * ((S + c[i].cols - 1) / c[i].cols);
+    const TileCost& c = tiles[i];
+    const int64_t units = (R + c.rows - 1) / c.rows * ((S + c.cols - 1) / c.cols);
     for (int64_t n = 1; n <= most; ++n) {
-      const double rounds = (double)((units * n + c[i].slots - 1) / c[i].slots);
-      double t = rounds * (steps / n * c[i].step + c[i].rest);
+      auto round = [&](int64_t per_cu) {
+        return steps / n * std::max(c.alone, per_cu * c.busy) + c.rest;
+      };
+      const int64_t full = units * n / (256 * c.most), left = units * n % (256 * c.most);
+      double t = full * round(c.most) + (left ? round((left + 255) / 256) : 0.0);
       if (n > 1) t += 4 + (double)(n + 1) * R * S * 4e-6 / 4;
       if (t < tbest) {
         tbest = t;
-        best = Plan{c[i].rows * 1000 + c[i].cols, (int)n};
+        best = Plan{c.rows * 1000 + c.cols, (int)n};
       }
-      if (units * n > 4 * c[i].slots) break;  // more runs only add partial sums
+      if (full > 3) break;  // more runs only add partial sums
     }
   }
   return best;
@@ -773,7 +781,8 @@ hipError_t go_tile(int tile, const char* name, const DenseArgs& A, hipStream_t s
     if (tile == 256192) return go<T, Wide, MODE, TO, SPLIT>(name, A, s);
   }
   if (tile == 128128) return go<T, Mid, MODE, TO, SPLIT>(name, A, s);
-  return go<T, Small64, MODE, TO, SPLIT>(name, A, s);
+  if (tile == 64064) return go<T, Small64, MODE, TO, SPLIT>(name, A, s);
+  return go<T, Tiny, MODE, TO, SPLIT>(name, A, s);
 }
 
 }  // namespace
