@@ -118,6 +118,7 @@ swimba_status swimba_layer_norm_backward(const swimba_dims* dims, const void* s,
  *   h_final   [batch, C] float32 out, or NULL; may be the same tensor as h_init
  *   carry     float32 out of swimba_gated_scan_carry_size() bytes, or NULL:
  *             the states that the backward starts its chunks of tokens from
+ *             (not written for chunks past a sequence's length)
  *   ws        workspace of SWIMBA_LAYER_GATED_SCAN
  */
 swimba_status swimba_gated_scan(const swimba_dims* dims, const void* x, const void* forget,

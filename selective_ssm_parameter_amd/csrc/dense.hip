@@ -706,6 +706,7 @@ Plan plan(bool is_bf16, bool split, bool gated, int64_t R, int64_t S, int64_t K,
   for (int i = 0; i < nt; ++i) {
     const TileCost& c = tiles[i];
     const int64_t units = (R + c.rows - 1) / c.rows * ((S + c.cols - 1) / c.cols);
+    if (i > 0 && units > (1 << 20)) continue;  // (a launch's threads are counted in 32 bits)
     for (int64_t n = 1; n <= most; ++n) {
       auto round = [&](int64_t per_cu) {
         return steps / n * std::max(c.alone, per_cu * c.busy) + c.rest;

@@ -156,11 +156,18 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* p) {
 __device__ __forceinline__ void post(uint64_t* p, uint64_t v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+// Waits for a word. It comes within microseconds unless another call works in
+// the same workspace at the same time, which the interface rules out; rather
+// than hang the device, the wait then ends after kWaitTicks with NaN.
+constexpr uint64_t kWaitTicks = 1000000000ull;  // 10 s of the 100 MHz clock
 __device__ __forceinline__ uint64_t wait_for(const uint64_t* p) {
   uint64_t v = peek(p);
-  while (v == kUnset) {
-    __builtin_amdgcn_s_sleep(1);
-    v = peek(p);
+  if (v == kUnset) {
+    const uint64_t t0 = wall_clock64();
+    do {
+      __builtin_amdgcn_s_sleep(1);
+      v = peek(p);
+    } while (v == kUnset && wall_clock64() - t0 < kWaitTicks);
   }
   return v;
 }

@@ -296,6 +296,12 @@ def test_gated_scan_lengths(dtype, T, lens):
     run_scan_checks(scan_case(4, T, 72, dtype, True, lens, seed=T))
 
 
+def test_gated_scan_lengths_over_several_groups():
+    """Groups of 2048 tokens that end before, at and behind a length."""
+    lens = [4200, 2048, 2049, 4097, 130, 0]
+    run_scan_checks(scan_case(6, 4200, 9, "f32", True, lens, seed=8))
+
+
 @pytest.mark.parametrize("dtype,C,pad", [("bf16", 64, 0), ("bf16", 64, 8), ("bf16", 64, 3),
                                          ("f32", 64, 4), ("f32", 64, 1), ("f32", 68, 0)])
 def test_gated_scan_strided_rows(dtype, C, pad):
