@@ -214,6 +214,19 @@ __device__ __forceinline__ bool unit_of(int nr, int nc, int& tr, int& tc) {
   return true;
 }
 
+// 8 elements of a gated output, past the L2's reuse order where its rows start on
+// 128-byte lines (through): 32768 x 8192 x 2048 2 % faster.
+template <typename T>
+__device__ __forceinline__ void store_gated(T* p, typename Vec<T>::x8 v, bool through) {
+  if constexpr (sizeof(T) == 2) {
+    if (through) {
+      __builtin_nontemporal_store(__builtin_bit_cast(int4v, v), reinterpret_cast<int4v*>(p));
+      return;
+    }
+  }
+  store8<T>(p, v);
+}
+
 template <typename T, class C, Mode MODE, typename TO, bool SPLIT>
 __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   typedef DLay<T, C, MODE, SPLIT> L;
@@ -439,6 +452,7 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
     static_assert(TN % 4 == 0, "a pair of g tiles and the pair of u tiles per wave");
     TO* h = static_cast<TO*>(A.out);
     TO* z = static_cast<TO*>(A.z);
+    const bool through = A.S % 64 == 0;
     // the gradients of h for this lane's rows, all requested before the first use
     typename Vec<T>::x8 dv[MODE == kGatedBwd ? TM * (TN / 4) : 1];
     if constexpr (MODE == kGatedBwd) {
@@ -472,8 +486,8 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
           }
           TO* hi = static_cast<TO*>(A.out) + row * 2 * A.S + col;
           const typename Vec<TO>::x8 hg = convert8<TO, float>(dg), hu = convert8<TO, float>(du);
-          store8<TO>(hi, hg);
-          store8<TO>(hi + A.S, hu);
+          store_gated<TO>(hi, hg, through);
+          store_gated<TO>(hi + A.S, hu, through);
           if constexpr (ES == 2) {
             TO* lo = hi + (size_t)A.R * 2 * A.S;
 #pragma unroll
@@ -481,8 +495,8 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
               dg[q] -= to_f32(hg[q]);
               du[q] -= to_f32(hu[q]);
             }
-            store8<TO>(lo, convert8<TO, float>(dg));
-            store8<TO>(lo + A.S, convert8<TO, float>(du));
+            store_gated<TO>(lo, convert8<TO, float>(dg), through);
+            store_gated<TO>(lo + A.S, convert8<TO, float>(du), through);
           }
           continue;
         }
@@ -496,10 +510,10 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
           oh[q] = from_f32<TO>(act_of(A.act, gv) * uv);
         }
         const size_t row = (size_t)(r0 + r);
-        store8<TO>(h + row * A.S + col, oh);
+        store_gated<TO>(h + row * A.S + col, oh, through);
         if (z) {
-          store8<TO>(z + row * 2 * A.S + col, og);
-          store8<TO>(z + row * 2 * A.S + A.S + col, ou);
+          store_gated<TO>(z + row * 2 * A.S + col, og, through);
+          store_gated<TO>(z + row * 2 * A.S + A.S + col, ou, through);
         }
       }
     }
