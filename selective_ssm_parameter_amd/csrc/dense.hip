@@ -691,19 +691,20 @@ hipError_t go(const char* name, const DenseArgs& A, hipStream_t s) {
 struct TileCost {
   int rows, cols, most;
   double busy, alone, rest;
+  double split;  // factor of a step with hi and lo
 };
-constexpr TileCost kBf16Tiles[] = {{256, 256, 1, 0.90, 0.90, 10},
-                                   {256, 192, 1, 0.72, 0.72, 9},
-                                   {128, 128, 2, 0.31, 0.35, 6},
-                                   {64, 64, 4, 0.16, 0.20, 4},
-                                   {32, 64, 6, 0.10, 0.20, 4}};
-constexpr TileCost kBf16Gated[] = {{256, 256, 1, 0.90, 0.90, 12},
-                                   {128, 128, 2, 0.31, 0.35, 7},
-                                   {64, 128, 3, 0.19, 0.22, 5}};
-constexpr TileCost kF32Tiles[] = {{128, 128, 1, 2.0, 2.0, 8},
-                                  {64, 64, 2, 0.52, 0.65, 6},
-                                  {32, 64, 3, 0.25, 0.40, 5}};
-constexpr TileCost kF32Gated[] = {{128, 128, 2, 1.8, 2.0, 8}, {64, 128, 1, 1.0, 1.0, 6}};
+constexpr TileCost kBf16Tiles[] = {{256, 256, 1, 0.90, 0.90, 10, 1.8},
+                                   {256, 192, 1, 0.72, 0.72, 9, 1.9},
+                                   {128, 128, 2, 0.31, 0.35, 6, 1.6},
+                                   {64, 64, 4, 0.16, 0.20, 4, 1.8},
+                                   {32, 64, 6, 0.10, 0.20, 4, 1.8}};
+constexpr TileCost kBf16Gated[] = {{256, 256, 1, 0.90, 0.90, 12, 1},
+                                   {128, 128, 2, 0.31, 0.35, 7, 1},
+                                   {64, 128, 3, 0.19, 0.22, 5, 1}};
+constexpr TileCost kF32Tiles[] = {{128, 128, 1, 2.0, 2.0, 8, 1},
+                                  {64, 64, 2, 0.52, 0.65, 6, 1},
+                                  {32, 64, 3, 0.25, 0.40, 5, 1}};
+constexpr TileCost kF32Gated[] = {{128, 128, 2, 1.8, 2.0, 8, 1}, {64, 128, 1, 1.0, 1.0, 6, 1}};
 
 struct Plan {
   int tile, splits;  // tile: rows * 1000 + columns
@@ -716,9 +717,9 @@ Plan plan(bool is_bf16, bool split, bool gated, int64_t R, int64_t S, int64_t K,
   const TileCost* tiles =
       is_bf16 ? (gated ? kBf16Gated : kBf16Tiles) : (gated ? kF32Gated : kF32Tiles);
   const int nt = is_bf16 ? (gated ? 3 : 5) : (gated ? 2 : 3);
-  const double steps = (double)((K + kBK - 1) / kBK) * (split ? 1.8 : 1.0);
   for (int i = 0; i < nt; ++i) {
     const TileCost& c = tiles[i];
+    const double steps = (double)((K + kBK - 1) / kBK) * (split ? c.split : 1.0);
     const int64_t units = (R + c.rows - 1) / c.rows * ((S + c.cols - 1) / c.cols);
     if (i > 0 && units > (1 << 20)) continue;  // (a launch's threads are counted in 32 bits)
     for (int64_t n = 1; n <= most; ++n) {
