@@ -233,16 +233,31 @@ __device__ __forceinline__ Run waves_before(const Place& p, Shared& sh, const Ru
   return r;
 }
 
-// From each thread's run to its states. start: the state that enters the first
-// chunk, or null. CHAIN: sequences have more than one chunk.
+// The state that enters the sequence (start, or null for zeros) where
+// enter_states takes it: of a chain, in the last wave of the first group's
+// chunks. Loaded before the chunk's tokens, so that waiting for it does not wait
+// for them.
+template <bool REV, bool CHAIN>
+__device__ __forceinline__ float first_state(const GScanArgs& A, const Place& p,
+                                             const float* start) {
+  const bool last = p.wave == (REV ? 0 : kWaves - 1);
+  if (!start || !p.on || (CHAIN && !(last && p.step < kGroup))) return 0.f;
+  return start[(size_t)p.b * A.C + p.c];
+}
+
+// From each thread's run to its states. CHAIN: sequences have more than one chunk.
 template <bool REV, bool CHAIN>
 __device__ __forceinline__ States enter_states(const GScanArgs& A, const Place& p, Shared& sh,
-                                               const Run& own, const float* start) {
+                                               const Run& own, float first) {
   const int lane = threadIdx.x & 63, ord = REV ? kWaves - 1 - p.wave : p.wave;
-  const Run before = waves_before<REV>(p, sh, own);
   const bool last = ord == kWaves - 1;
+  // The state that leaves the sequence may be written over the one that enters
+  // it: by a wave of this workgroup after the barrier below, or by a workgroup
+  // that waited for the run that this one posts. The (empty) use makes the load
+  // of `first` complete before both.
+  asm volatile("" : "+v"(first) : : "memory");
+  const Run before = waves_before<REV>(p, sh, own);
   const Run total = join(before, own);  // of the chunk, in the last wave
-  const float first = start && p.on ? start[(size_t)p.b * A.C + p.c] : 0.f;
   States st;
   st.in = first;
   if constexpr (CHAIN) {
@@ -310,6 +325,7 @@ __device__ __forceinline__ void gscan_chunk(const GScanArgs& A, const Place& p, 
       store_one<T, NT>(ry, w0 + i < rows ? col : kOOB, (w0 + i) * ypitch, 0.f);
     return;
   }
+  const float first = first_state<false, CHAIN>(A, p, A.h_init);
   uint32_t xr[kTpt], fr[kTpt], gr[kTpt];
 #pragma unroll
   for (int i = 0; i < kTpt; ++i) {
@@ -328,7 +344,7 @@ __device__ __forceinline__ void gscan_chunk(const GScanArgs& A, const Place& p, 
     extend(own, k[i]);
     own.S = step(k[i], value<T>(xr[i]), own.S);
   }
-  const States st = enter_states<false, CHAIN>(A, p, sh, own, A.h_init);
+  const States st = enter_states<false, CHAIN>(A, p, sh, own, first);
   if (p.on && A.carry && p.wave == 0) A.carry[p.cw * A.C + p.c] = st.in;
   if (p.on && A.h_final && p.step == p.nc - 1 && p.wave == kWaves - 1)
     A.h_final[(size_t)p.b * A.C + p.c] = st.out;
@@ -388,6 +404,7 @@ __global__ __launch_bounds__(kTh, 4) void gscan_bwd_kernel(GScanArgs A) {
     }
     return;
   }
+  const float first = first_state<true, CHAIN>(A, p, A.dh_final);
   uint32_t xr[kTpt], fr[kTpt], gr[kTpt], dr[kTpt];
 #pragma unroll
   for (int i = 0; i < kTpt; ++i) {
@@ -418,7 +435,7 @@ __global__ __launch_bounds__(kTh, 4) void gscan_bwd_kernel(GScanArgs A) {
   const Run fbefore = waves_before<false>(p, sh, fw);
   float h = p.on ? apply(fbefore, A.carry_in[p.cw * A.C + p.c]) : 0.f;
   __syncthreads();  // the runs in LDS are no longer read
-  const States st = enter_states<true, CHAIN>(A, p, sh, bw, A.dh_final);
+  const States st = enter_states<true, CHAIN>(A, p, sh, bw, first);
   if (p.on && A.dh_init && p.step == p.nc - 1 && p.wave == 0)
     A.dh_init[(size_t)p.b * A.C + p.c] = st.out;
   // e_t from the last token back

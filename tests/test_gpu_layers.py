@@ -289,6 +289,25 @@ def test_gated_scan(Bt, T, C, dtype, gate):
     run_scan_checks(c)
 
 
+@pytest.mark.parametrize("T", [1, 17, 128, 129, 300, 2049, 4500])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gated_scan_states_in_place(T, dtype):
+    """The final state over the initial one, and their gradients: the same bits
+    as in tensors of their own, with chains of none, one and several groups."""
+    c = scan_case(3, T, 200, dtype, lens=[T, T // 2, 0], seed=T)
+    y, h, ca = scan_forward(c)
+    dx, df, do, dh0 = scan_backward(c, ca)
+    ws = sl.layer_workspace(c["dims"], sl.LAYER_GATED_SCAN)
+    y2, state = empty(3 * T, 200, dt=c["dt"]), c["h0"].clone()
+    sl.swimba_gated_scan(c["dims"], c["x"], c["f"], c["o"], c["lens"], state, y2, state, None, ws)
+    assert torch.equal(y2, y) and torch.equal(state, h)
+    ws = sl.layer_workspace(c["dims"], sl.LAYER_GATED_SCAN_BACKWARD)
+    g, grad = [empty(3 * T, 200, dt=c["dt"]) for _ in range(3)], c["dh"].clone()
+    sl.swimba_gated_scan_backward(c["dims"], c["x"], c["f"], c["o"], c["lens"], ca, c["dy"], grad,
+                                  *g, grad, ws)
+    assert all(torch.equal(a, b) for a, b in zip(g + [grad], (dx, df, do, dh0)))
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T,lens", [(300, [300, 0, 1, 299]), (520, [256, 257, 255, 512]),
                                     (64, [-3, 70, 64, 0])])
