@@ -71,6 +71,13 @@ swimba_status read_dims(const swimba_dims* d, Dims& o) {
   return SWIMBA_OK;
 }
 
+bool query_dims(const swimba_dims* d, Dims& o) {
+  const std::string saved = g_err;
+  const bool ok = read_dims(d, o) == SWIMBA_OK;
+  g_err = saved;
+  return ok;
+}
+
 swimba_status check_ws(void* ws, size_t have, size_t need) {
   if (need == 0) return SWIMBA_OK;
   if (!ws) return fail(SWIMBA_ERR_WORKSPACE, "workspace of %zu bytes required, got NULL", need);
@@ -371,10 +378,7 @@ const char* swimba_last_error(void) { return g_err.c_str(); }
 
 size_t swimba_workspace_size(const swimba_dims* dims, int32_t call) {
   Dims d;
-  std::string saved = g_err;
-  const swimba_status st = read_dims(dims, d);
-  g_err = saved;
-  if (st != SWIMBA_OK) return 0;
+  if (!query_dims(dims, d)) return 0;
   switch (call) {
     case SWIMBA_CALL_ROUTE: return 0;
     case SWIMBA_CALL_PROJECT: return d.M == 0 ? 0 : proj_ws(d).total;

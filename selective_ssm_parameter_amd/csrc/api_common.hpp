@@ -26,6 +26,8 @@ struct Dims {
 };
 
 swimba_status read_dims(const swimba_dims* d, Dims& o);
+// The same for a size query, which leaves swimba_last_error() as it was.
+bool query_dims(const swimba_dims* d, Dims& o);
 
 // The largest record a buffer resource may cover: loads that must read zeros
 // take the byte offset 2^31, which has to lie past it.

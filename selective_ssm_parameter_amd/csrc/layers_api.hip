@@ -16,11 +16,12 @@ namespace {
 // A grid's threads are counted in 32 bits.
 constexpr int64_t kMaxThreads = int64_t(1) << 32;
 constexpr int64_t kMaxLd = int64_t(1) << 22;
+constexpr int64_t kMaxD = int64_t(1) << 20;
 
 swimba_status read_layer_dims(const swimba_dims* dims, Dims& d) {
   const swimba_status st = read_dims(dims, d);
   if (st != SWIMBA_OK) return st;
-  if (d.D > (1 << 20)) return fail(SWIMBA_ERR_DIMS, "d_model must be at most 2^20");
+  if (d.D > kMaxD) return fail(SWIMBA_ERR_DIMS, "d_model must be at most 2^20");
   return SWIMBA_OK;
 }
 
@@ -98,13 +99,13 @@ extern "C" {
 
 size_t swimba_layer_workspace_size(const swimba_dims* dims, int32_t call) {
   Dims d;
-  if (read_layer_dims(dims, d) != SWIMBA_OK) return 0;
+  if (!query_dims(dims, d) || d.D > kMaxD) return 0;
   return layer_ws(d, call);
 }
 
 size_t swimba_gated_scan_carry_size(const swimba_dims* dims) {
   Dims d;
-  if (read_layer_dims(dims, d) != SWIMBA_OK) return 0;
+  if (!query_dims(dims, d) || d.D > kMaxD) return 0;
   return sizeof(float) * (size_t)(d.Bt * gscan_chunks((int)d.T) * d.HP);
 }
 

@@ -199,6 +199,15 @@ def test_workspace_of_invalid_dims():
     assert sl.lib().swimba_gated_scan_carry_size(ref(bad)) == 0
 
 
+def test_size_queries_keep_the_last_error():
+    lib()
+    assert norm(None) == -1 and "dims is NULL" in err()
+    for bad in (dims(batch=-1), dims(d=(1 << 20) + 8, f=8, seqlen=1)):
+        assert sl.layer_workspace_size(bad, sl.LAYER_NORM_BACKWARD) == 0
+        assert sl.lib().swimba_gated_scan_carry_size(ref(bad)) == 0
+        assert "dims is NULL" in err()
+
+
 def test_binding_checks_row_strides():
     lib()
     wide = torch.zeros(4, 30)
