@@ -82,8 +82,11 @@ def gated_scan_carry(dims, device="cuda") -> torch.Tensor:
 # torch for no more than it needs.
 
 def _device():
-    """The current device's index (-1 before CUDA is initialised)."""
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+    """The current device's index. Before CUDA is initialised no tensor lies on
+    the GPU (and a host tensor's index, -1, must not pass for a device's)."""
+    if not torch.cuda.is_initialized():
+        raise ValueError("CUDA is not initialised: the tensors cannot lie on the current device")
+    return torch._C._cuda_getDevice()
 
 
 def _refuse(t, dev):
@@ -153,9 +156,9 @@ def swimba_layer_norm(dims, x, residual, weight, bias, eps, sum, y, mean=None, r
 
 def swimba_layer_norm_backward(dims, s, weight, mean, rstd, dy, dres, dx, dweight, dbias, ws,
                                ws_bytes=None, stream=None):
-    dev = _device()
     if dy is not None and dy.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"dy of {dy.dtype}: bfloat16 or float32")
+    dev = _device()
     dy_dtype = sb.BF16 if dy is not None and dy.dtype == torch.bfloat16 else sb.F32
     p = _ptrs(dev, s, weight, mean, rstd, dy, dres, dx, dweight, dbias, ws)
     _check(lib().swimba_layer_norm_backward(ctypes.byref(dims), *p[:5], dy_dtype, *p[5:],

@@ -1,0 +1,99 @@
+"""What the binding of the layer calls refuses before the library is entered.
+
+The library's functions are replaced by one that records its call, so that a
+check that lets a call through is seen and nothing can be launched."""
+from __future__ import annotations
+
+import os
+
+import pytest
+import torch
+
+from selective_ssm_parameter_amd import binding as sb
+from selective_ssm_parameter_amd import layers as sl
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+class Recorder:
+    """Stands in for the library: sizes come from it, calls are only noted."""
+
+    def __init__(self, real):
+        self.real, self.calls = real, []
+
+    def __getattr__(self, name):
+        if name.endswith("_size"):
+            return getattr(self.real, name)
+
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+
+        return call
+
+
+@pytest.fixture
+def library(monkeypatch):
+    if not os.path.exists(sb.LIB_PATH):
+        pytest.skip("libswimba.so not built")
+    rec = Recorder(sl.lib())
+    monkeypatch.setattr(sl, "lib", lambda: rec)
+    return rec
+
+
+def z(*shape, dt=BF):
+    return torch.zeros(*shape, dtype=dt)
+
+
+def calls(B=2, T=200, D=16, C=24, dtype="bf16"):
+    """name -> (function, arguments by name) of a call that is right in all but
+    where its tensors lie."""
+    dt = BF if dtype == "bf16" else F32
+    M, d = B * T, sl.layer_dims(B, T, D, C, dtype)
+    n = lambda *s: z(*s, dt=dt)
+    f = lambda *s: z(*s, dt=F32)
+    ws = lambda c: sl.layer_workspace(d, c, device="cpu")
+    lens = torch.zeros(B, dtype=torch.int32)
+    return {
+        "norm": (sl.swimba_layer_norm, dict(
+            dims=d, x=n(M, D), residual=n(M, D), weight=n(D), bias=n(D), eps=1e-5, sum=n(M, D),
+            y=n(M, D), mean=f(M), rstd=f(M))),
+        "norm_backward": (sl.swimba_layer_norm_backward, dict(
+            dims=d, s=n(M, D), weight=n(D), mean=f(M), rstd=f(M), dy=f(M, D), dres=f(M, D),
+            dx=f(M, D), dweight=f(D), dbias=f(D), ws=ws(sl.LAYER_NORM_BACKWARD))),
+        "scan": (sl.swimba_gated_scan, dict(
+            dims=d, x=n(M, C), forget=n(M, C), gate=n(M, C), seq_lens=lens, h_init=f(B, C),
+            y=n(M, C), h_final=f(B, C), carry=sl.gated_scan_carry(d, device="cpu"),
+            ws=ws(sl.LAYER_GATED_SCAN))),
+        "scan_backward": (sl.swimba_gated_scan_backward, dict(
+            dims=d, x=n(M, C), forget=n(M, C), gate=n(M, C), seq_lens=lens,
+            carry=sl.gated_scan_carry(d, device="cpu"), dy=n(M, C), dh_final=f(B, C), dx=n(M, C),
+            dforget=n(M, C), dgate=n(M, C), dh_init=f(B, C),
+            ws=ws(sl.LAYER_GATED_SCAN_BACKWARD))),
+        "step": (sl.swimba_gated_step, dict(
+            dims=sl.layer_dims(B, 1, D, C, dtype), x=n(B, C), forget=n(B, C), gate=n(B, C),
+            h_prev=f(B, C), h=f(B, C), y=n(B, C))),
+        "project": (sl.swimba_gated_project, dict(
+            dims=d, x=n(M, D), w_in=n(2 * C, D), act=0, z=n(M, 2 * C), h=n(M, C))),
+        "project_backward": (sl.swimba_gated_project_backward, dict(
+            dims=d, x=n(M, D), w_in=n(2 * C, D), dh=n(M, C), act=0, dx=f(M, D),
+            dw_in=f(2 * C, D), ws=ws(sl.LAYER_GATED_PROJECT_BACKWARD))),
+        "output_backward": (sl.swimba_output_project_backward, dict(
+            dims=d, y=n(M, C), w_out=n(D, C), dout=n(M, D), dy=n(M, C), dw_out=f(D, C),
+            ws=ws(sl.LAYER_OUTPUT_PROJECT_BACKWARD))),
+    }
+
+
+NAMES = ["norm", "norm_backward", "scan", "scan_backward", "step", "project", "project_backward",
+         "output_backward"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_host_tensors_are_refused_without_a_device(library, monkeypatch, name):
+    """As long as CUDA is not initialised no tensor can lie on the GPU, so the
+    call must not reach the library, whose launch would initialise it."""
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: False)
+    fn, kw = calls()[name]
+    with pytest.raises(ValueError, match="not initialised"):
+        fn(**kw, stream=0)
+    assert not library.calls
