@@ -121,8 +121,8 @@ def _rows(dev, *tensors):
             stride = t.stride()
         if ld is None:
             rows, cols = t.shape
-            single = rows <= 1
-            ld = max(stride[0], cols) if single else stride[0]
+            single = rows <= 1  # whatever its stride is, no row follows
+            ld = cols if single else stride[0]
         elif stride[0] != ld and not single:
             raise ValueError("the gated scan's tensors must have one row stride")
         if stride[1] != 1 and t.shape[1] > 1:

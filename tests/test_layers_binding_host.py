@@ -97,3 +97,27 @@ def test_host_tensors_are_refused_without_a_device(library, monkeypatch, name):
     with pytest.raises(ValueError, match="not initialised"):
         fn(**kw, stream=0)
     assert not library.calls
+
+
+@pytest.fixture
+def on_device(library, monkeypatch):
+    """The tensors count as lying on the current device."""
+    monkeypatch.setattr(sl, "_device", lambda: -1)
+    return library
+
+
+def test_one_row_has_no_distance_to_a_next_one(on_device):
+    """A token of a single sequence, cut from a tensor whose sequences are 2^22
+    elements apart (the library refuses rows that far apart)."""
+    T, C = 4096, 1024
+    x, f, o = (z(1, T, C)[:, 5] for _ in range(3))
+    assert x.stride(0) == 1 << 22
+    sl.swimba_gated_step(sl.layer_dims(1, 1, 8, C, "bf16"), x, f, o, z(1, C, dt=F32),
+                         z(1, C, dt=F32), z(1, C), stream=0)
+    (name, args), = on_device.calls
+    assert name == "swimba_gated_step" and args[4] == C
+    # the stride of more than one row is passed on as it is
+    wide = z(2, 3 * C)
+    sl.swimba_gated_step(sl.layer_dims(2, 1, 8, C, "bf16"), wide[:, :C], wide[:, C:2 * C],
+                         wide[:, 2 * C:], z(2, C, dt=F32), z(2, C, dt=F32), z(2, C), stream=0)
+    assert on_device.calls[1][1][4] == 3 * C
