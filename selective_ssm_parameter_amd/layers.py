@@ -4,8 +4,9 @@ Argument marshalling only, as in :mod:`.binding`: every step runs in the HIP
 kernels of ``libswimba.so``. Tensors are contiguous, but for the inputs and
 gradients of the gated scan, which may be column ranges of a wider tensor
 (unit stride along the channels, one row stride for all of them). All tensors
-of a call must lie on the current device; work goes to that device's current
-stream unless ``stream`` is given.
+of a call must lie on the current device, have the header's element types
+(``seq_lens`` int32) and hold at least the elements that ``dims`` asks for, else
+ValueError; work goes to that device's current stream unless ``stream`` is given.
 """
 from __future__ import annotations
 
@@ -89,7 +90,16 @@ def _device():
     return torch._C._cuda_getDevice()
 
 
-def _refuse(t, dev):
+# The element type of dims.dtype.
+_TYPES = {sb.F32: torch.float32, sb.BF16: torch.bfloat16}
+_F32 = torch.float32
+
+
+def _refuse(t, dev, dt=None, n=0):
+    if n > 0 and dt is not None and t.dtype is not dt:
+        raise ValueError(f"tensor of {t.dtype}, but the call takes it as {dt}")
+    if t.numel() < n:
+        raise ValueError(f"tensor of {t.numel()} elements, but the call takes {n}")
     if t.get_device() != dev:
         raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
     raise ValueError("tensors passed to the Swimba library must be contiguous")
@@ -108,9 +118,22 @@ def _ptrs(dev, *tensors):
     return out
 
 
-def _rows(dev, *tensors):
+def _ptr(dev, dt, t, n):
+    """The pointer of one that holds n elements of dt or more. (Where n is 0, for
+    want of tokens, nothing is read and any type will do; an element type that
+    the library does not know, None here, is refused there.)"""
+    if t is None:
+        return None
+    if t.dtype is dt and t.numel() >= n and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if (n <= 0 or dt is None) and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    return _refuse(t, dev, dt, n)
+
+
+def _rows(dev, *tensors, dt=None, M=0, C=0):
     """Pointers of [M, C] tensors whose rows are equally far apart, and that distance."""
-    ld, ptrs, single = None, [], False
+    ld, ptrs = None, []
     for t in tensors:
         if t is None:
             ptrs.append(None)
@@ -119,23 +142,30 @@ def _rows(dev, *tensors):
         if len(stride) != 2:
             t = t.view(-1, t.shape[-1])
             stride = t.stride()
+        rows, cols = t.shape
         if ld is None:
-            rows, cols = t.shape
             single = rows <= 1  # whatever its stride is, no row follows
             ld = cols if single else stride[0]
         elif stride[0] != ld and not single:
             raise ValueError("the gated scan's tensors must have one row stride")
-        if stride[1] != 1 and t.shape[1] > 1:
+        if stride[1] != 1 and cols > 1:
             raise ValueError("rows of the gated scan must have unit stride along the channels")
+        if t.dtype is not dt and M > 0 and dt is not None:
+            _refuse(t, dev, dt, 1)
+        if rows < M or cols < C:
+            raise ValueError(f"tensor of {rows} rows of {cols}, but the call takes {M} of {C}")
         if t.get_device() != dev:
             _refuse(t, dev)
         ptrs.append(t.data_ptr())
     return ptrs, ld
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(stream, dev):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _raw_stream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -148,66 +178,103 @@ def _ws(ws, ws_bytes):
 
 def swimba_layer_norm(dims, x, residual, weight, bias, eps, sum, y, mean=None, rstd=None,
                       stream=None):
-    dev = _device()
-    px, pr, pw, pb, ps, py, pm, pq = _ptrs(dev, x, residual, weight, bias, sum, y, mean, rstd)
-    _check(lib().swimba_layer_norm(ctypes.byref(dims), px, pr, pw, pb, eps, ps, py, pm, pq,
-                                   _stream(stream, dev)))
+    dev, dt, M, D = _device(), _TYPES.get(dims.dtype), dims.batch * dims.seqlen, dims.d_model
+    n = M * D
+    st = lib().swimba_layer_norm(
+        dims, _ptr(dev, dt, x, n), _ptr(dev, dt, residual, n), _ptr(dev, dt, weight, D),
+        _ptr(dev, dt, bias, D), eps, _ptr(dev, dt, sum, 0 if residual is None else n),
+        _ptr(dev, dt, y, n), None if mean is None else _ptr(dev, _F32, mean, M),
+        None if rstd is None else _ptr(dev, _F32, rstd, M),
+        _raw_stream(dev) if stream is None else _stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def swimba_layer_norm_backward(dims, s, weight, mean, rstd, dy, dres, dx, dweight, dbias, ws,
                                ws_bytes=None, stream=None):
     if dy is not None and dy.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"dy of {dy.dtype}: bfloat16 or float32")
-    dev = _device()
+    dev, dt, M, D = _device(), _TYPES.get(dims.dtype), dims.batch * dims.seqlen, dims.d_model
+    n = M * D
     dy_dtype = sb.BF16 if dy is not None and dy.dtype == torch.bfloat16 else sb.F32
-    p = _ptrs(dev, s, weight, mean, rstd, dy, dres, dx, dweight, dbias, ws)
-    _check(lib().swimba_layer_norm_backward(ctypes.byref(dims), *p[:5], dy_dtype, *p[5:],
-                                            _ws(ws, ws_bytes), _stream(stream, dev)))
+    _check(lib().swimba_layer_norm_backward(
+        dims, _ptr(dev, dt, s, n), _ptr(dev, dt, weight, D), _ptr(dev, _F32, mean, M),
+        _ptr(dev, _F32, rstd, M), _ptr(dev, _TYPES[dy_dtype], dy, n), dy_dtype,
+        _ptr(dev, _F32, dres, n), _ptr(dev, _F32, dx, n), _ptr(dev, _F32, dweight, D),
+        _ptr(dev, _F32, dbias, D), *_ptrs(dev, ws), _ws(ws, ws_bytes), _stream(stream, dev)))
+
+
+def _carry_ptr(dev, dims, carry):
+    return None if carry is None else \
+        _ptr(dev, _F32, carry, lib().swimba_gated_scan_carry_size(dims) // 4)
 
 
 def swimba_gated_scan(dims, x, forget, gate, seq_lens, h_init, y, h_final, carry, ws,
                       ws_bytes=None, stream=None):
-    dev = _device()
-    rows, ld = _rows(dev, x, forget, gate)
-    p = _ptrs(dev, seq_lens, h_init, y, h_final, carry, ws)
-    _check(lib().swimba_gated_scan(ctypes.byref(dims), *rows, ld, *p, _ws(ws, ws_bytes),
-                                   _stream(stream, dev)))
+    dev, dt, B, C = _device(), _TYPES.get(dims.dtype), dims.batch, dims.nheads * dims.headdim
+    M, n = B * dims.seqlen, B * C
+    rows, ld = _rows(dev, x, forget, gate, dt=dt, M=M, C=C)
+    _check(lib().swimba_gated_scan(
+        dims, *rows, ld, _ptr(dev, torch.int32, seq_lens, B if M else 0),
+        _ptr(dev, _F32, h_init, n), _ptr(dev, dt, y, M * C), _ptr(dev, _F32, h_final, n),
+        _carry_ptr(dev, dims, carry), *_ptrs(dev, ws), _ws(ws, ws_bytes), _stream(stream, dev)))
 
 
 def swimba_gated_scan_backward(dims, x, forget, gate, seq_lens, carry, dy, dh_final, dx, dforget,
                                dgate, dh_init, ws, ws_bytes=None, stream=None):
-    dev = _device()
-    rows, ld = _rows(dev, x, forget, gate)
-    drows, ldd = _rows(dev, dx, dforget, dgate if gate is not None else None)
-    p = _ptrs(dev, seq_lens, carry, dy, dh_final, dh_init, ws)
-    _check(lib().swimba_gated_scan_backward(ctypes.byref(dims), *rows, ld, *p[:4], *drows, ldd,
-                                            *p[4:], _ws(ws, ws_bytes), _stream(stream, dev)))
+    dev, dt, B, C = _device(), _TYPES.get(dims.dtype), dims.batch, dims.nheads * dims.headdim
+    M, n = B * dims.seqlen, B * C
+    rows, ld = _rows(dev, x, forget, gate, dt=dt, M=M, C=C)
+    drows, ldd = _rows(dev, dx, dforget, dgate if gate is not None else None, dt=dt, M=M, C=C)
+    _check(lib().swimba_gated_scan_backward(
+        dims, *rows, ld, _ptr(dev, torch.int32, seq_lens, B if M else 0),
+        _carry_ptr(dev, dims, carry), _ptr(dev, dt, dy, M * C), _ptr(dev, _F32, dh_final, n),
+        *drows, ldd, _ptr(dev, _F32, dh_init, n), *_ptrs(dev, ws), _ws(ws, ws_bytes),
+        _stream(stream, dev)))
 
 
 def swimba_gated_step(dims, x, forget, gate, h_prev, h, y, stream=None):
-    dev = _device()
-    rows, ld = _rows(dev, x, forget, gate)
-    _check(lib().swimba_gated_step(ctypes.byref(dims), *rows, ld, *_ptrs(dev, h_prev, h, y),
-                                   _stream(stream, dev)))
+    dev, dt, B, C = _device(), _TYPES.get(dims.dtype), dims.batch, dims.nheads * dims.headdim
+    n = B * C
+    (px, pf, po), ld = _rows(dev, x, forget, gate, dt=dt, M=B, C=C)
+    st = lib().swimba_gated_step(
+        dims, px, pf, po, ld, _ptr(dev, _F32, h_prev, n), _ptr(dev, _F32, h, n),
+        _ptr(dev, dt, y, n), _raw_stream(dev) if stream is None else _stream(stream, dev))
+    if st:
+        _check(st)
+
+
+def _project_sizes(dims):
+    """The element type and the elements of [M, D], [M, F] and [F, D]."""
+    M, D, F = dims.batch * dims.seqlen, dims.d_model, dims.nheads * dims.headdim
+    return _TYPES.get(dims.dtype), M * D, M * F, F * D
 
 
 def swimba_gated_project(dims, x, w_in, act, z, h, stream=None):
     dev = _device()
-    px, pw, pz, ph = _ptrs(dev, x, w_in, z, h)
-    _check(lib().swimba_gated_project(ctypes.byref(dims), px, pw, act, pz, ph, _stream(stream, dev)))
+    dt, nx, nh, nw = _project_sizes(dims)
+    st = lib().swimba_gated_project(
+        dims, _ptr(dev, dt, x, nx), _ptr(dev, dt, w_in, 2 * nw), act, _ptr(dev, dt, z, 2 * nh),
+        _ptr(dev, dt, h, nh), _raw_stream(dev) if stream is None else _stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def swimba_gated_project_backward(dims, x, w_in, dh, act, dx, dw_in, ws, ws_bytes=None,
                                   stream=None):
     dev = _device()
-    px, pw, pd, pdx, pdw, pws = _ptrs(dev, x, w_in, dh, dx, dw_in, ws)
-    _check(lib().swimba_gated_project_backward(ctypes.byref(dims), px, pw, pd, act, pdx, pdw, pws,
-                                               _ws(ws, ws_bytes), _stream(stream, dev)))
+    dt, nx, nh, nw = _project_sizes(dims)
+    _check(lib().swimba_gated_project_backward(
+        dims, _ptr(dev, dt, x, nx), _ptr(dev, dt, w_in, 2 * nw), _ptr(dev, dt, dh, nh), act,
+        _ptr(dev, _F32, dx, nx), _ptr(dev, _F32, dw_in, 2 * nw), *_ptrs(dev, ws),
+        _ws(ws, ws_bytes), _stream(stream, dev)))
 
 
 def swimba_output_project_backward(dims, y, w_out, dout, dy, dw_out, ws, ws_bytes=None,
                                    stream=None):
     dev = _device()
+    dt, nx, ny, nw = _project_sizes(dims)
     _check(lib().swimba_output_project_backward(
-        ctypes.byref(dims), *_ptrs(dev, y, w_out, dout, dy, dw_out, ws), _ws(ws, ws_bytes),
+        dims, _ptr(dev, dt, y, ny), _ptr(dev, dt, w_out, nw), _ptr(dev, dt, dout, nx),
+        _ptr(dev, dt, dy, ny), _ptr(dev, _F32, dw_out, nw), *_ptrs(dev, ws), _ws(ws, ws_bytes),
         _stream(stream, dev)))

@@ -121,3 +121,64 @@ def test_one_row_has_no_distance_to_a_next_one(on_device):
     sl.swimba_gated_step(sl.layer_dims(2, 1, 8, C, "bf16"), wide[:, :C], wide[:, C:2 * C],
                          wide[:, 2 * C:], z(2, C, dt=F32), z(2, C, dt=F32), z(2, C), stream=0)
     assert on_device.calls[1][1][4] == 3 * C
+
+
+# The arguments of every call and what the library takes them for: a tensor of
+# another type or of fewer elements would be read or written past its end.
+def tensors(kw):
+    return [k for k, v in kw.items() if isinstance(v, torch.Tensor) and k != "ws"]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", NAMES)
+def test_calls_that_fit_go_through(on_device, name, dtype):
+    fn, kw = calls(dtype=dtype)[name]
+    fn(**kw, stream=0)
+    assert len(on_device.calls) == 1
+    # tensors that are larger than needed fit as well
+    d0 = kw["dims"]
+    kw["dims"] = sl.layer_dims(1, d0.seqlen, d0.d_model, d0.headdim, dtype)
+    fn(**kw, stream=0)
+    # without tokens nothing is read, whatever is passed
+    kw["dims"] = sl.layer_dims(0, d0.seqlen, d0.d_model, d0.headdim, dtype)
+    fn(**kw, stream=0)
+    assert len(on_device.calls) == 3
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", NAMES)
+def test_other_types_are_refused(on_device, name, dtype):
+    fn, kw = calls(dtype=dtype)[name]
+    for k in tensors(kw):
+        for other in (torch.float16, torch.float64, torch.int64, BF, F32):
+            if other == kw[k].dtype or (k == "dy" and name == "norm_backward" and other == BF):
+                continue  # (the norm's dy is of either type; the library checks the pair)
+            with pytest.raises(ValueError, match=str(other)):
+                fn(**dict(kw, **{k: kw[k].to(other)}), stream=0)
+    assert not on_device.calls
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_smaller_tensors_are_refused(on_device, name):
+    fn, kw = calls()[name]
+    rows = {"x", "forget", "gate", "dx", "dforget", "dgate"} if "scan" in name or name == "step" \
+        else set()
+    for k in tensors(kw):
+        t = kw[k]
+        short = [t[:-1]] if k in rows else [t.reshape(-1)[:-1]]
+        if k in rows:
+            short.append(t[:, :-1])  # rows too short, at the right distance
+        for s in short:
+            with pytest.raises(ValueError, match="elements|rows"):
+                fn(**dict(kw, **{k: s}), stream=0)
+    assert not on_device.calls
+
+
+def test_lengths_of_another_type_are_refused(on_device):
+    """torch's default integers are 64 bits wide; read as 32 they are lengths
+    and zeros in turn."""
+    for name in ("scan", "scan_backward"):
+        fn, kw = calls()[name]
+        with pytest.raises(ValueError, match="int64"):
+            fn(**dict(kw, seq_lens=torch.tensor([200, 100])), stream=0)
+    assert not on_device.calls
