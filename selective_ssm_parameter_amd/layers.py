@@ -6,7 +6,8 @@ gradients of the gated scan, which may be column ranges of a wider tensor
 (unit stride along the channels, one row stride for all of them). All tensors
 of a call must lie on the current device, have the header's element types
 (``seq_lens`` int32) and hold at least the elements that ``dims`` asks for, else
-ValueError; work goes to that device's current stream unless ``stream`` is given.
+ValueError; work goes to that device's current stream unless ``stream`` (one of
+the same device) is given.
 """
 from __future__ import annotations
 
@@ -166,7 +167,12 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 def _stream(stream, dev):
     if stream is None:
         return _raw_stream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+    if isinstance(stream, int):
+        return stream
+    of = getattr(stream, "device_index", dev)
+    if of != dev:
+        raise ValueError(f"stream of device {of}, but the current device is cuda:{dev}")
+    return stream.cuda_stream
 
 
 def _ws(ws, ws_bytes):

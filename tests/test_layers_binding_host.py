@@ -182,3 +182,14 @@ def test_lengths_of_another_type_are_refused(on_device):
         with pytest.raises(ValueError, match="int64"):
             fn(**dict(kw, seq_lens=torch.tensor([200, 100])), stream=0)
     assert not on_device.calls
+
+
+def test_a_stream_of_another_device_is_refused(on_device):
+    class Other:
+        device_index, cuda_stream = 3, 0
+
+    for name in NAMES:
+        fn, kw = calls()[name]
+        with pytest.raises(ValueError, match="stream of device 3"):
+            fn(**kw, stream=Other())
+    assert not on_device.calls
