@@ -119,7 +119,10 @@ swimba_status swimba_layer_norm_backward(const swimba_dims* dims, const void* s,
  *   carry     float32 out of swimba_gated_scan_carry_size() bytes, or NULL:
  *             the states that the backward starts its chunks of tokens from
  *             (not written for chunks past a sequence's length)
- *   ws        workspace of SWIMBA_LAYER_GATED_SCAN
+ *   ws        workspace of SWIMBA_LAYER_GATED_SCAN. Chunks of tokens hand their
+ *             states on through it: calls that use one workspace at the same
+ *             time, which the conventions rule out, return SWIMBA_OK and give
+ *             wrong results, NaN after some ten seconds of waiting among them
  */
 swimba_status swimba_gated_scan(const swimba_dims* dims, const void* x, const void* forget,
                                 const void* gate, int64_t ld, const int32_t* seq_lens,
@@ -143,7 +146,8 @@ size_t swimba_gated_scan_carry_size(const swimba_dims* dims);
  *             gate and ignored without
  *   dh_init   [batch, C] float32 out, or NULL; may be the same tensor as
  *             dh_final
- *   ws        workspace of SWIMBA_LAYER_GATED_SCAN_BACKWARD
+ *   ws        workspace of SWIMBA_LAYER_GATED_SCAN_BACKWARD (used as the
+ *             forward's)
  */
 swimba_status swimba_gated_scan_backward(const swimba_dims* dims, const void* x,
                                          const void* forget, const void* gate, int64_t ld,

@@ -163,16 +163,15 @@ __device__ __forceinline__ void post(uint64_t* p, uint64_t v) {
 }
 // Waits for a word. It comes within microseconds unless another call works in
 // the same workspace at the same time, which the interface rules out; rather
-// than hang the device, the wait then ends after kWaitTicks with NaN.
-constexpr uint64_t kWaitTicks = 1000000000ull;  // 10 s of the 100 MHz clock
+// than hang the device, the wait then ends with NaN. It is bounded by its own
+// polls (a load past the caches each: some ten seconds in all), not by a clock,
+// which would run on while the queue is off the device.
+constexpr uint32_t kWaitPolls = 1u << 24;
 __device__ __forceinline__ uint64_t wait_for(const uint64_t* p) {
   uint64_t v = peek(p);
-  if (v == kUnset) {
-    const uint64_t t0 = wall_clock64();
-    do {
-      __builtin_amdgcn_s_sleep(1);
-      v = peek(p);
-    } while (v == kUnset && wall_clock64() - t0 < kWaitTicks);
+  for (uint32_t n = 0; v == kUnset && n < kWaitPolls; ++n) {
+    __builtin_amdgcn_s_sleep(1);
+    v = peek(p);
   }
   return v;
 }
