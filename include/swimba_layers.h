@@ -1,13 +1,14 @@
 /*
  * swimba_layers.h - C ABI of the layers around the Swimba mixer on MI355X.
  *
- * The pages put the mixer into a hybrid stack of recurrent layers and
+ * The pages put the mixer into a hybrid stack of Mamba-2, attention and
  * feed-forward layers and fine-tune it (papernotes.org notes, Experiments).
- * These calls are what such a layer needs next to the mixer of swimba.h: a
- * layer norm with the residual add, a gated linear recurrence over channels,
- * the gated feed-forward projection, the backward of each, and the backward
- * of swimba_output_project (the mixer's output projection and the
- * feed-forward layer's down projection).
+ * These calls are what such a stack needs next to the mixer of swimba.h: a
+ * layer norm with the residual add, the gated feed-forward projection, the
+ * backward of each, and the backward of swimba_output_project (the mixer's
+ * output projection and the feed-forward layer's down projection). The gated
+ * linear recurrence over channels is not on the pages: it is a neighbour of
+ * the scans of swimba.h, with a decay per channel and token and a backward.
  *
  * The conventions are those of swimba.h (device pointers, dense row-major
  * tensors unless a row stride is an argument, 16-byte alignment, caller-owned
@@ -189,8 +190,10 @@ swimba_status swimba_gated_project(const swimba_dims* dims, const void* x, const
  * and w_in, so that the forward keeps nothing:
  *   dg = dh u act'(g),  du = dh act(g),  dz = [dg | du],
  *   dx = dz w_in,   dw_in = dz^T x.
- * bf16 problems take dz into both products as the sum of two bf16 numbers (16
- * bits of it), so that dx and dw_in carry no bf16 rounding.
+ * bf16 problems take dz into both products as the sum of two bf16 numbers: an
+ * element is off by at most 2^-16 of itself, where float32 would hold 2^-24 and
+ * one bf16 2^-8, and dx by at most 2^-16 |dz| |w_in| from that (dw_in likewise).
+ * An element of dz above the largest bf16 number, 3.38e38, gives NaN there.
  *   x, w_in, act as given to the forward
  *   dh      [M, F] dtype
  *   dx      [M, D] float32 out;  dw_in [2 F, D] float32 out (zeros without tokens)

@@ -54,7 +54,8 @@ template <typename T>
 __device__ __forceinline__ float value(uint32_t bits) {
   return __uint_as_float(sizeof(T) == 4 ? bits : bits << 16);
 }
-// NT: stored past the L2's reuse order (nothing here reads it again), which took
+// NT: stored past the L2's reuse order (nothing here reads it again; the next
+// kernel sees the values as those of any store), which took
 // 43 -> 39 and 91 -> 77 us off a forward and backward of 8 x 2048 x 1536. Only
 // where every row starts on a 128-byte line: partial lines are better gathered in
 // L2 (3 x 1777 x 1001 fp32 backward: 43 us against 30).

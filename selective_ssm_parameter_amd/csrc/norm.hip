@@ -37,8 +37,10 @@ __device__ __forceinline__ void loadv(const T* p, float* v) {
     for (int i = 0; i < 4; ++i) v[i] = to_f32(r[i]);
   }
 }
-// Stored past the L2's reuse order: nothing here reads it again (62 -> 58 us for
-// the forward and backward of 16384 x 768).
+// Stored past the L2's reuse order: nothing here reads it again, and the next
+// kernel sees the values as those of any store (61 -> 57 us for the forward and
+// backward of 16384 x 768; with a device-wide scope as well, which writes each
+// half line of dx through, 85).
 template <typename T, int VEC>
 __device__ __forceinline__ void storev(T* p, const float* v) {
   if constexpr (VEC == 1) {
