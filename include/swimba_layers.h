@@ -193,7 +193,7 @@ swimba_status swimba_gated_project(const swimba_dims* dims, const void* x, const
  * bf16 problems take dz into both products as the sum of two bf16 numbers: an
  * element is off by at most 2^-16 of itself, where float32 would hold 2^-24 and
  * one bf16 2^-8, and dx by at most 2^-16 |dz| |w_in| from that (dw_in likewise).
- * An element of dz above the largest bf16 number, 3.38e38, gives NaN there.
+ * An element of dz that bf16 rounds to infinity (above 3.39e38) gives NaN there.
  *   x, w_in, act as given to the forward
  *   dh      [M, F] dtype
  *   dx      [M, D] float32 out;  dw_in [2 F, D] float32 out (zeros without tokens)

@@ -13,13 +13,14 @@
 // Tiles of 256 x 256 and 256 x 192 (8 waves), 128 x 128, 64 x 64, 32 x 64 and,
 // for gated products, 64 x 128 and 32 x 128 (4 waves), k steps of 32; two to
 // four LDS stages (DLay::NS), all but one filled ahead by buffer-to-LDS copies
-// that are waited for with a fixed count; fp32 accumulation in the matrix cores. The gated projection's backward recomputes g and u with the
-// forward's product and turns them into dz in the epilogue, in fp32; for bf16
-// problems dz then goes through both products as hi + lo, two bf16 numbers: 16
-// bits of dz, an element off by at most 2^-16 of itself, where one bf16 rounding
-// is off by 2^-8 (16384 x 768 -> 2 x 2048: dx and dw_in 2.5e-6 off in the 2-norm
-// instead of 2.5e-3; 24 bits, an fp32 product, 1.2e-6): each LDS stage holds both, three stages of them, and a
-// fragment of the other operand serves both.
+// that are waited for with a fixed count; fp32 accumulation in the matrix cores.
+// The gated projection's backward recomputes g and u with the forward's product
+// and turns them into dz in the epilogue, in fp32; for bf16 problems dz then
+// goes through both products as hi + lo, two bf16 numbers: 16 bits of dz, an
+// element off by at most 2^-16 of itself, where one bf16 rounding is off by
+// 2^-8 (16384 x 768 -> 2 x 2048: dx and dw_in 2.5e-6 off in the 2-norm, against
+// 2.5e-3 with one and 1.2e-6 with an fp32 product): each LDS stage holds both,
+// three stages of them, and a fragment of the other operand serves both.
 // Bound by the matrix cores for many tokens.
 #include <algorithm>
 #include <type_traits>

@@ -39,8 +39,7 @@ __device__ __forceinline__ void loadv(const T* p, float* v) {
 }
 // Stored past the L2's reuse order: nothing here reads it again, and the next
 // kernel sees the values as those of any store (61 -> 57 us for the forward and
-// backward of 16384 x 768; with a device-wide scope as well, which writes each
-// half line of dx through, 85).
+// backward of 16384 x 768).
 template <typename T, int VEC>
 __device__ __forceinline__ void storev(T* p, const float* v) {
   if constexpr (VEC == 1) {
