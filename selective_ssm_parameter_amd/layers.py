@@ -176,8 +176,12 @@ def _stream(stream, dev):
 
 
 def _ws(ws, ws_bytes):
-    return (ws.numel() * ws.element_size() if ws is not None else 0) if ws_bytes is None \
-        else ws_bytes
+    have = ws.numel() * ws.element_size() if ws is not None else 0
+    if ws_bytes is None:
+        return have
+    if ws_bytes > have:
+        raise ValueError(f"workspace of {have} bytes passed as one of {ws_bytes}")
+    return ws_bytes
 
 
 # ----------------------------------------------------------------- raw calls

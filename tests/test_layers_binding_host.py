@@ -193,3 +193,16 @@ def test_a_stream_of_another_device_is_refused(on_device):
         with pytest.raises(ValueError, match="stream of device 3"):
             fn(**kw, stream=Other())
     assert not on_device.calls
+
+
+def test_a_workspace_is_not_longer_than_its_tensor(on_device):
+    for name in ("norm_backward", "scan", "scan_backward", "project_backward", "output_backward"):
+        fn, kw = calls()[name]
+        n = kw["ws"].numel() * kw["ws"].element_size()
+        fn(**kw, ws_bytes=n, stream=0)
+        fn(**kw, ws_bytes=n - 16, stream=0)  # (the library refuses what is too little)
+        done = len(on_device.calls)
+        for ws, more in ((kw["ws"], n + 1), (None, 16)):
+            with pytest.raises(ValueError, match="workspace"):
+                fn(**dict(kw, ws=ws), ws_bytes=more, stream=0)
+        assert len(on_device.calls) == done
