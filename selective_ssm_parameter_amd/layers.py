@@ -161,7 +161,8 @@ def _rows(dev, *tensors, dt=None, M=0, C=0):
     return ptrs, ld
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# (a torch without GPU support lacks it, and loads this file all the same)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream, dev):

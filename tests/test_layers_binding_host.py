@@ -206,3 +206,11 @@ def test_a_workspace_is_not_longer_than_its_tensor(on_device):
             with pytest.raises(ValueError, match="workspace"):
                 fn(**dict(kw, ws=ws), ws_bytes=more, stream=0)
         assert len(on_device.calls) == done
+
+
+def test_loads_with_a_torch_without_gpu_support(monkeypatch):
+    import importlib.util
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    spec = importlib.util.spec_from_file_location("selective_ssm_parameter_amd._layers_again",
+                                                  sl.__file__)
+    spec.loader.exec_module(importlib.util.module_from_spec(spec))
