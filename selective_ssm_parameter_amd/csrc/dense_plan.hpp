@@ -17,6 +17,9 @@ constexpr int kBK = 32;  // k elements of a tile's step
 // `most`; `rest` is what a tile adds (first copies, epilogue, stores). Fitted to
 // products of 999 x 1016 x 480 and 4096 x 1024 x 1024 with each tile and of
 // 32768 x 8192 x 2048. fp32 stages of 256 rows do not fit LDS.
+// (At 14 sizes drawn at random, 77 to 13483 tokens and widths of 64 to 5024 in both
+// types, the planned tile took 3 to 5 % longer than the best one on average over
+// each kind of product, 23 % at worst: fp32 6855 x 352 -> 2 x 440, 55 against 45 us.)
 struct TileCost {
   int rows, cols, most;
   double busy, alone, rest;
