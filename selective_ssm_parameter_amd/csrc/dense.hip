@@ -681,11 +681,8 @@ hipError_t go(const char* name, const DenseArgs& A, hipStream_t s) {
   constexpr int SN = is_gated(MODE) ? C::BN / 2 : C::BN;
   const int64_t units = (int64_t)((A.R + C::BM - 1) / C::BM) * ((A.S + SN - 1) / SN) *
                         (is_gated(MODE) ? 1 : A.splits);
-  hipEvent_t e0, e1;
-  prof_kernel(name, &e0, &e1);
-  hipExtLaunchKernelGGL((dense_kernel<T, C, MODE, TO, SPLIT>),
-                        dim3((unsigned)((units + 7) / 8 * 8)), dim3(C::NTH), 0, s, e0, e1, 0, A);
-  return hipGetLastError();
+  return launch(name, dense_kernel<T, C, MODE, TO, SPLIT>, dim3((unsigned)((units + 7) / 8 * 8)),
+                dim3(C::NTH), 0, s, A);
 }
 
 template <typename T, Mode MODE>
@@ -704,21 +701,15 @@ constexpr int kSkinnyTokens = 64;
 template <typename T, int MT>
 hipError_t go_skinny(const DenseArgs& A, hipStream_t s) {
   const int units = (A.S + 15) / 16;
-  hipEvent_t e0, e1;
-  prof_kernel("gated_project", &e0, &e1);
   auto run = [&](auto kw) {
     constexpr int KW = decltype(kw)::value;
-    hipExtLaunchKernelGGL((gated_skinny_kernel<T, MT, KW>), dim3((unsigned)units), dim3(64 * KW),
-                          0, s, e0, e1, 0, A);
+    return launch("gated_project", gated_skinny_kernel<T, MT, KW>, dim3((unsigned)units),
+                  dim3(64 * KW), 0, s, A);
   };
   // (8 waves leave 256 registers each, which more tiles of tokens do not fit)
-  if constexpr (MT == 1) {
-    if (units < 192) run(std::integral_constant<int, 8>());
-    else run(std::integral_constant<int, 4>());
-  } else {
-    run(std::integral_constant<int, 4>());
-  }
-  return hipGetLastError();
+  if constexpr (MT == 1)
+    if (units < 192) return run(std::integral_constant<int, 8>());
+  return run(std::integral_constant<int, 4>());
 }
 
 template <typename T, Mode MODE, typename TO, bool SPLIT>
@@ -767,13 +758,10 @@ namespace {
 // The sum of a product's k runs (in ws) to out.
 template <typename TO>
 hipError_t sum_runs(const DenseArgs& A, const void* ws, void* out, hipStream_t s) {
-  hipEvent_t e0, e1;
-  prof_kernel("dense_sum", &e0, &e1);
   const size_t n4 = (size_t)A.R * A.S / 4;
   const unsigned blocks = (unsigned)std::min<size_t>((n4 + 255) / 256, 4096);
-  hipExtLaunchKernelGGL(dense_sum_kernel<TO>, dim3(blocks), dim3(256), 0, s, e0, e1, 0,
-                        (const float*)ws, A.splits, n4, (TO*)out);
-  return hipGetLastError();
+  return launch("dense_sum", dense_sum_kernel<TO>, dim3(blocks), dim3(256), 0, s, (const float*)ws,
+                A.splits, n4, (TO*)out);
 }
 
 }  // namespace

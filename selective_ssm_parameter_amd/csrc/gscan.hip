@@ -533,16 +533,14 @@ __global__ __launch_bounds__(256) void gscan_step_kernel(const T* __restrict__ x
 // BWD: the backward's kernel.
 template <typename T, bool BWD>
 hipError_t go(const GScanArgs& A, hipStream_t s) {
-  hipEvent_t e0, e1;
   const bool chain = gscan_chunks(A.T) > 1;
   if (chain) {
-    prof_kernel("gated_scan_unset", &e0, &e1);
     const size_t n = gscan_ws_bytes(A.Bt, A.T, A.C) / 16;
     const unsigned blocks = (unsigned)std::min<size_t>((n + 255) / 256, 2048);
-    hipExtLaunchKernelGGL(gscan_unset_kernel, dim3(blocks), dim3(256), 0, s, e0, e1, 0,
-                          (uint4*)A.ws, n);
+    const hipError_t e = launch("gated_scan_unset", gscan_unset_kernel, dim3(blocks), dim3(256), 0,
+                                s, (uint4*)A.ws, n);
+    if (e != hipSuccess) return e;
   }
-  prof_kernel(BWD ? "gated_scan_bwd" : "gated_scan", &e0, &e1);
   const dim3 grid((unsigned)gscan_blocks(A.Bt, A.T, A.C));
   // output rows that start on 128-byte lines
   auto lines = [](const void* t, int64_t ld) {
@@ -554,18 +552,17 @@ hipError_t go(const GScanArgs& A, hipStream_t s) {
     constexpr bool CH = decltype(chained)::value, GA = decltype(gated)::value,
                    NT = decltype(through)::value;
     if constexpr (BWD)
-      hipExtLaunchKernelGGL((gscan_bwd_kernel<T, CH, GA, NT>), grid, dim3(kTh), 0, s, e0, e1, 0, A);
+      return launch("gated_scan_bwd", gscan_bwd_kernel<T, CH, GA, NT>, grid, dim3(kTh), 0, s, A);
     else
-      hipExtLaunchKernelGGL((gscan_kernel<T, CH, GA, NT>), grid, dim3(kTh), 0, s, e0, e1, 0, A);
+      return launch("gated_scan", gscan_kernel<T, CH, GA, NT>, grid, dim3(kTh), 0, s, A);
   };
   const std::true_type yes{};
   const std::false_type no{};
   auto run_nt = [&](auto chained, auto gated) {
-    nt ? run(chained, gated, yes) : run(chained, gated, no);
+    return nt ? run(chained, gated, yes) : run(chained, gated, no);
   };
-  if (chain) A.o ? run_nt(yes, yes) : run_nt(yes, no);
-  else A.o ? run_nt(no, yes) : run_nt(no, no);
-  return hipGetLastError();
+  if (chain) return A.o ? run_nt(yes, yes) : run_nt(yes, no);
+  return A.o ? run_nt(no, yes) : run_nt(no, no);
 }
 
 }  // namespace
@@ -593,23 +590,18 @@ hipError_t launch_gscan_backward(bool is_bf16, const GScanArgs& a, hipStream_t s
 hipError_t launch_gscan_step(bool is_bf16, const void* x, const void* f, const void* o, int64_t ld,
                              const float* h_prev, float* h, void* y, int Bt, int C,
                              hipStream_t s) {
-  hipEvent_t e0, e1;
-  prof_kernel("gated_step", &e0, &e1);
   auto go = [&](auto tag, auto vec) {
     typedef decltype(tag) T;
     constexpr int VEC = decltype(vec)::value;
     const dim3 grid((unsigned)(((size_t)Bt * (C / VEC) + 255) / 256));
-    hipExtLaunchKernelGGL((gscan_step_kernel<T, VEC>), grid, dim3(256), 0, s, e0, e1, 0,
-                          (const T*)x, (const T*)f, (const T*)o, ld, h_prev, h, (T*)y, Bt, C);
+    return launch("gated_step", gscan_step_kernel<T, VEC>, grid, dim3(256), 0, s, (const T*)x,
+                  (const T*)f, (const T*)o, ld, h_prev, h, (T*)y, Bt, C);
   };
-  if (is_bf16) {
-    if (C % 4 == 0 && ld % 4 == 0) go(bf16(), std::integral_constant<int, 4>());
-    else go(bf16(), std::integral_constant<int, 1>());
-  } else {
-    if (C % 4 == 0 && ld % 4 == 0) go(0.f, std::integral_constant<int, 4>());
-    else go(0.f, std::integral_constant<int, 1>());
-  }
-  return hipGetLastError();
+  const std::integral_constant<int, 4> four{};
+  const std::integral_constant<int, 1> one{};
+  const bool by4 = C % 4 == 0 && ld % 4 == 0;
+  if (is_bf16) return by4 ? go(bf16(), four) : go(bf16(), one);
+  return by4 ? go(0.f, four) : go(0.f, one);
 }
 
 }  // namespace swimba

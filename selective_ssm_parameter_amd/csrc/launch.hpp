@@ -19,6 +19,25 @@ void prof_end(hipStream_t s);
 // are null, and the launch behaves as a plain one.
 void prof_kernel(const char* name, hipEvent_t* start, hipEvent_t* stop);
 
+// Launches a kernel, timed under `name` (see prof_kernel). Returns the error of
+// this launch alone: hipGetLastError would also give one that some earlier call
+// of the thread left behind.
+template <typename... P, typename... A>
+hipError_t launch(const char* name, void (*kernel)(P...), dim3 grid, dim3 block, size_t lds,
+                  hipStream_t s, A... a) {
+  static_assert(sizeof...(P) == sizeof...(A), "the kernel's parameters");
+  hipEvent_t e0, e1;
+  prof_kernel(name, &e0, &e1);
+  auto run = [&](P... p) {
+    void* args[] = {const_cast<void*>(static_cast<const void*>(&p))...};
+    return hipExtLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, args, lds, s, e0,
+                              e1, 0);
+  };
+  const hipError_t e = run(static_cast<P>(a)...);
+  if (e != hipSuccess) (void)hipGetLastError();  // reported here, and kept for nobody else
+  return e;
+}
+
 struct ProjGeom {
   int M, D, H, P, G, N, E, k, W;
   int bw_one = 0;  // B_hat without the routing weight (the separated-SSM layout)

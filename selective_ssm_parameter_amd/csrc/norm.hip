@@ -335,29 +335,23 @@ __global__ __launch_bounds__(32 * kDwSums) void norm_dw_kernel(const float* __re
 template <typename T, int VEC, int NT, int EPT>
 hipError_t fwd_cfg(const NormFwdArgs& a, hipStream_t s) {
   constexpr int RP = RowCfg<NT>::RP;
-  hipEvent_t e0, e1;
-  prof_kernel("layer_norm", &e0, &e1);
-  hipExtLaunchKernelGGL((norm_fwd_kernel<T, VEC, NT, EPT>), dim3((unsigned)((a.M + RP - 1) / RP)),
-                        dim3(RowCfg<NT>::TH), 0, s, e0, e1, 0, (const T*)a.x,
-                        (const T*)a.residual, (const T*)a.weight, (const T*)a.bias, a.eps,
-                        (T*)a.sum, (T*)a.y, a.mean, a.rstd, a.M, a.D);
-  return hipGetLastError();
+  return launch("layer_norm", norm_fwd_kernel<T, VEC, NT, EPT>,
+                dim3((unsigned)((a.M + RP - 1) / RP)), dim3(RowCfg<NT>::TH), 0, s, (const T*)a.x,
+                (const T*)a.residual, (const T*)a.weight, (const T*)a.bias, a.eps, (T*)a.sum,
+                (T*)a.y, a.mean, a.rstd, a.M, a.D);
 }
 
 template <typename T, typename TG, int VEC, int NT, int EPT>
 hipError_t bwd_cfg(const NormBwdArgs& a, hipStream_t s) {
   constexpr int RP = RowCfg<NT>::RP;
   const int np = norm_bwd_parts(a.M, a.D);
-  hipEvent_t e0, e1;
-  prof_kernel("layer_norm_backward", &e0, &e1);
-  hipExtLaunchKernelGGL((norm_bwd_kernel<T, TG, VEC, NT, EPT>), dim3((unsigned)np),
-                        dim3(RowCfg<NT>::TH), RP > 1 ? 2 * a.D * sizeof(float) : 0, s, e0, e1, 0,
-                        (const T*)a.s, (const T*)a.weight, a.mean, a.rstd, (const TG*)a.dy, a.dres,
-                        a.dx, a.part, a.M, a.D);
-  prof_kernel("layer_norm_dw", &e0, &e1);
-  hipExtLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((2 * a.D + 31) / 32)),
-                        dim3(32 * kDwSums), 0, s, e0, e1, 0, a.part, np, a.D, a.dw, a.db);
-  return hipGetLastError();
+  const hipError_t e =
+      launch("layer_norm_backward", norm_bwd_kernel<T, TG, VEC, NT, EPT>, dim3((unsigned)np),
+             dim3(RowCfg<NT>::TH), RP > 1 ? 2 * a.D * sizeof(float) : 0, s, (const T*)a.s,
+             (const T*)a.weight, a.mean, a.rstd, (const TG*)a.dy, a.dres, a.dx, a.part, a.M, a.D);
+  if (e != hipSuccess) return e;
+  return launch("layer_norm_dw", norm_dw_kernel, dim3((unsigned)((2 * a.D + 31) / 32)),
+                dim3(32 * kDwSums), 0, s, a.part, np, a.D, a.dw, a.db);
 }
 
 // Threads per row for E elements each; 1024 threads then take up to 32 each.

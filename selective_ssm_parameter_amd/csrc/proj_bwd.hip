@@ -473,8 +473,7 @@ __global__ void fill_zero_kernel(float* dst, size_t n) {
 hipError_t launch_fill_zero(float* dst, size_t n, hipStream_t s) {
   if (n == 0) return hipSuccess;
   const size_t blocks = std::min<size_t>((n + 255) / 256, 4096);
-  hipLaunchKernelGGL(fill_zero_kernel, dim3((unsigned)blocks), dim3(256), 0, s, dst, n);
-  return hipGetLastError();
+  return launch("fill_zero", fill_zero_kernel, dim3((unsigned)blocks), dim3(256), 0, s, dst, n);
 }
 
 // ---------------------------------------------------------------- launch

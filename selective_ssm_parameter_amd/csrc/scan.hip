@@ -1348,11 +1348,8 @@ __global__ void state_copy_kernel(const float* __restrict__ src, float* __restri
 
 hipError_t launch_state_copy(const float* src, float* dst, size_t n, hipStream_t s) {
   if (n == 0 || src == dst) return hipSuccess;
-  prof_begin("state_copy", s);
-  hipLaunchKernelGGL(state_copy_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, src,
-                     dst, n);
-  prof_end(s);
-  return hipGetLastError();
+  return launch("state_copy", state_copy_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0,
+                s, src, dst, n);
 }
 
 // Tuning knob (environment, read once): SWIMBA_SCAN_WGS = the most workgroups
