@@ -210,22 +210,22 @@ hipError_t launch_bucket(bool is_bf16, const int32_t* idx, const float* topk_w, 
   const size_t hl = (size_t)(E + 1) * sizeof(int);
   if (nblk > 0 && !counted) {
     prof_begin("bucket_count", s);
-    hipLaunchKernelGGL(bucket_count_kernel, dim3(nblk), dim3(256), hl, s, idx, pairs, E, counts);
+    enqueue(bucket_count_kernel, dim3(nblk), dim3(256), hl, s, idx, pairs, E, counts);
     prof_end(s);
   }
   const size_t pl = (size_t)(6 * (E + 1) + 256) * sizeof(int);
   prof_begin("bucket_place", s);
   const dim3 grid(nblk > 0 ? nblk : 1);
   if (is_bf16)
-    hipLaunchKernelGGL(bucket_place_kernel<f16>, grid, dim3(256), pl, s, idx, topk_w, pairs, E, bp,
-                       nblk, counts, bm, ntiles_max, offsets, tile_info, sorted, sorted_w,
-                       (f16*)X_hat, HP, (f16*)B_hat, GN, c_part);
+    enqueue(bucket_place_kernel<f16>, grid, dim3(256), pl, s, idx, topk_w, pairs, E, bp,
+            nblk, counts, bm, ntiles_max, offsets, tile_info, sorted, sorted_w,
+            (f16*)X_hat, HP, (f16*)B_hat, GN, c_part);
   else
-    hipLaunchKernelGGL(bucket_place_kernel<float>, grid, dim3(256), pl, s, idx, topk_w, pairs, E,
-                       bp, nblk, counts, bm, ntiles_max, offsets, tile_info, sorted, sorted_w,
-                       (float*)X_hat, HP, (float*)B_hat, GN, c_part);
+    enqueue(bucket_place_kernel<float>, grid, dim3(256), pl, s, idx, topk_w, pairs, E,
+            bp, nblk, counts, bm, ntiles_max, offsets, tile_info, sorted, sorted_w,
+            (float*)X_hat, HP, (float*)B_hat, GN, c_part);
   prof_end(s);
-  return hipGetLastError();
+  return enqueued();
 }
 
 }  // namespace swimba

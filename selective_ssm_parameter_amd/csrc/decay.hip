@@ -74,16 +74,16 @@ hipError_t launch_mix_decay(const int32_t* idx, const float* w, const float* a_e
   const dim3 grid((unsigned)((T + L - 1) / L), (unsigned)((H + 3) / 4), (unsigned)Bt);
   prof_begin("mix_decay", s);
   if (L <= 64)
-    hipLaunchKernelGGL(mix_decay_kernel<1>, grid, dim3(256), 0, s, idx, w, a_experts, ld, T, H,
-                       E, k, L);
+    enqueue(mix_decay_kernel<1>, grid, dim3(256), 0, s, idx, w, a_experts, ld, T, H,
+            E, k, L);
   else if (L <= 128)
-    hipLaunchKernelGGL(mix_decay_kernel<2>, grid, dim3(256), 0, s, idx, w, a_experts, ld, T, H,
-                       E, k, L);
+    enqueue(mix_decay_kernel<2>, grid, dim3(256), 0, s, idx, w, a_experts, ld, T, H,
+            E, k, L);
   else
-    hipLaunchKernelGGL(mix_decay_kernel<4>, grid, dim3(256), 0, s, idx, w, a_experts, ld, T, H,
-                       E, k, L);
+    enqueue(mix_decay_kernel<4>, grid, dim3(256), 0, s, idx, w, a_experts, ld, T, H,
+            E, k, L);
   prof_end(s);
-  return hipGetLastError();
+  return enqueued();
 }
 
 }  // namespace swimba

@@ -146,13 +146,13 @@ static void launch_decode_state_t(bool is_bf16, dim3 grid, const void* B_hat, co
                                   const float* c_part, const float* a, float* h, void* y, int H,
                                   int G, int k, hipStream_t s, DecayMix m) {
   if (is_bf16)
-    hipLaunchKernelGGL((decode_state_kernel<f16, bf16, N, KM>), grid, dim3(256), 0, s,
-                       (const f16*)B_hat, (const f16*)X_hat, c_part, a, h, (bf16*)y, H, G, k,
-                       m.idx, m.w, m.a_experts, m.E);
+    enqueue((decode_state_kernel<f16, bf16, N, KM>), grid, dim3(256), 0, s,
+            (const f16*)B_hat, (const f16*)X_hat, c_part, a, h, (bf16*)y, H, G, k,
+            m.idx, m.w, m.a_experts, m.E);
   else
-    hipLaunchKernelGGL((decode_state_kernel<float, float, N, KM>), grid, dim3(256), 0, s,
-                       (const float*)B_hat, (const float*)X_hat, c_part, a, h, (float*)y, H, G,
-                       k, m.idx, m.w, m.a_experts, m.E);
+    enqueue((decode_state_kernel<float, float, N, KM>), grid, dim3(256), 0, s,
+            (const float*)B_hat, (const float*)X_hat, c_part, a, h, (float*)y, H, G,
+            k, m.idx, m.w, m.a_experts, m.E);
 }
 
 template <int N>
@@ -187,7 +187,7 @@ hipError_t launch_decode_state(bool is_bf16, int Bt, int H, int G, int N, int P,
     default: launch_decode_state_n<128>(is_bf16, grid, B_hat, X_hat, c_part, a, h, y, H, G, k, s, m); break;
   }
   prof_end(s);
-  return hipGetLastError();
+  return enqueued();
 }
 
 }  // namespace swimba

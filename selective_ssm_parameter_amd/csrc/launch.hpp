@@ -19,15 +19,13 @@ void prof_end(hipStream_t s);
 // are null, and the launch behaves as a plain one.
 void prof_kernel(const char* name, hipEvent_t* start, hipEvent_t* stop);
 
-// Launches a kernel, timed under `name` (see prof_kernel). Returns the error of
+// Launches a kernel with start and stop events (or none) and returns the error of
 // this launch alone: hipGetLastError would also give one that some earlier call
-// of the thread left behind.
+// of the thread left behind, and end a call of several kernels half way.
 template <typename... P, typename... A>
-hipError_t launch(const char* name, void (*kernel)(P...), dim3 grid, dim3 block, size_t lds,
-                  hipStream_t s, A... a) {
+hipError_t launch_with(void (*kernel)(P...), dim3 grid, dim3 block, size_t lds, hipStream_t s,
+                       hipEvent_t e0, hipEvent_t e1, A... a) {
   static_assert(sizeof...(P) == sizeof...(A), "the kernel's parameters");
-  hipEvent_t e0, e1;
-  prof_kernel(name, &e0, &e1);
   auto run = [&](P... p) {
     void* args[] = {const_cast<void*>(static_cast<const void*>(&p))...};
     return hipExtLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, args, lds, s, e0,
@@ -35,6 +33,32 @@ hipError_t launch(const char* name, void (*kernel)(P...), dim3 grid, dim3 block,
   };
   const hipError_t e = run(static_cast<P>(a)...);
   if (e != hipSuccess) (void)hipGetLastError();  // reported here, and kept for nobody else
+  return e;
+}
+// The same, timed under `name` (see prof_kernel).
+template <typename... P, typename... A>
+hipError_t launch(const char* name, void (*kernel)(P...), dim3 grid, dim3 block, size_t lds,
+                  hipStream_t s, A... a) {
+  hipEvent_t e0, e1;
+  prof_kernel(name, &e0, &e1);
+  return launch_with(kernel, grid, block, lds, s, e0, e1, a...);
+}
+// The same in a row: enqueued() returns the first error among the launches since
+// it was last asked on this thread. A launcher that enqueues ends with it.
+inline thread_local hipError_t t_enqueued = hipSuccess;
+template <typename... P, typename... A>
+void enqueue_timed(void (*kernel)(P...), dim3 grid, dim3 block, size_t lds, hipStream_t s,
+                   hipEvent_t e0, hipEvent_t e1, A... a) {
+  const hipError_t e = launch_with(kernel, grid, block, lds, s, e0, e1, a...);
+  if (t_enqueued == hipSuccess) t_enqueued = e;
+}
+template <typename... P, typename... A>
+void enqueue(void (*kernel)(P...), dim3 grid, dim3 block, size_t lds, hipStream_t s, A... a) {
+  enqueue_timed(kernel, grid, block, lds, s, nullptr, nullptr, a...);
+}
+inline hipError_t enqueued() {
+  const hipError_t e = t_enqueued;
+  t_enqueued = hipSuccess;
   return e;
 }
 

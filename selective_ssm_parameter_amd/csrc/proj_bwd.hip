@@ -484,35 +484,35 @@ template <typename T, typename S>
 static hipError_t launch_pbwd_t(const ProjBwdArgs& A, hipStream_t s) {
   const int pairs = A.M * A.k;
   prof_begin("proj_bwd_dz", s);
-  hipLaunchKernelGGL((pbwd_dz_kernel<T, S>), dim3((unsigned)((pairs + 3) / 4)), dim3(256), 0, s, A);
+  enqueue((pbwd_dz_kernel<T, S>), dim3((unsigned)((pairs + 3) / 4)), dim3(256), 0, s, A);
   prof_end(s);
   prof_begin("proj_bwd_router", s);
-  hipLaunchKernelGGL(pbwd_router_kernel<T>, dim3((unsigned)((A.M + kRouterTok - 1) / kRouterTok)),
-                     dim3(256), 0, s, A);
+  enqueue(pbwd_router_kernel<T>, dim3((unsigned)((A.M + kRouterTok - 1) / kRouterTok)),
+          dim3(256), 0, s, A);
   prof_end(s);
   const int ncol = (A.D + kGB - 1) / kGB;
   // row tiles over all experts: sum_e ceil(n_e / 128) <= pairs / 128 + E
   const int ntr = pairs / kGB + A.E;
   prof_begin("proj_bwd_du", s);
-  hipLaunchKernelGGL((pbwd_gemm_kernel<T, 0>), dim3((unsigned)((ntr * ncol + 7) / 8 * 8)),
-                     dim3(256), 0, s, A);
+  enqueue((pbwd_gemm_kernel<T, 0>), dim3((unsigned)((ntr * ncol + 7) / 8 * 8)),
+          dim3(256), 0, s, A);
   prof_end(s);
   prof_begin("proj_bwd_du_sum", s);
-  hipLaunchKernelGGL(pbwd_du_sum_kernel, dim3((unsigned)(((size_t)A.M * A.D / 4 + 255) / 256)),
-                     dim3(256), 0, s, A);
+  enqueue(pbwd_du_sum_kernel, dim3((unsigned)(((size_t)A.M * A.D / 4 + 255) / 256)),
+          dim3(256), 0, s, A);
   prof_end(s);
   const int nwt = (A.W + kGB - 1) / kGB;
   prof_begin("proj_bwd_dw", s);
-  hipLaunchKernelGGL((pbwd_gemm_kernel<T, 1>), dim3((unsigned)((A.E * nwt * ncol + 7) / 8 * 8)),
-                     dim3(256), 0, s, A);
+  enqueue((pbwd_gemm_kernel<T, 1>), dim3((unsigned)((A.E * nwt * ncol + 7) / 8 * 8)),
+          dim3(256), 0, s, A);
   prof_end(s);
   prof_begin("proj_bwd_dwr", s);
-  hipLaunchKernelGGL(pbwd_dwr_kernel<T>, dim3((unsigned)((A.D + 63) / 64), (unsigned)A.nsplit),
-                     dim3(256), 0, s, A);
-  hipLaunchKernelGGL(pbwd_dwr_sum_kernel, dim3((unsigned)(((size_t)A.E * A.D + 63) / 64)),
-                     dim3(64), 0, s, A);
+  enqueue(pbwd_dwr_kernel<T>, dim3((unsigned)((A.D + 63) / 64), (unsigned)A.nsplit),
+          dim3(256), 0, s, A);
+  enqueue(pbwd_dwr_sum_kernel, dim3((unsigned)(((size_t)A.E * A.D + 63) / 64)),
+          dim3(64), 0, s, A);
   prof_end(s);
-  return hipGetLastError();
+  return enqueued();
 }
 
 hipError_t launch_project_backward(bool is_bf16, ProjBwdArgs A, hipStream_t s) {

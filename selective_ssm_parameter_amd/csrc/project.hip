@@ -681,15 +681,14 @@ static hipError_t launch_proj_cfg(const ProjGeom& g, const T* u, const T* wexp,
   hipEvent_t e0, e1;
   prof_kernel("expert_project", &e0, &e1);
   if (g.D % (kProjStages * ProjLay<T, C>::BK) == 0)
-    hipExtLaunchKernelGGL((proj_kernel<T, C, false, float, true>), grid, dim3(C::NTH), 0, s, e0, e1,
-                          0, u, wexp, sorted, sorted_w, tile_info, g.M, g.D, g.W, g.HP(), g.GN(),
-                          g.k, nrow, X_hat, B_hat, c_part, (float*)nullptr, g.bw_one,
-                          proj_group_rows());
+    enqueue_timed((proj_kernel<T, C, false, float, true>), grid, dim3(C::NTH), 0, s, e0, e1, u,
+                  wexp, sorted, sorted_w, tile_info, g.M, g.D, g.W, g.HP(), g.GN(), g.k, nrow,
+                  X_hat, B_hat, c_part, (float*)nullptr, g.bw_one, proj_group_rows());
   else
-    hipExtLaunchKernelGGL((proj_kernel<T, C>), grid, dim3(C::NTH), 0, s, e0, e1, 0, u, wexp, sorted,
-                          sorted_w, tile_info, g.M, g.D, g.W, g.HP(), g.GN(), g.k, nrow, X_hat,
-                          B_hat, c_part, (float*)nullptr, g.bw_one, proj_group_rows());
-  return hipGetLastError();
+    enqueue_timed((proj_kernel<T, C>), grid, dim3(C::NTH), 0, s, e0, e1, u, wexp, sorted,
+                  sorted_w, tile_info, g.M, g.D, g.W, g.HP(), g.GN(), g.k, nrow, X_hat,
+                  B_hat, c_part, (float*)nullptr, g.bw_one, proj_group_rows());
+  return enqueued();
 }
 
 template <typename T>
@@ -707,11 +706,11 @@ static hipError_t launch_project_t(const ProjGeom& g, const T* u, const T* wexp,
       const int ntiles = nrow * ((g.W + kSkBN - 1) / kSkBN);
       hipEvent_t e0, e1;
       prof_kernel("expert_project", &e0, &e1);
-      hipExtLaunchKernelGGL(proj_skinny_kernel<false>, dim3((unsigned)((ntiles + 7) / 8 * 8)),
-                            dim3(256), 0, s, e0, e1, 0, u, wexp, sorted, sorted_w, ti, g.M, g.D,
-                            g.W, g.HP(), g.GN(), g.k, nrow, X_hat, B_hat, c_part, g.bw_one,
-                            (const int32_t*)nullptr, (const float*)nullptr, g.E);
-      err = hipGetLastError();
+      enqueue_timed(proj_skinny_kernel<false>, dim3((unsigned)((ntiles + 7) / 8 * 8)),
+                    dim3(256), 0, s, e0, e1, u, wexp, sorted, sorted_w, ti, g.M, g.D,
+                    g.W, g.HP(), g.GN(), g.k, nrow, X_hat, B_hat, c_part, g.bw_one,
+                    (const int32_t*)nullptr, (const float*)nullptr, g.E);
+      err = enqueued();
     } else if (bm == 256)
       err = launch_proj_cfg<T, ProjBig>(g, u, wexp, sorted, sorted_w, ti, B_hat, X_hat, c_part, s);
     else if (bm == 128)
@@ -725,13 +724,13 @@ static hipError_t launch_project_t(const ProjGeom& g, const T* u, const T* wexp,
       err = launch_proj_cfg<T, ProjSmall>(g, u, wexp, sorted, sorted_w, ti, B_hat, X_hat, c_part, s);
   }
   if (err != hipSuccess) return err;
-  if (!C_mix) return hipGetLastError();
+  if (!C_mix) return enqueued();
   const size_t n4 = (size_t)g.M * g.GN() / 4;
   prof_begin("mix_c", s);
-  hipLaunchKernelGGL(mix_c_kernel<S>, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s, c_part,
-                     g.M, g.k, g.GN(), C_mix);
+  enqueue(mix_c_kernel<S>, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s, c_part,
+          g.M, g.k, g.GN(), C_mix);
   prof_end(s);
-  return hipGetLastError();
+  return enqueued();
 }
 
 // Output projection out[M, N] = y[M, K] w_out[N, K]^T (fp32 accumulation, out in
@@ -745,17 +744,17 @@ static hipError_t launch_outproj_cfg(int M, int K, int N, const T* y, const T* w
   const dim3 grid((unsigned)((units + 7) / 8 * 8));
   typedef typename StreamOf<T>::type S;
   if (K % (kProjStages * ProjLay<T, C>::BK) == 0)
-    hipLaunchKernelGGL((proj_kernel<T, C, true, T, true>), grid, dim3(C::NTH), 0, s, y, w,
-                       (const int32_t*)nullptr, (const float*)nullptr, (const int4v*)nullptr, M, K,
-                       N, 0, 0, 1, nrow, (S*)nullptr, (S*)nullptr, (float*)nullptr, out, 0,
-                       proj_group_rows());
+    enqueue((proj_kernel<T, C, true, T, true>), grid, dim3(C::NTH), 0, s, y, w,
+            (const int32_t*)nullptr, (const float*)nullptr, (const int4v*)nullptr, M, K,
+            N, 0, 0, 1, nrow, (S*)nullptr, (S*)nullptr, (float*)nullptr, out, 0,
+            proj_group_rows());
   else
-    hipLaunchKernelGGL((proj_kernel<T, C, true, T>), grid, dim3(C::NTH), 0, s, y, w,
-                       (const int32_t*)nullptr, (const float*)nullptr, (const int4v*)nullptr, M, K,
-                       N, 0, 0, 1, nrow, (S*)nullptr, (S*)nullptr, (float*)nullptr, out, 0,
-                       proj_group_rows());
+    enqueue((proj_kernel<T, C, true, T>), grid, dim3(C::NTH), 0, s, y, w,
+            (const int32_t*)nullptr, (const float*)nullptr, (const int4v*)nullptr, M, K,
+            N, 0, 0, 1, nrow, (S*)nullptr, (S*)nullptr, (float*)nullptr, out, 0,
+            proj_group_rows());
   prof_end(s);
-  return hipGetLastError();
+  return enqueued();
 }
 
 hipError_t launch_output_project(bool is_bf16, int M, int K, int N, const void* y,
@@ -783,12 +782,12 @@ hipError_t launch_project_direct(const ProjGeom& g, const void* u, const void* w
   const int units = g.E * ((g.W + kSkBN - 1) / kSkBN);
   hipEvent_t e0, e1;
   prof_kernel("expert_project", &e0, &e1);
-  hipExtLaunchKernelGGL(proj_skinny_kernel<true>, dim3((unsigned)((units + 7) / 8 * 8)), dim3(256),
-                        0, s, e0, e1, 0, (const bf16*)u, (const bf16*)w_experts,
-                        (const int32_t*)nullptr, (const float*)nullptr, (const int4v*)nullptr, g.M,
-                        g.D, g.W, g.HP(), g.GN(), g.k, 0, (f16*)X_hat, (f16*)B_hat, c_part,
-                        g.bw_one, idx, topk_w, g.E);
-  return hipGetLastError();
+  enqueue_timed(proj_skinny_kernel<true>, dim3((unsigned)((units + 7) / 8 * 8)), dim3(256),
+                0, s, e0, e1, (const bf16*)u, (const bf16*)w_experts,
+                (const int32_t*)nullptr, (const float*)nullptr, (const int4v*)nullptr, g.M,
+                g.D, g.W, g.HP(), g.GN(), g.k, 0, (f16*)X_hat, (f16*)B_hat, c_part,
+                g.bw_one, idx, topk_w, g.E);
+  return enqueued();
 }
 
 hipError_t launch_project(bool is_bf16, const ProjGeom& g, const void* u, const void* w_experts,

@@ -306,8 +306,8 @@ hipError_t launch_route(bool is_bf16, const void* u, const void* w_router, int M
     if (err != hipSuccess) return err;
     prof_begin("route_topk", s);
 #define SWIMBA_ROUTE_BIG(TT, G, RBQ)                                                           \
-  hipLaunchKernelGGL((route_big_kernel<TT, G, RBQ>), grid, dim3(256), lds, s, (const TT*)u,   \
-                     (const TT*)w_router, M, D, E, k, idx, w, logits)
+  enqueue((route_big_kernel<TT, G, RBQ>), grid, dim3(256), lds, s, (const TT*)u,   \
+          (const TT*)w_router, M, D, E, k, idx, w, logits)
     if (is_bf16) {
       if (ET > 2) SWIMBA_ROUTE_BIG(bf16, 4, 2);
       else if (ET > 1) SWIMBA_ROUTE_BIG(bf16, 2, 2);
@@ -319,7 +319,7 @@ hipError_t launch_route(bool is_bf16, const void* u, const void* w_router, int M
     }
 #undef SWIMBA_ROUTE_BIG
     prof_end(s);
-    return hipGetLastError();
+    return enqueued();
   }
   const int tpw = route_tokens_per_wg(M);
   const int ET = (E + 15) / 16;
@@ -346,8 +346,8 @@ hipError_t launch_route(bool is_bf16, const void* u, const void* w_router, int M
   if (err != hipSuccess) return err;
   prof_begin("route_topk", s);
 #define SWIMBA_ROUTE(TT, G, W)                                                                  \
-  hipLaunchKernelGGL((route_kernel<TT, G, W>), grid, block, lds, s, (const TT*)u,              \
-                     (const TT*)w_router, M, D, E, k, idx, w, logits, hist, tpw, ksplit)
+  enqueue((route_kernel<TT, G, W>), grid, block, lds, s, (const TT*)u,              \
+          (const TT*)w_router, M, D, E, k, idx, w, logits, hist, tpw, ksplit)
 #define SWIMBA_ROUTE_T(TT)                       \
   if (wide) {                                    \
     if (GT == 2) SWIMBA_ROUTE(TT, 2, 16);        \
@@ -363,7 +363,7 @@ hipError_t launch_route(bool is_bf16, const void* u, const void* w_router, int M
 #undef SWIMBA_ROUTE_T
 #undef SWIMBA_ROUTE
   prof_end(s);
-  return hipGetLastError();
+  return enqueued();
 }
 
 }  // namespace swimba

@@ -1480,11 +1480,11 @@ static hipError_t launch_scan_t(const ScanGeom& g, ScanArgs args, hipStream_t s)
   prof_begin("scan_gram", s);
   const int diag = (sizeof(T) == 2 && KS <= 2 && !TV && g.walk == 1) ? 1 : 0;
   const int ng = (diag ? g.L / BT : args.npairs) * g.G * args.nc * g.Bt;
-  hipLaunchKernelGGL((scan_gram_kernel<T, NP, KS, BT>), dim3((unsigned)((ng + 7) / 8 * 8)),
-                     dim3(256), 0, s, static_cast<const T*>(args.B_hat),
-                     static_cast<const T*>(args.C_mix), static_cast<T*>(const_cast<void*>(args.gram)),
-                     g.T, g.G, g.N, g.L, args.nc, args.npairs, g.Bt,
-                     diag);
+  enqueue((scan_gram_kernel<T, NP, KS, BT>), dim3((unsigned)((ng + 7) / 8 * 8)),
+          dim3(256), 0, s, static_cast<const T*>(args.B_hat),
+          static_cast<const T*>(args.C_mix), static_cast<T*>(const_cast<void*>(args.gram)),
+          g.T, g.G, g.N, g.L, args.nc, args.npairs, g.Bt,
+          diag);
   prof_end(s);
   if (g.segs > 1) {
     prof_begin("scan_segment_state", s);
@@ -1492,21 +1492,21 @@ static hipError_t launch_scan_t(const ScanGeom& g, ScanArgs args, hipStream_t s)
     if constexpr (sizeof(T) == 2 && KS <= 2 && !TV) {
       if (carry_two(g)) {
         const int n1 = (g.H / 2) * (g.segs - 1) * g.sub * g.Bt;
-        hipLaunchKernelGGL((scan_carry_kernel<T, NP, KS, BT>), dim3((unsigned)((n1 + 7) / 8 * 8)),
-                           dim3(kCarryThreads), 0, s, args);
+        enqueue((scan_carry_kernel<T, NP, KS, BT>), dim3((unsigned)((n1 + 7) / 8 * 8)),
+                dim3(kCarryThreads), 0, s, args);
         done = true;
       }
     }
     if (!done) {
       const int n1 = g.H * (g.segs - 1) * g.sub * g.Bt;
-      hipLaunchKernelGGL(k1, dim3((unsigned)((n1 + 7) / 8 * 8)), dim3(kScanThreads), l1, s, args);
+      enqueue(k1, dim3((unsigned)((n1 + 7) / 8 * 8)), dim3(kScanThreads), l1, s, args);
     }
     prof_end(s);
     const int NPsz = g.N * g.P;
     prof_begin("scan_state_pass", s);
-    hipLaunchKernelGGL(scan_combine_kernel, dim3((NPsz / 4 + 255) / 256, g.H, g.Bt), dim3(256), 0,
-                       s, args.a, args.h_init, args.ws, g.H, NPsz, g.T, g.L,
-                       (g.segs - 1) * g.sub + 1, g.seg_chunks / g.sub, args.ld);
+    enqueue(scan_combine_kernel, dim3((NPsz / 4 + 255) / 256, g.H, g.Bt), dim3(256), 0,
+            s, args.a, args.h_init, args.ws, g.H, NPsz, g.T, g.L,
+            (g.segs - 1) * g.sub + 1, g.seg_chunks / g.sub, args.ld);
     prof_end(s);
   }
   hipEvent_t e0, e1;
@@ -1514,16 +1514,14 @@ static hipError_t launch_scan_t(const ScanGeom& g, ScanArgs args, hipStream_t s)
   if constexpr (sizeof(T) == 2 && KS <= 2 && !TV) {
     if (g.walk == 1) {
       const int n3 = (g.H / 2) * g.segs * g.Bt;
-      hipExtLaunchKernelGGL((scan_block_kernel<T, TY, NP, KS, BT>),
-                            dim3((unsigned)((n3 + 7) / 8 * 8)), dim3(kBlockThreads), 0, s, e0, e1,
-                            0, args);
-      return hipGetLastError();
+      enqueue_timed((scan_block_kernel<T, TY, NP, KS, BT>),
+                    dim3((unsigned)((n3 + 7) / 8 * 8)), dim3(kBlockThreads), 0, s, e0, e1, args);
+      return enqueued();
     }
   }
   const int n3 = g.H * g.segs * g.Bt;
-  hipExtLaunchKernelGGL(k3, dim3((unsigned)((n3 + 7) / 8 * 8)), dim3(kScanThreads), l3, s, e0, e1,
-                        0, args);
-  return hipGetLastError();
+  enqueue_timed(k3, dim3((unsigned)((n3 + 7) / 8 * 8)), dim3(kScanThreads), l3, s, e0, e1, args);
+  return enqueued();
 }
 
 template <typename T, typename TY, int NP, int KS>

@@ -890,7 +890,7 @@ template <typename T, typename S, typename TY, int NP, int KS, int BL>
 static hipError_t launch_bwd_t(const BwdArgs& A, int Bt, hipStream_t s) {
   const dim3 g1((unsigned)A.nb, (unsigned)A.H, (unsigned)Bt);
   prof_begin("scan_bwd_local", s);
-  hipLaunchKernelGGL((bwd_local_kernel<T, S, TY, NP, KS, BL>), g1, dim3(256), 0, s, A);
+  enqueue((bwd_local_kernel<T, S, TY, NP, KS, BL>), g1, dim3(256), 0, s, A);
   prof_end(s);
   prof_begin("scan_bwd_sweep", s);
   {
@@ -900,28 +900,28 @@ static hipError_t launch_bwd_t(const BwdArgs& A, int Bt, hipStream_t s) {
     const bool narrow = (size_t)Bt * A.H * A.N * kBP / V16 < (size_t)131072;
     const int V = narrow ? 4 : V16;
     const dim3 gs((unsigned)((A.N * kBP / V + 255) / 256), A.H, Bt);
-    if (narrow) hipLaunchKernelGGL((bwd_sweep_kernel<T, BL, 4>), gs, dim3(256), 0, s, A);
-    else hipLaunchKernelGGL((bwd_sweep_kernel<T, BL, V16>), gs, dim3(256), 0, s, A);
+    if (narrow) enqueue((bwd_sweep_kernel<T, BL, 4>), gs, dim3(256), 0, s, A);
+    else enqueue((bwd_sweep_kernel<T, BL, V16>), gs, dim3(256), 0, s, A);
   }
   prof_end(s);
   prof_begin("scan_bwd_grad", s);
-  hipLaunchKernelGGL((bwd_grad_kernel<T, S, TY, NP, KS, BL>),
-                     dim3((unsigned)A.nb, (unsigned)(A.G * A.hs), (unsigned)Bt),
-                     dim3(64 * kGradWaves), 0, s, A);
+  enqueue((bwd_grad_kernel<T, S, TY, NP, KS, BL>),
+          dim3((unsigned)A.nb, (unsigned)(A.G * A.hs), (unsigned)Bt),
+          dim3(64 * kGradWaves), 0, s, A);
   prof_end(s);
   if (A.hs > 1) {
     const size_t M = (size_t)Bt * A.T;
     const size_t nb4 = M * A.k * A.G * A.N / 4, nc4 = M * A.G * A.N / 4;
     prof_begin("scan_bwd_slice_sum", s);
-    hipLaunchKernelGGL(bwd_slice_sum_kernel, dim3((unsigned)((nb4 + nc4 + 255) / 256)),
-                       dim3(256), 0, s, A.dBp, A.dCp, A.dB, A.dC, nb4, nc4, A.hs);
+    enqueue(bwd_slice_sum_kernel, dim3((unsigned)((nb4 + nc4 + 255) / 256)),
+            dim3(256), 0, s, A.dBp, A.dCp, A.dB, A.dC, nb4, nc4, A.hs);
     prof_end(s);
   }
   prof_begin("scan_bwd_da", s);
-  hipLaunchKernelGGL(bwd_da_kernel, dim3((unsigned)A.H), dim3(64), 0, s, A.da_part, A.da, Bt,
-                     A.nb, A.H);
+  enqueue(bwd_da_kernel, dim3((unsigned)A.H), dim3(64), 0, s, A.da_part, A.da, Bt,
+          A.nb, A.H);
   prof_end(s);
-  return hipGetLastError();
+  return enqueued();
 }
 
 template <typename T, typename S, typename TY, int NP>
@@ -952,16 +952,16 @@ hipError_t launch_scan_backward(bool is_bf16, int Bt, int T, int H, int G, int N
                                 float* dh_init, void* ws, hipStream_t s) {
   if (Bt == 0) {
     if (H > 0)
-      hipLaunchKernelGGL(bwd_empty_kernel, dim3((unsigned)((H + 255) / 256)), dim3(256), 0, s,
-                         nullptr, nullptr, da, (size_t)0, H);
-    return hipGetLastError();
+      enqueue(bwd_empty_kernel, dim3((unsigned)((H + 255) / 256)), dim3(256), 0, s,
+              nullptr, nullptr, da, (size_t)0, H);
+    return enqueued();
   }
   if (T == 0) {
     const size_t n = (size_t)Bt * H * N * kBP;
     const size_t m = n > (size_t)H ? n : (size_t)H;
-    hipLaunchKernelGGL(bwd_empty_kernel, dim3((unsigned)((m + 255) / 256)), dim3(256), 0, s,
-                       dh_final, dh_init, da, n, H);
-    return hipGetLastError();
+    enqueue(bwd_empty_kernel, dim3((unsigned)((m + 255) / 256)), dim3(256), 0, s,
+            dh_final, dh_init, da, n, H);
+    return enqueued();
   }
   const int BL = scan_bwd_block(is_bf16);
   const int nb = (T + BL - 1) / BL;

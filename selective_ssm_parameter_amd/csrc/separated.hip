@@ -85,15 +85,15 @@ hipError_t launch_sep_scatter(bool is_bf16, const int32_t* idx, const void* X_ha
   if (n == 0) return hipSuccess;
   prof_begin("sep_scatter", s);
   if (is_bf16)
-    hipLaunchKernelGGL(sep_scatter_kernel<f16>, dim3(grid_for(n)), dim3(256), 0, s, idx,
-                       (const f16*)X_hat, (const f16*)B_hat, c_part, Bt, T, E, k, HP, GN, (f16*)Xs,
-                       (f16*)Bs, (f16*)Cs);
+    enqueue(sep_scatter_kernel<f16>, dim3(grid_for(n)), dim3(256), 0, s, idx,
+            (const f16*)X_hat, (const f16*)B_hat, c_part, Bt, T, E, k, HP, GN, (f16*)Xs,
+            (f16*)Bs, (f16*)Cs);
   else
-    hipLaunchKernelGGL(sep_scatter_kernel<float>, dim3(grid_for(n)), dim3(256), 0, s, idx,
-                       (const float*)X_hat, (const float*)B_hat, c_part, Bt, T, E, k, HP, GN,
-                       (float*)Xs, (float*)Bs, (float*)Cs);
+    enqueue(sep_scatter_kernel<float>, dim3(grid_for(n)), dim3(256), 0, s, idx,
+            (const float*)X_hat, (const float*)B_hat, c_part, Bt, T, E, k, HP, GN,
+            (float*)Xs, (float*)Bs, (float*)Cs);
   prof_end(s);
-  return hipGetLastError();
+  return enqueued();
 }
 
 hipError_t launch_sep_sum(bool is_bf16, const float* yp, int Bt, int T, int E, int HP, void* y,
@@ -102,13 +102,13 @@ hipError_t launch_sep_sum(bool is_bf16, const float* yp, int Bt, int T, int E, i
   if (n4 == 0) return hipSuccess;
   prof_begin("sep_sum", s);
   if (is_bf16)
-    hipLaunchKernelGGL(sep_sum_kernel<bf16>, dim3(grid_for(n4)), dim3(256), 0, s, yp, Bt, T, E, HP,
-                       (bf16*)y);
+    enqueue(sep_sum_kernel<bf16>, dim3(grid_for(n4)), dim3(256), 0, s, yp, Bt, T, E, HP,
+            (bf16*)y);
   else
-    hipLaunchKernelGGL(sep_sum_kernel<float>, dim3(grid_for(n4)), dim3(256), 0, s, yp, Bt, T, E,
-                       HP, (float*)y);
+    enqueue(sep_sum_kernel<float>, dim3(grid_for(n4)), dim3(256), 0, s, yp, Bt, T, E,
+            HP, (float*)y);
   prof_end(s);
-  return hipGetLastError();
+  return enqueued();
 }
 
 }  // namespace swimba

@@ -75,3 +75,54 @@ def test_an_earlier_error_is_not_the_calls_own():
         hip.hipGetLastError()
     torch.cuda.synchronize()
     assert not failed, failed
+
+
+def test_an_earlier_error_is_not_the_mixers_own():
+    from gpu_util import upload
+    from selective_ssm_parameter_amd import synth
+    hip = sl.lib()
+    hip.hipSetDevice.restype = hip.hipGetLastError.restype = ctypes.c_int
+    wl = synth.small("errors", 51, batch=2, seqlen=200, d_model=128, nheads=2, headdim=64,
+                     dstate=64, ngroups=1, n_experts=4, top_k=2, chunk=64, dtype=synth.BF16,
+                     a_lo=0.9, a_hi=0.999)
+    d = upload(wl, synth.make_inputs(wl))
+    dims, one = sb.dims_of(wl), sb.dims_of(wl, seqlen=1)
+    buf, grads, sep = sb.alloc_buffers(dims), sb.alloc_grads(dims), sb.alloc_separated(dims)
+    a_exp = torch.rand(wl.n_experts, wl.nheads, device="cuda")
+    log_decay = torch.empty(wl.batch, wl.nheads, wl.seqlen, device="cuda")
+    w_out = torch.randn(wl.d_model, wl.d_inner, device="cuda").bfloat16()
+    out = torch.empty(wl.tokens, wl.d_model, device="cuda", dtype=torch.bfloat16)
+    ws, _ = sb.workspace(one, sb.CALL_DECODE, "cuda")
+    h = torch.zeros(wl.batch, wl.nheads, wl.dstate, 64, device="cuda")
+    y1 = torch.empty(wl.batch, wl.nheads, 64, dtype=torch.bfloat16, device="cuda")
+    u1 = d["u"][:wl.batch].contiguous()
+    dy = torch.randn(wl.tokens, wl.nheads, 64, device="cuda").bfloat16()
+    w = (d["u"], d["w_router"], d["w_experts"])
+    y = buf.y.view(wl.tokens, wl.d_inner)
+    calls = {
+        "forward": lambda: sb.forward(dims, *w, d["a"], None, buf),
+        "forward_mixed": lambda: sb.forward_mixed(dims, *w, a_exp, None, buf, log_decay),
+        "output_project": lambda: sb.swimba_output_project(dims, y, w_out, out),
+        "backward": lambda: sb.backward(dims, *w, d["a"], None, dy, None, buf, grads),
+        "decode": lambda: sb.swimba_decode_step(one, u1, w[1], w[2], d["a"], h, y1, None, ws),
+        "separated": lambda: sb.separated_forward(dims, *w, d["a"], None, sep),
+    }
+    for c in calls.values():
+        c()
+    torch.cuda.synchronize()
+    failed = []
+    stream = torch.cuda.current_stream().cuda_stream  # (asked for without an error before it)
+    real = sb._stream
+    sb._stream = lambda s: stream
+    try:
+        for name, c in calls.items():
+            assert hip.hipSetDevice(1 << 20) != 0
+            try:
+                c()
+            except sb.SwimbaError as e:
+                failed.append(f"{name}: {e}")
+            hip.hipGetLastError()
+    finally:
+        sb._stream = real
+    torch.cuda.synchronize()
+    assert not failed, failed
