@@ -52,8 +52,30 @@ typedef Cfg<32, 128, 2, 2> TinyGated;  // fp32 gated products: 100 x 512 x 1024
                                          // 21.8 -> 15.2 us, 300 x 2048 x 4096 142 -> 113
 
 // kGated: h; kGatedBwd: the same product, dz in the epilogue
-enum Mode { kGated, kGatedBwd, kNN, kTN };
+// kXent: z = x w^T of the cross entropy, a tile's softmax statistics in the
+// epilogue; kXentBwd: the same product, the gradient of z in the epilogue
+enum Mode { kGated, kGatedBwd, kXent, kXentBwd, kNN, kTN };
 constexpr bool is_gated(Mode m) { return m == kGated || m == kGatedBwd; }
+constexpr bool is_xent(Mode m) { return m == kXent || m == kXentBwd; }
+constexpr bool rows_b(Mode m) { return is_gated(m) || is_xent(m); }  // b by rows, k in one run
+
+// What the cross entropy's epilogues read and write besides the product.
+struct XentArgs {
+  const int32_t* targets;  // [R]
+  float* zt;               // kXent: the targets' z
+  float2* part;            // kXent: [tile columns][R]
+  const float *lse, *dloss;  // kXentBwd
+  int V, v0;               // the vocabulary; the first row of the piece at hand
+};
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// Two ranges' (largest z, sum of exp(z - that)) as one's. (An exponential of
+// -inf - -inf would be NaN: a range without a finite z keeps the other's base.)
+__device__ __forceinline__ float2 xent_join(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x), base = m == -INFINITY ? 0.f : m;
+  return make_float2(m, a.y * __builtin_amdgcn_exp2f((a.x - base) * kLog2e) +
+                            b.y * __builtin_amdgcn_exp2f((b.x - base) * kLog2e));
+}
 
 struct DenseArgs {
   const void *a, *b;
@@ -66,6 +88,10 @@ struct DenseArgs {
   int splits;     // kNN, kTN: k is cut into this many runs of ksplit, their
                   // partial products [splits][R][S] float32 in out
   int ksplit;
+  int lda;        // kTN: elements from row to row of a (R, or more)
+  int kb;         // kNN: rows of b (K, or fewer: the others are zeros)
+  int add;        // kNN, one run, float32 out: out += the product
+  XentArgs xe;    // kXent, kXentBwd: S = the vocabulary's (or its piece's) rows
 };
 
 template <typename T, class C, Mode MODE, bool SPLIT>
@@ -75,8 +101,8 @@ struct DLay {
   // 114 against 90 TFLOP/s at 12000 x 320 x 512; no gain for columns tiles)
   // (32 x 128: three, also for two workgroups a CU)
   static constexpr int NS =
-      SPLIT ? 3 : !(is_gated(MODE) && ES == 4) ? 4 : C::BM == 128 ? 2 : C::BM == 32 ? 3 : 4;
-  static constexpr bool ACOL = MODE == kTN, BCOL = !is_gated(MODE);
+      SPLIT ? 3 : !(rows_b(MODE) && ES == 4) ? 4 : C::BM == 128 ? 2 : C::BM == 32 ? 3 : 4;
+  static constexpr bool ACOL = MODE == kTN, BCOL = !rows_b(MODE);
   // tile in LDS: rows of CPR 16-byte chunks
   static constexpr int AROWS = ACOL ? kBK : C::BM, ACPR = (ACOL ? C::BM : kBK) / EPC;
   static constexpr int BROWS = BCOL ? kBK : C::BN, BCPR = (BCOL ? C::BN : kBK) / EPC;
@@ -233,6 +259,108 @@ __device__ __forceinline__ void store_gated(T* p, typename Vec<T>::x8 v, bool th
   store8<T>(p, v);
 }
 
+// ---- epilogues of the cross entropy. A lane holds, of each of its rows, 8
+// consecutive columns of every pair of column tiles.
+//
+// One value of the lanes that hold the same row (c, in the four lane groups g).
+template <class Op> __device__ __forceinline__ float over_groups(float v, Op op) {
+  v = op(v, __shfl_xor(v, 16));
+  return op(v, __shfl_xor(v, 32));
+}
+// The tile's largest z and the sum of exp(z - that) of each row, through LDS (the
+// waves of a row in their order), to part[tile column][row]; the target's z where
+// it lies in this tile. A column past S counts as -inf. Where all of a row's z
+// are -inf the sum is 0; a NaN or +inf makes the sum NaN.
+template <class C>
+__device__ __forceinline__ void xent_stats(const DenseArgs& A,
+                                           const floatx4 (&acc)[C::TM][C::TN], int r0, int s0,
+                                           int tc, unsigned char* lds) {
+  constexpr int TM = C::TM, TN = C::TN;
+  const int lane = lane_id(), g = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  float2* part = reinterpret_cast<float2*>(lds);  // [WN][BM]
+  __syncthreads();                                // the stage is no longer read
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int r = wm * TM * 16 + 16 * i + c;
+    const bool on = r0 + r < A.R;
+    const int hit = on ? A.xe.targets[r0 + r] - A.xe.v0 : -1;
+    float m = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = s0 + wn * TN * 16 + 32 * (j >> 1) + 8 * g + 4 * (j & 1) + q;
+        if (col < A.S) {
+          m = fmaxf(m, acc[i][j][q]);
+          if (on && col == hit) A.xe.zt[r0 + r] = acc[i][j][q];
+        }
+      }
+    m = over_groups(m, [](float a, float b) { return fmaxf(a, b); });
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = s0 + wn * TN * 16 + 32 * (j >> 1) + 8 * g + 4 * (j & 1) + q;
+        const float e = __builtin_amdgcn_exp2f((acc[i][j][q] - base) * kLog2e);
+        sum += col < A.S ? e : 0.f;
+      }
+    sum = over_groups(sum, [](float a, float b) { return a + b; });
+    if (g == 0) part[wn * C::BM + r] = make_float2(m, sum);
+  }
+  __syncthreads();
+  for (int r = threadIdx.x; r < C::BM; r += C::NTH) {
+    if (r0 + r >= A.R) break;
+    float2 v = part[r];
+#pragma unroll
+    for (int w = 1; w < C::WN; ++w) v = xent_join(v, part[w * C::BM + r]);
+    A.xe.part[(size_t)tc * A.R + r0 + r] = v;
+  }
+}
+// dz = (exp(z - lse) - [target]) dloss, zeros where the target counts for nothing
+// and in the columns from S to the next multiple of 8; bf16: as two bf16 numbers,
+// the second in a half of its own (see the top of this file).
+template <typename T, class C>
+__device__ __forceinline__ void xent_dz(const DenseArgs& A, const floatx4 (&acc)[C::TM][C::TN],
+                                        int r0, int s0) {
+  constexpr int TM = C::TM, TN = C::TN;
+  const int lane = lane_id(), g = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const int ld = (A.S + 7) / 8 * 8;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int row = r0 + wm * TM * 16 + 16 * i + c;
+    if (row >= A.R) continue;
+    const int t = A.xe.targets[row];
+    const bool counts = t >= 0 && t < A.xe.V;
+    const float lse = A.xe.lse[row], dl = counts ? A.xe.dloss[row] : 0.f;
+    const int hit = counts ? t - A.xe.v0 : -1;
+#pragma unroll
+    for (int jj = 0; jj < TN / 2; ++jj) {
+      const int col = s0 + (wn * (TN / 2) + jj) * 32 + 8 * g;
+      if (col >= ld) continue;
+      floatx8 d;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float z = acc[i][2 * jj + (q >> 2)][q & 3];
+        const float p = __builtin_amdgcn_exp2f((z - lse) * kLog2e);
+        d[q] = counts && col + q < A.S ? (p - (col + q == hit ? 1.f : 0.f)) * dl : 0.f;
+      }
+      T* hi = static_cast<T*>(A.out) + (size_t)row * ld + col;
+      const typename Vec<T>::x8 h = convert8<T, float>(d);
+      store8<T>(hi, h);
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) d[q] -= to_f32(h[q]);
+        store8<T>(hi + (size_t)A.R * ld, convert8<T, float>(d));
+      }
+    }
+  }
+}
+
 template <typename T, class C, Mode MODE, typename TO, bool SPLIT>
 __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   typedef DLay<T, C, MODE, SPLIT> L;
@@ -251,7 +379,7 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
 
   const int nr = (A.R + BM - 1) / BM, nc = (A.S + SN - 1) / SN;
   int tr, tc, split = 0;
-  if constexpr (!is_gated(MODE)) {
+  if constexpr (!rows_b(MODE)) {
     // the splits of one unit follow each other
     if (!unit_of(nr, nc * A.splits, tr, tc)) return;
     split = tc % A.splits;
@@ -262,7 +390,7 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   const int r0 = tr * BM, s0 = tc * SN;
   const int nrows = min(BM, A.R - r0);
   const int kbeg = split * A.ksplit;
-  const int K = is_gated(MODE) ? A.K : min(A.ksplit, A.K - kbeg);
+  const int K = rows_b(MODE) ? A.K : min(A.ksplit, A.K - kbeg);
 
   const int lane = lane_id(), g = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -281,9 +409,9 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   int akc[MA], bkc[MB];  // rows operands: the chunk's first k, to cut at K
   uint32_t astep, bstep;
   if constexpr (L::ACOL) {
-    rA = make_rsrc(ap + (size_t)kbeg * A.R, (uint64_t)K * A.R * ES);
-    if constexpr (SPLIT) rL = make_rsrc(lp + (size_t)kbeg * A.R, (uint64_t)K * A.R * ES);
-    astep = kBK * (uint32_t)A.R * ES;
+    rA = make_rsrc(ap + (size_t)kbeg * A.lda, (uint64_t)K * A.lda * ES);
+    if constexpr (SPLIT) rL = make_rsrc(lp + (size_t)kbeg * A.lda, (uint64_t)K * A.lda * ES);
+    astep = kBK * (uint32_t)A.lda * ES;
   } else {
     const uint64_t bytes = ((uint64_t)nrows * A.K - kbeg) * ES;
     rA = make_rsrc(ap + (size_t)r0 * A.K + kbeg, bytes);
@@ -291,8 +419,13 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
     astep = kBK * ES;
   }
   if constexpr (L::BCOL) {
-    rB = make_rsrc(bp + (size_t)kbeg * A.S, (uint64_t)K * A.S * ES);
+    const int kb = MODE == kNN ? max(min(K, A.kb - kbeg), 0) : K;
+    rB = make_rsrc(bp + (size_t)kbeg * A.S, (uint64_t)kb * A.S * ES);
     bstep = kBK * (uint32_t)A.S * ES;
+  } else if constexpr (is_xent(MODE)) {
+    // (from this tile's rows on: the vocabulary's weights may exceed 2 GiB)
+    rB = make_rsrc(bp + (size_t)s0 * A.K, (uint64_t)min(BN, A.S - s0) * A.K * ES);
+    bstep = kBK * ES;
   } else {
     rB = make_rsrc(bp, (uint64_t)2 * A.S * A.K * ES);
     bstep = kBK * ES;
@@ -303,7 +436,7 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
     const int r = slot / L::ACPR, pc = slot % L::ACPR;
     if constexpr (L::ACOL) {
       const int col = r0 + (pc ^ swz_cols<T, L::ACPR>(r)) * EPC;
-      aoff[m] = col < A.R ? ((uint32_t)r * A.R + col) * ES : kOOB;
+      aoff[m] = col < A.lda ? ((uint32_t)r * A.lda + col) * ES : kOOB;
       akc[m] = r;
     } else {
       akc[m] = (pc ^ swz_rows<T, L::ACPR>(r)) * EPC;
@@ -318,6 +451,9 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
       const int col = s0 + (pc ^ swz_cols<T, L::BCPR>(r)) * EPC;
       boff[m] = col < A.S ? ((uint32_t)r * A.S + col) * ES : kOOB;
       bkc[m] = r;
+    } else if constexpr (is_xent(MODE)) {
+      bkc[m] = (pc ^ swz_rows<T, L::BCPR>(r)) * EPC;
+      boff[m] = s0 + r < A.S ? ((uint32_t)r * A.K + bkc[m]) * ES : kOOB;
     } else {
       // 64 tile rows are 32 columns of g and the same 32 of u
       const int col = s0 + (r >> 6) * 32 + (r & 31);
@@ -353,8 +489,8 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
 
   // ---- fragments. acc[i][j] holds, in lane (g, c), index c of row tile i and
   // indexes 4 g .. + 3 of column tile j of this wave's block (b is the matrix
-  // cores' A operand). The gated tile's columns are permuted within pairs of
-  // tiles so that a lane's 8 values of a pair are consecutive columns
+  // cores' A operand). The columns of a b read by rows are permuted within pairs
+  // of tiles so that a lane's 8 values of a pair are consecutive columns
   // 8 g .. 8 g + 7.
   auto load_a = [&](const unsigned char* st, F (&f)[TM]) __attribute__((always_inline)) {
     const int row = wm * TM * 16;
@@ -385,7 +521,7 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   // DEFER (the gated products on the largest tile): the products of a step's
   // last row of fragments are issued after the reads of the next step (past its
   // barrier), so that they cover the wait for those reads: 1 to 3 %.
-  constexpr bool DEFER = is_gated(MODE) && TM == 8;
+  constexpr bool DEFER = rows_b(MODE) && TM == 8;
   F bd[DEFER ? TN : 1], ad = zero8<T>();
   if constexpr (DEFER) {
 #pragma unroll
@@ -454,7 +590,11 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   wait_vm<0>();  // the copies past the end land before the workgroup's LDS is released
 
   // ---- epilogue
-  if constexpr (is_gated(MODE)) {
+  if constexpr (MODE == kXent) {
+    xent_stats<C>(A, acc, r0, s0, tc, stg0);
+  } else if constexpr (MODE == kXentBwd) {
+    xent_dz<T, C>(A, acc, r0, s0);
+  } else if constexpr (is_gated(MODE)) {
     static_assert(TN % 4 == 0, "a pair of g tiles and the pair of u tiles per wave");
     TO* h = static_cast<TO*>(A.out);
     TO* z = static_cast<TO*>(A.z);
@@ -540,6 +680,8 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
           ON o;
 #pragma unroll
           for (int j = 0; j < TN; ++j) o[j] = from_f32<TO>(acc[i][j][q]);
+          if constexpr (MODE == kNN && sizeof(TO) == 4)
+            if (A.add) o = o + *reinterpret_cast<const ON*>(row + col);
           *reinterpret_cast<ON*>(row + col) = o;
         }
       } else {
@@ -551,6 +693,8 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
           O4 o;
 #pragma unroll
           for (int q = 0; q < 4; ++q) o[q] = from_f32<TO>(acc[i][j][q]);
+          if constexpr (MODE == kNN && sizeof(TO) == 4)
+            if (A.add) o = o + *reinterpret_cast<const O4*>(row + col);
           *reinterpret_cast<O4*>(row + col) = o;
         }
       }
@@ -662,13 +806,14 @@ __global__ __launch_bounds__(64 * KW) void gated_skinny_kernel(DenseArgs A) {
   }
 }
 
-// out = the splits' partial products added in split order.
-template <typename TO>
+// out = (ADD: out +) the splits' partial products added in split order.
+template <typename TO, bool ADD>
 __global__ __launch_bounds__(256) void dense_sum_kernel(const float* __restrict__ part, int splits,
                                                         size_t n4, TO* __restrict__ out) {
   for (size_t q = (size_t)blockIdx.x * 256 + threadIdx.x; q < n4; q += (size_t)gridDim.x * 256) {
     floatx4 s = reinterpret_cast<const floatx4*>(part)[q];
     for (int p = 1; p < splits; ++p) s = s + reinterpret_cast<const floatx4*>(part)[p * n4 + q];
+    if constexpr (ADD) s = s + reinterpret_cast<const floatx4*>(out)[q];
     typename Vec<TO>::x4 o;
 #pragma unroll
     for (int j = 0; j < 4; ++j) o[j] = from_f32<TO>(s[j]);
@@ -680,14 +825,17 @@ template <typename T, class C, Mode MODE, typename TO, bool SPLIT = false>
 hipError_t go(const char* name, const DenseArgs& A, hipStream_t s) {
   constexpr int SN = is_gated(MODE) ? C::BN / 2 : C::BN;
   const int64_t units = (int64_t)((A.R + C::BM - 1) / C::BM) * ((A.S + SN - 1) / SN) *
-                        (is_gated(MODE) ? 1 : A.splits);
+                        (rows_b(MODE) ? 1 : A.splits);
   return launch(name, dense_kernel<T, C, MODE, TO, SPLIT>, dim3((unsigned)((units + 7) / 8 * 8)),
                 dim3(C::NTH), 0, s, A);
 }
 
+// The gated products and those of the cross entropy.
 template <typename T, Mode MODE>
-hipError_t go_gated(const char* name, const DenseArgs& A, hipStream_t s) {
-  const int tile = plan(sizeof(T) == 2, false, true, A.R, 2 * (int64_t)A.S, A.K, 1).tile;
+hipError_t go_rows(const char* name, const DenseArgs& A, hipStream_t s) {
+  const int tile = is_gated(MODE)
+                       ? plan(sizeof(T) == 2, false, true, A.R, 2 * (int64_t)A.S, A.K, 1).tile
+                       : xent_tile(sizeof(T) == 2, A.R, A.S, A.K);
   if constexpr (sizeof(T) == 2)
     if (tile == 256256) return go<T, Big, MODE, T>(name, A, s);
   if (tile == 128128) return go<T, Mid, MODE, T>(name, A, s);
@@ -732,8 +880,8 @@ hipError_t launch_gated_project(bool is_bf16, int M, int D, int F, int act, cons
   if (M <= 16) return is_bf16 ? go_skinny<bf16, 1>(A, s) : go_skinny<float, 1>(A, s);
   if (M <= 32) return is_bf16 ? go_skinny<bf16, 2>(A, s) : go_skinny<float, 2>(A, s);
   if (M <= kSkinnyTokens) return is_bf16 ? go_skinny<bf16, 4>(A, s) : go_skinny<float, 4>(A, s);
-  return is_bf16 ? go_gated<bf16, kGated>("gated_project", A, s)
-                 : go_gated<float, kGated>("gated_project", A, s);
+  return is_bf16 ? go_rows<bf16, kGated>("gated_project", A, s)
+                 : go_rows<float, kGated>("gated_project", A, s);
 }
 
 size_t gated_dz_bytes(bool is_bf16, int M, int F) {
@@ -744,8 +892,8 @@ hipError_t launch_gated_dz(bool is_bf16, int M, int D, int F, int act, const voi
                            const void* w_in, const void* dh, void* dz, hipStream_t s) {
   DenseArgs A{};
   A.a = x; A.b = w_in; A.out = dz; A.dh = dh; A.R = M; A.S = F; A.K = D; A.act = act;
-  return is_bf16 ? go_gated<bf16, kGatedBwd>("gated_dz", A, s)
-                 : go_gated<float, kGatedBwd>("gated_dz", A, s);
+  return is_bf16 ? go_rows<bf16, kGatedBwd>("gated_dz", A, s)
+                 : go_rows<float, kGatedBwd>("gated_dz", A, s);
 }
 
 size_t dense_ws_bytes(bool is_bf16, bool split, bool tn, int R, int S, int K) {
@@ -756,37 +904,41 @@ size_t dense_ws_bytes(bool is_bf16, bool split, bool tn, int R, int S, int K) {
 namespace {
 
 // The sum of a product's k runs (in ws) to out.
-template <typename TO>
+template <typename TO, bool ADD = false>
 hipError_t sum_runs(const DenseArgs& A, const void* ws, void* out, hipStream_t s) {
   const size_t n4 = (size_t)A.R * A.S / 4;
   const unsigned blocks = (unsigned)std::min<size_t>((n4 + 255) / 256, 4096);
-  return launch("dense_sum", dense_sum_kernel<TO>, dim3(blocks), dim3(256), 0, s, (const float*)ws,
+  return launch("dense_sum", dense_sum_kernel<TO, ADD>, dim3(blocks), dim3(256), 0, s, (const float*)ws,
                 A.splits, n4, (TO*)out);
 }
 
 }  // namespace
 
 hipError_t launch_dense_nn(bool is_bf16, const char* name, int M, int K, int S, const void* a,
-                           const void* a_lo, const void* b, void* out, void* ws, hipStream_t s) {
+                           const void* a_lo, const void* b, void* out, void* ws, hipStream_t s,
+                           int kb, bool add) {
   DenseArgs A{};
-  A.a = a; A.a_lo = a_lo; A.b = b; A.R = M; A.S = S; A.K = K;
+  A.a = a; A.a_lo = a_lo; A.b = b; A.R = M; A.S = S; A.K = K; A.kb = kb < 0 ? K : kb;
   const Runs r = runs_of(is_bf16, a_lo != nullptr, false, M, S, K);
   A.splits = r.splits;
   A.ksplit = r.ksplit;
   A.out = r.splits > 1 ? ws : out;
+  A.add = add && r.splits == 1;
   hipError_t e;
   if (!is_bf16) e = go_tile<float, kNN, float, false>(r.tile, name, A, s);
   else if (a_lo) e = go_tile<bf16, kNN, float, true>(r.tile, name, A, s);
   else if (r.splits > 1) e = go_tile<bf16, kNN, float, false>(r.tile, name, A, s);
   else e = go_tile<bf16, kNN, bf16, false>(r.tile, name, A, s);
   if (e != hipSuccess || r.splits == 1) return e;
+  if (add) return sum_runs<float, true>(A, ws, out, s);
   return is_bf16 && !a_lo ? sum_runs<bf16>(A, ws, out, s) : sum_runs<float>(A, ws, out, s);
 }
 
 hipError_t launch_dense_tn(bool is_bf16, const char* name, int M, int R, int S, const void* a,
-                           const void* a_lo, const void* b, float* out, void* ws, hipStream_t s) {
+                           const void* a_lo, const void* b, float* out, void* ws, hipStream_t s,
+                           int lda) {
   DenseArgs A{};
-  A.a = a; A.a_lo = a_lo; A.b = b; A.R = R; A.S = S; A.K = M;
+  A.a = a; A.a_lo = a_lo; A.b = b; A.R = R; A.S = S; A.K = M; A.lda = lda < 0 ? R : lda;
   const Runs r = runs_of(is_bf16, a_lo != nullptr, true, R, S, M);
   A.splits = r.splits;
   A.ksplit = r.ksplit;
@@ -797,6 +949,78 @@ hipError_t launch_dense_tn(bool is_bf16, const char* name, int M, int R, int S, 
   else e = go_tile<bf16, kTN, float, false>(r.tile, name, A, s);
   if (e != hipSuccess || r.splits == 1) return e;
   return sum_runs<float>(A, ws, out, s);
+}
+
+// ---- cross entropy
+
+namespace {
+
+// Each row's logarithm of the sum of exponentials from the tiles' statistics, and
+// its loss: 64 rows a workgroup, a quarter of the tiles each wave, joined in order.
+__global__ __launch_bounds__(256) void xent_finish_kernel(XentArgs X, int M, int tiles,
+                                                          float* loss, float* lse) {
+  __shared__ float2 part[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int row = blockIdx.x * 64 + lane;
+  const int per = (tiles + 3) / 4, t1 = min(tiles, (wave + 1) * per);
+  float2 v = make_float2(-INFINITY, 0.f);
+  if (row < M)
+    for (int t = wave * per; t < t1; ++t) v = xent_join(v, X.part[(size_t)t * M + row]);
+  part[wave][lane] = v;
+  __syncthreads();
+  if (wave || row >= M) return;
+#pragma unroll
+  for (int w = 1; w < 4; ++w) v = xent_join(v, part[w][lane]);
+  // a row of -inf alone: -inf
+  const float l = v.x == -INFINITY && v.y == 0.f ? -INFINITY : v.x + logf(v.y);
+  const int t = X.targets[row];
+  lse[row] = l;
+  loss[row] = t >= 0 && t < X.V ? l - X.zt[row] : 0.f;
+}
+
+int xent_tile_cols(int tile) { return tile == 256256 ? 256 : 128; }
+
+template <typename T>
+hipError_t xent_forward(int M, int D, int V, const void* x, const void* w, const int32_t* targets,
+                        float* loss, float* lse, void* ws, hipStream_t s) {
+  DenseArgs A{};
+  A.a = x; A.b = w; A.R = M; A.S = V; A.K = D;
+  A.xe.targets = targets;
+  A.xe.V = V;
+  A.xe.zt = static_cast<float*>(ws);
+  A.xe.part = reinterpret_cast<float2*>(static_cast<float*>(ws) + (M + 3) / 4 * 4);
+  const hipError_t e = go_rows<T, kXent>("cross_entropy", A, s);
+  if (e != hipSuccess) return e;
+  const int cols = xent_tile_cols(xent_tile(sizeof(T) == 2, M, V, D));
+  return launch("cross_entropy_finish", xent_finish_kernel, dim3((unsigned)((M + 63) / 64)),
+                dim3(256), 0, s, A.xe, M, (V + cols - 1) / cols, loss, lse);
+}
+
+}  // namespace
+
+size_t xent_ws_bytes(bool is_bf16, int M, int D, int V) {
+  const int cols = xent_tile_cols(xent_tile(is_bf16, M, V, D));
+  return 4 * (size_t)((M + 3) / 4 * 4) + 8 * (size_t)((V + cols - 1) / cols) * M;
+}
+
+hipError_t launch_xent(bool is_bf16, int M, int D, int V, const void* x, const void* w,
+                       const int32_t* targets, float* loss, float* lse, void* ws, hipStream_t s) {
+  return is_bf16 ? xent_forward<bf16>(M, D, V, x, w, targets, loss, lse, ws, s)
+                 : xent_forward<float>(M, D, V, x, w, targets, loss, lse, ws, s);
+}
+
+hipError_t launch_xent_dz(bool is_bf16, int M, int D, int V, int v0, int nv, const void* x,
+                          const void* w, const int32_t* targets, const float* lse,
+                          const float* dloss, void* dz, hipStream_t s) {
+  DenseArgs A{};
+  A.a = x; A.b = w; A.out = dz; A.R = M; A.S = nv; A.K = D;
+  A.xe.targets = targets;
+  A.xe.lse = lse;
+  A.xe.dloss = dloss;
+  A.xe.V = V;
+  A.xe.v0 = v0;
+  return is_bf16 ? go_rows<bf16, kXentBwd>("cross_entropy_dz", A, s)
+                 : go_rows<float, kXentBwd>("cross_entropy_dz", A, s);
 }
 
 }  // namespace swimba

@@ -92,4 +92,10 @@ inline Runs runs_of(bool is_bf16, bool split, bool tn, int R, int S, int K) {
   return r;
 }
 
+// The tile of the cross entropy's products (tokens x vocabulary rows), by the costs
+// of the gated products' tiles, whose kernel it shares up to the epilogue.
+inline int xent_tile(bool is_bf16, int64_t R, int64_t S, int64_t K) {
+  return plan(is_bf16, false, true, R, S, K, 1).tile;
+}
+
 }  // namespace swimba

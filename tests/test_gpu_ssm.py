@@ -1,0 +1,529 @@
+"""The selective state space layer's calls and its loss against the fp64 oracle
+(``oracle/ssm.py``), with the bounds of ``ssm_bounds.py``."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import ssm_bounds as sbd
+from oracle import ssm as osm
+from selective_ssm_parameter_amd import ssm
+from ssm_bounds import DT, check, dev, empty, host
+
+pytestmark = pytest.mark.gpu
+
+TYPES = ["bf16", "f32"]
+F32 = torch.float32
+
+
+def rng(seed):
+    return np.random.default_rng(seed)
+
+
+def lens_of(kind, Bt, T, seed):
+    if kind is None:
+        return None
+    return rng(seed).integers(-2, T + 4, Bt).astype(np.int32)
+
+
+def spoil(t, lens, Bt, T):
+    """NaN past each sequence's length, where nothing may look."""
+    if lens is not None:
+        v = t.view(Bt, T, -1)
+        for b, n in enumerate(osm.lengths(Bt, T, lens)):
+            v[b, n:] = float("nan")
+    return t
+
+
+def column(a, dt, pad, lens, Bt, T):
+    """[Bt, T, C] values as a [M, C] column range of a tensor whose rows are pad wider (and
+    start on 16 bytes)."""
+    per = 16 // dt.itemsize
+    C = a.shape[2]
+    wide = torch.full((Bt * T, -(-(C + pad) // per) * per), float("nan"), dtype=dt, device="cuda")
+    t = dev(a.reshape(Bt * T, C), dt)
+    wide[:, :C] = spoil(t, lens, Bt, T)
+    return wide[:, :C], host(dev(a, dt))
+
+
+# ------------------------------------------------------------------ convolution
+
+def conv_case(Bt, T, C, W, dtype, act=1, bias=True, state=True, lens=None, pad=0, seed=0):
+    dt, r = DT[dtype], rng(seed)
+    n = r.standard_normal
+    x, xh = column(n((Bt, T, C)), dt, pad, lens, Bt, T)
+    w, b = dev(n((C, W)) * W ** -0.5, dt), dev(n(C), dt) if bias else None
+    s0 = dev(n((Bt, W - 1, C)), dt) if state else None
+    dy = spoil(dev(n((Bt * T, C)), dt), lens, Bt, T)
+    ds = dev(n((Bt, W - 1, C))) if state else None
+    dyh = np.nan_to_num(host(dy).reshape(Bt, T, C))
+    hv = lambda t: None if t is None else host(t)
+    return dict(d=ssm.ssm_dims(Bt, T, C, 1, 1, dtype), dt=dt, W=W, act=act, x=x, w=w, b=b, s0=s0,
+                dy=dy, ds=ds, lens=None if lens is None else dev(lens, torch.int32),
+                host=(xh, hv(w), hv(b), act, dyh, hv(ds), hv(s0), lens))
+
+
+def conv_forward(q):
+    d, C = q["d"], q["x"].shape[1]
+    y, s = empty(*q["x"].shape, dt=q["dt"]), empty(d.batch, q["W"] - 1, C, dt=q["dt"])
+    ssm.swimba_causal_conv(d, q["W"], q["x"], q["w"], q["b"], q["act"], q["lens"], q["s0"], y, s)
+    return y, s
+
+
+def conv_backward(q, pad=0):
+    d, C, M = q["d"], q["x"].shape[1], q["x"].shape[0]
+    per = 16 // q["dt"].itemsize
+    dx = empty(M, -(-(C + pad) // per) * per, dt=q["dt"])[:, :C]
+    dw, db = empty(C, q["W"]), empty(C) if q["b"] is not None else None
+    ds0 = empty(d.batch, q["W"] - 1, C)
+    ssm.swimba_causal_conv_backward(d, q["W"], q["x"], q["w"], q["b"], q["act"], q["lens"],
+                                    q["s0"], q["dy"], q["ds"], dx, dw, db, ds0,
+                                    ssm.ssm_workspace(d, ssm.CAUSAL_CONV_BACKWARD))
+    return dx, dw, db, ds0
+
+
+CONV = [  # Bt, T, C, W, act, bias, state, ragged, pad
+    (1, 1, 1, 4, 1, True, True, None, 0), (3, 2, 8, 4, 1, True, True, None, 0),
+    (2, 3, 24, 4, 0, False, True, "r", 8), (5, 7, 13, 3, 1, True, False, "r", 3),
+    (2, 8, 64, 2, 1, False, True, None, 64), (4, 9, 40, 4, 1, True, True, "r", 0),
+    (1, 65, 512, 4, 1, True, False, None, 0), (3, 130, 100, 3, 0, True, True, "r", 28),
+    (2, 333, 72, 2, 1, True, True, "r", 0), (70, 17, 33, 4, 1, True, True, "r", 1),
+    (1, 1040, 264, 4, 1, False, False, None, 8), (2, 100, 1000, 4, 0, True, True, "r", 0),
+]
+
+
+@pytest.mark.parametrize("Bt,T,C,W,act,bias,state,lens,pad", CONV)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_causal_conv(Bt, T, C, W, act, bias, state, lens, pad, dtype):
+    q = conv_case(Bt, T, C, W, dtype, act, bias, state, lens_of(lens, Bt, T, T), pad, seed=T + C)
+    x, w, b, _, dyh, ds, s0, ln = q["host"]
+    y, s = conv_forward(q)
+    dx, dw, db, ds0 = conv_backward(q, pad)
+    wy, _, ws = osm.causal_conv(x, w, b, act, s0, ln)
+    tol = sbd.conv_bounds(x, w, b, act, dyh, ds, s0, ln, q["dt"], runs=Bt * T + 8)
+    check("y", y, wy, tol["y"])
+    assert np.array_equal(host(s), ws)  # the inputs themselves
+    wdx, wdw, wdb, wds = osm.causal_conv_backward(x, w, b, act, dyh, ds, s0, ln)
+    check("dx", dx, wdx, tol["dx"])
+    check("dw", dw, wdw, tol["dw"])
+    check("ds0", ds0, wds, tol["ds0"])
+    if db is not None:
+        check("db", db, wdb, tol["db"])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("W,C", [(2, 40), (3, 13), (4, 4096)])
+def test_causal_conv_step_follows_the_sequence(W, C, dtype):
+    """Tokens one by one, in place, give the same bits as the sequence at once."""
+    Bt, T = 3, 6
+    q = conv_case(Bt, T, C, W, dtype, seed=C)
+    y, s = conv_forward(q)
+    d1 = ssm.ssm_dims(Bt, 1, C, 1, 1, dtype)
+    state = q["s0"].clone()
+    xs = q["x"].reshape(Bt, T, C)
+    for t in range(T):
+        yt = empty(Bt, C, dt=q["dt"])
+        ssm.swimba_causal_conv_step(d1, W, xs[:, t], q["w"], q["b"], 1, state, state, yt)
+        assert torch.equal(yt, y.view(Bt, T, C)[:, t])
+    assert torch.equal(state, s)
+
+
+def test_causal_conv_of_long_rows():
+    """Rows whose offsets pass 32 bits; the same bits as from a dense tensor."""
+    T, C, ld = 36000, 64, 65536
+    wide = torch.empty(T, ld, dtype=torch.bfloat16, device="cuda")
+    x = torch.randn(T, C, device="cuda").bfloat16()
+    wide[:, -C:] = x
+    d, w = ssm.ssm_dims(1, T, C, 1, 1, "bf16"), torch.randn(C, 4, device="cuda").bfloat16()
+    ya, yb = empty(T, C, dt=x.dtype), empty(T, C, dt=x.dtype)
+    ssm.swimba_causal_conv(d, 4, x, w, None, 1, None, None, ya)
+    ssm.swimba_causal_conv(d, 4, wide[:, -C:], w, None, 1, None, None, yb)
+    assert torch.equal(ya, yb)
+    dy, ws = torch.randn(T, C, device="cuda").bfloat16(), \
+        ssm.ssm_workspace(d, ssm.CAUSAL_CONV_BACKWARD)
+    dxa, dwa, dwb = empty(T, C, dt=x.dtype), empty(C, 4), empty(C, 4)
+    ssm.swimba_causal_conv_backward(d, 4, x, w, None, 1, None, None, dy, None, dxa, dwa, None,
+                                    None, ws)
+    ssm.swimba_causal_conv_backward(d, 4, wide[:, -C:], w, None, 1, None, None, dy, None,
+                                    wide[:, :C], dwb, None, None, ws)
+    assert torch.equal(dxa, wide[:, :C]) and torch.equal(dwa, dwb)
+
+
+def test_causal_conv_keeps_infinities_to_their_window():
+    T, C, W = 40, 16, 3
+    x = torch.randn(T, C, device="cuda")
+    x[10, 3], x[20, 5] = float("inf"), float("nan")
+    w = torch.rand(C, W, device="cuda") + 0.5
+    y = empty(T, C)
+    ssm.swimba_causal_conv(ssm.ssm_dims(1, T, C, 1, 1, "f32"), W, x, w, None, 0, None, None, y)
+    bad = ~torch.isfinite(y)
+    want = torch.zeros_like(bad)
+    want[10:13, 3] = want[20:23, 5] = True
+    assert torch.equal(bad, want)
+
+
+# ------------------------------------------------------------------ selective scan
+
+def scan_case(Bt, T, Ch, N, G, dtype, gate=True, lens=None, pad=0, h0=True, D=True, bias=True,
+              seed=0, spread=1.0):
+    dt, r = DT[dtype], rng(seed)
+    n = r.standard_normal
+    dims = ssm.ssm_dims(Bt, T, Ch, N, G, dtype)
+    t, v = {}, {}
+    for k in ("x", "dt", "z"):
+        t[k], v[k] = column(n((Bt, T, Ch)) * (spread if k == "dt" else 1.0), dt, pad, lens, Bt, T)
+    if not gate:
+        t["z"] = v["z"] = None
+    bc = column(np.concatenate([n((Bt, T, G * N)), n((Bt, T, G * N))], 2), dt, pad, lens, Bt, T)[0]
+    per = 16 // dt.itemsize  # B and C as column ranges of one tensor where they start on 16 bytes
+    if G * N % per == 0:
+        t["B"], t["C"] = bc[:, :G * N], bc[:, G * N:]
+    else:
+        t["B"], t["C"] = bc[:, :G * N].clone(), bc[:, G * N:].clone()
+    for k in ("B", "C"):
+        v[k] = np.nan_to_num(host(t[k])).reshape(Bt, T, G, N)
+    f = dict(A=-np.exp(n((Ch, N))), D=n(Ch) if D else None, bias=n(Ch) - 1.0 if bias else None,
+             h_init=n((Bt, Ch, N)) if h0 else None)
+    for k, a in f.items():
+        t[k] = None if a is None else dev(a)
+        v[k] = None if a is None else host(t[k])
+    v = {k: v[k] for k in ("x", "dt", "z", "B", "C", "A", "D", "bias", "h_init")}
+    dy = spoil(dev(n((Bt * T, Ch)), dt), lens, Bt, T)
+    dh = dev(n((Bt, Ch, N))) if h0 else None
+    return dict(d=dims, t=t, v=v, dt=dt, lens_h=lens, dy=dy, dh=dh, N=N, G=G, Ch=Ch,
+                lens=None if lens is None else dev(lens, torch.int32),
+                dyh=np.nan_to_num(host(dy)).reshape(Bt, T, Ch),
+                dhh=None if dh is None else host(dh))
+
+
+def scan_inputs(q):
+    return [q["t"][k] for k in ("x", "dt", "z", "B", "C", "A", "D", "bias")]
+
+
+def scan_forward(q, carry=None, final=True):
+    d = q["d"]
+    y = empty(d.batch * d.seqlen, q["Ch"], dt=q["dt"])
+    h = empty(d.batch, q["Ch"], q["N"]) if final else None
+    ssm.swimba_selective_scan(d, *scan_inputs(q), q["lens"], q["t"]["h_init"], y, h, carry,
+                              ssm.ssm_workspace(d, ssm.SELECTIVE_SCAN))
+    return y, h
+
+
+def scan_backward(q, carry, pad=0, sums=True):
+    d, M, Ch, GN = q["d"], q["d"].batch * q["d"].seqlen, q["Ch"], q["G"] * q["N"]
+    per = 16 // q["dt"].itemsize
+    rows = lambda c: empty(M, -(-(c + pad) // per) * per, dt=q["dt"])[:, :c]
+    o = dict(dx=rows(Ch), ddt=rows(Ch), dz=rows(Ch) if q["t"]["z"] is not None else None,
+             dB=rows(GN), dC=rows(GN), dA=empty(Ch, q["N"]), dD=empty(Ch) if sums else None,
+             dbias=empty(Ch) if sums else None,
+             dh_init=empty(d.batch, Ch, q["N"]) if sums else None)
+    ssm.swimba_selective_scan_backward(d, *scan_inputs(q), q["lens"], carry, q["dy"], q["dh"],
+                                       *o.values(), ssm.ssm_workspace(d, ssm.SELECTIVE_SCAN_BACKWARD))
+    return o
+
+
+SCAN = [  # Bt, T, Ch, N, G, gate, ragged, pad, h0 (and D and bias)
+    (1, 1, 1, 1, 1, True, None, 0, True), (3, 2, 16, 16, 1, True, None, 0, True),
+    (2, 15, 17, 3, 1, False, "r", 3, True), (2, 16, 64, 16, 1, True, None, 64, False),
+    (1, 17, 65, 4, 1, True, None, 0, True), (4, 40, 24, 16, 3, True, "r", 8, True),
+    (2, 64, 130, 11, 2, False, "r", 0, True), (1, 129, 40, 16, 1, True, None, 0, True),
+    (3, 150, 20, 17, 1, True, "r", 1, True), (2, 200, 48, 32, 2, False, "r", 0, True),
+    (1, 333, 12, 16, 1, True, None, 0, False), (1, 260, 10, 33, 1, True, None, 5, True),
+    (2, 70, 36, 48, 1, True, "r", 0, True), (1, 90, 20, 64, 1, False, None, 0, True),
+    (2, 40, 18, 100, 1, True, "r", 0, True), (1, 140, 8, 128, 1, True, None, 0, True),
+    (6, 30, 8, 65, 2, False, "r", 0, True),
+]
+
+
+@pytest.mark.parametrize("Bt,T,Ch,N,G,gate,lens,pad,h0", SCAN)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_selective_scan(Bt, T, Ch, N, G, gate, lens, pad, h0, dtype):
+    q = scan_case(Bt, T, Ch, N, G, dtype, gate, lens_of(lens, Bt, T, T), pad, h0, h0, h0,
+                  seed=T + Ch)
+    v, ln = q["v"], q["lens_h"]
+    carry = ssm.selective_scan_carry(q["d"])
+    y, h = scan_forward(q, carry)
+    o = scan_backward(q, carry, pad)
+    tol = sbd.scan_bounds(v, ln, q["dt"], q["dyh"], q["dhh"])
+    wy, _, hs = osm.selective_scan(*v.values(), ln)
+    check("y", y, wy, tol["y"])
+    check("h", h, hs[:, -1], tol["h"])
+    want = osm.selective_scan_backward(*v.values(), q["dyh"], q["dhh"], ln)
+    for k, got in o.items():
+        if got is not None:
+            check(k, got, want[k], tol[k])
+    # without what may be left out: the same bits
+    assert torch.equal(scan_forward(q, None, final=False)[0], y)
+    o2 = scan_backward(q, carry, sums=False)
+    for k in ("dx", "ddt", "dB", "dC", "dA"):
+        assert torch.equal(o2[k], o[k]), k
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("Ch,N,G,gate", [(40, 16, 1, True), (7, 5, 1, False), (12, 64, 2, True),
+                                         (300, 17, 3, True), (9, 128, 1, True)])
+def test_selective_step_follows_the_sequence(Ch, N, G, gate, dtype):
+    Bt, T = 3, 5
+    q = scan_case(Bt, T, Ch, N, G, dtype, gate, seed=Ch)
+    tol = sbd.scan_bounds(q["v"], None, q["dt"])
+    wy, _, hs = osm.selective_scan(*q["v"].values())
+    d1 = ssm.ssm_dims(Bt, 1, Ch, N, G, dtype)
+    h, t = q["t"]["h_init"].clone(), q["t"]
+    ys = []
+    for i in range(T):
+        row = lambda a: None if a is None else a.reshape(Bt, T, -1)[:, i] if a.is_contiguous() \
+            else torch.as_strided(a, (Bt, a.shape[1]), (a.stride(0) * T, 1),
+                                  a.storage_offset() + i * a.stride(0))
+        bc = [row(t["B"]), row(t["C"])]
+        if any(b.data_ptr() % 16 for b in bc):
+            bc = [b.clone() for b in bc]
+        al = lambda a: None if a is None else a if a.data_ptr() % 16 == 0 else a.clone()
+        y = empty(Bt, Ch, dt=q["dt"])
+        ssm.swimba_selective_step(d1, al(row(t["x"])), al(row(t["dt"])), al(row(t["z"])), *bc,
+                                  t["A"], t["D"], t["bias"], h, h, y)
+        ys.append(y)
+    check("y", torch.stack(ys, 1), wy, tol["y"])
+    check("h", h, hs[:, -1], tol["h"])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_selective_scan_in_pieces(dtype):
+    """A sequence cut anywhere and resumed from its state."""
+    q = scan_case(2, 100, 24, 16, 1, dtype, seed=4)
+    tol = sbd.scan_bounds(q["v"], None, q["dt"])
+    wy, _, hs = osm.selective_scan(*q["v"].values())
+    h, ys = q["t"]["h_init"], []
+    for t0, t1 in ((0, 1), (1, 38), (38, 100)):
+        cut = lambda a: a.reshape(2, 100, -1)[:, t0:t1].reshape(2 * (t1 - t0), -1).contiguous()
+        t = q["t"]
+        d = ssm.ssm_dims(2, t1 - t0, 24, 16, 1, dtype)
+        y, hn = empty(2 * (t1 - t0), 24, dt=q["dt"]), empty(2, 24, 16)
+        ssm.swimba_selective_scan(d, cut(t["x"]), cut(t["dt"]), cut(t["z"]), cut(t["B"]),
+                                  cut(t["C"]), t["A"], t["D"], t["bias"], None, h, y, hn, None,
+                                  ssm.ssm_workspace(d, ssm.SELECTIVE_SCAN))
+        h = hn
+        ys.append(y.view(2, t1 - t0, 24))
+    check("y", torch.cat(ys, 1), wy, tol["y"])
+    check("h", h, hs[:, -1], tol["h"])
+
+
+def test_selective_scan_without_tokens():
+    d = ssm.ssm_dims(2, 0, 24, 16, 1, "f32")
+    z, h0, h = torch.empty(0, 24, device="cuda"), torch.randn(2, 24, 16, device="cuda"), \
+        empty(2, 24, 16)
+    bc, A = torch.empty(0, 16, device="cuda"), -torch.ones(24, 16, device="cuda")
+    ssm.swimba_selective_scan(d, z, z, None, bc, bc, A, None, None, None, h0, z, h, None, None)
+    assert torch.equal(h, h0)
+    ssm.swimba_selective_scan(d, z, z, None, bc, bc, A, None, None, None, None, z, h, None, None)
+    assert not h.any()
+    dA, dD, db, dh0 = empty(24, 16), empty(24), empty(24), empty(2, 24, 16)
+    ssm.swimba_selective_scan_backward(d, z, z, None, bc, bc, A, None, None, None, None, z, h0, z,
+                                       z, None, bc, bc, dA, dD, db, dh0, None)
+    assert torch.equal(dh0, h0) and not (dA.any() or dD.any() or db.any())
+    s0, s = torch.randn(2, 3, 24, device="cuda"), empty(2, 3, 24)
+    dc = ssm.ssm_dims(2, 0, 24, 1, 1, "f32")
+    w = torch.ones(24, 4, device="cuda")
+    ssm.swimba_causal_conv(dc, 4, z, w, None, 1, None, s0, z, s)
+    assert torch.equal(s, s0)
+    ssm.swimba_causal_conv(dc, 4, z, w, None, 1, None, None, z, s)
+    assert not s.any()
+    dw, ds0 = empty(24, 4), empty(2, 3, 24)
+    ssm.swimba_causal_conv_backward(dc, 4, z, w, None, 1, None, s0, z, s0, z, dw, db, ds0, None)
+    assert torch.equal(ds0, s0) and not (dw.any() or db.any())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_selective_scan_special_values(dtype):
+    """dt of -inf leaves the state as it is; a NaN or infinity stays in its channel (but for
+    the gradients that all channels add up to), from its token on."""
+    Bt, T, Ch, N = 1, 70, 40, 16
+    q = scan_case(Bt, T, Ch, N, 1, dtype, gate=False, seed=3)
+    t = q["t"]
+    t["dt"][:, 5] = float("-inf")
+    t["x"][20, 7], t["x"][30, 9] = float("nan"), float("inf")
+    carry = ssm.selective_scan_carry(q["d"])
+    y, h = scan_forward(q, carry)
+    assert torch.equal(h[0, 5], t["h_init"][0, 5])
+    fin = torch.isfinite(y)
+    want = torch.ones_like(fin)
+    want[20:, 7] = want[30:, 9] = False
+    # (an infinity times a C of zero or infinities of both signs give NaN: not finite either way)
+    assert torch.equal(fin, want)
+    o = scan_backward(q, carry)
+    keep = [c for c in range(Ch) if c not in (7, 9)]
+    assert torch.isfinite(o["dx"][:, keep]).all() and torch.isfinite(o["ddt"][:, keep]).all()
+    assert torch.isfinite(o["dA"][keep]).all() and torch.isfinite(o["dB"][31:]).all()
+    assert not o["ddt"][:, 5].any()
+
+
+def test_selective_scan_of_large_steps():
+    """Steps of up to 30 and decays that underflow."""
+    q = scan_case(2, 50, 24, 16, 1, "f32", seed=8, spread=10.0)
+    tol = sbd.scan_bounds(q["v"], None, q["dt"], q["dyh"], q["dhh"])
+    carry = ssm.selective_scan_carry(q["d"])
+    y, h = scan_forward(q, carry)
+    o = scan_backward(q, carry)
+    wy, _, hs = osm.selective_scan(*q["v"].values())
+    check("y", y, wy, tol["y"])
+    check("h", h, hs[:, -1], tol["h"])
+    want = osm.selective_scan_backward(*q["v"].values(), q["dyh"], q["dhh"])
+    for k, got in o.items():
+        check(k, got, want[k], tol[k])
+
+
+def test_selective_scan_of_long_rows():
+    """Rows whose offsets pass 32 bits; the same bits as from dense tensors."""
+    T, C, N, ld = 36000, 64, 16, 65536
+    wide = torch.empty(T, ld, dtype=torch.bfloat16, device="cuda")
+    r = lambda *s: torch.randn(*s, device="cuda")
+    x, dt, z, B, Cm, dy = [r(T, c).bfloat16() for c in (C, C, C, N, N, C)]
+    A, D, bias = -torch.rand(C, N, device="cuda") - 0.1, r(C), r(C) - 3
+    cols = [wide[:, -C * (i + 1):ld - C * i] for i in range(6)]
+    for c, v in zip(cols, (x, dt, z)):
+        c.copy_(v)
+    bw, cw = wide[:, :N], wide[:, N:2 * N]
+    bw.copy_(B)
+    cw.copy_(Cm)
+    d = ssm.ssm_dims(1, T, C, N, 1, "bf16")
+    ws, wsb = ssm.ssm_workspace(d, ssm.SELECTIVE_SCAN), \
+        ssm.ssm_workspace(d, ssm.SELECTIVE_SCAN_BACKWARD)
+    outs = []
+    for v in ((x, dt, z, B, Cm), (*cols[:3], bw, cw)):
+        y, h, carry = empty(T, C, dt=x.dtype), empty(1, C, N), ssm.selective_scan_carry(d)
+        ssm.swimba_selective_scan(d, *v, A, D, bias, None, None, y, h, carry, ws)
+        if v[0] is x:
+            g = [empty(T, C, dt=x.dtype) for _ in range(3)] + [empty(T, N, dt=x.dtype)
+                                                               for _ in range(2)]
+        else:
+            g = [*cols[3:], wide[:, 2 * N:3 * N], wide[:, 3 * N:4 * N]]
+        dA = empty(C, N)
+        ssm.swimba_selective_scan_backward(d, *v, A, D, bias, None, carry, dy, None, *g, dA, None,
+                                           None, None, wsb)
+        outs.append([y, h, *g, dA])
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ cross entropy
+
+def loss_case(M, D, V, dtype, seed=0, scale=2.0):
+    dt, r = DT[dtype], rng(seed)
+    x, w = dev(r.standard_normal((M, D)), dt), dev(r.standard_normal((V, D)) * scale * D ** -0.5, dt)
+    t = r.integers(-1, V + 1, M).astype(np.int32)  # none (-1 and V) among them
+    g = dev(r.standard_normal(M))
+    g[torch.from_numpy((t < 0) | (t >= V)).cuda()] = float("nan")  # not looked at
+    return ssm.loss_dims(M, D, V, dtype), x, w, t, g
+
+
+def loss_run(d, x, w, t, g):
+    M, D, V = x.shape[0], x.shape[1], w.shape[0]
+    td, loss, lse, dx, dw = dev(t, torch.int32), empty(M), empty(M), empty(M, D), empty(V, D)
+    ssm.swimba_cross_entropy(d, x, w, td, loss, lse, ssm.ssm_workspace(d, ssm.CROSS_ENTROPY))
+    ssm.swimba_cross_entropy_backward(d, x, w, td, lse, g, dx, dw,
+                                      ssm.ssm_workspace(d, ssm.CROSS_ENTROPY_BACKWARD))
+    return loss, lse, dx, dw
+
+
+# (tokens, d_model, vocabulary): one word, one token, odd vocabularies, every tile of both types
+LOSS = [(1, 8, 1), (1, 64, 37), (3, 40, 1000), (64, 128, 129), (65, 72, 777), (130, 256, 2051),
+        (257, 136, 509), (300, 512, 4100), (1, 1024, 5003), (1000, 64, 333), (2000, 96, 1030),
+        (515, 1000, 3000)]
+
+
+@pytest.mark.parametrize("M,D,V", LOSS)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_cross_entropy(M, D, V, dtype):
+    d, x, w, t, g = loss_case(M, D, V, dtype, seed=M + V)
+    got = loss_run(d, x, w, t, g)
+    xh, wh, gh = host(x), host(w), np.nan_to_num(host(g))
+    loss, lse, _ = osm.cross_entropy(xh, wh, t)
+    dx, dw, _ = osm.cross_entropy_backward(xh, wh, t, gh)
+    tol = sbd.loss_bounds(xh, wh, t, gh, dtype)
+    for name, a, b in zip(("loss", "lse", "dx", "dw"), got, (loss, lse, dx, dw)):
+        check(name, a, b, tol[name])
+
+
+@pytest.mark.parametrize("dtype,M,D,V", [("bf16", 16500, 16, 9001), ("f32", 12000, 8, 11003),
+                                         ("bf16", 4100, 384, 8200), ("f32", 4100, 64, 4096)])
+def test_cross_entropy_of_several_pieces_and_large_tiles(dtype, M, D, V):
+    """Against float64 on the GPU, with the same bounds."""
+    d, x, w, t, g = loss_case(M, D, V, dtype, seed=V)
+    loss, lse, dx, dw = loss_run(d, x, w, t, g)
+    f64 = torch.float64
+    xd, wd, td = x.to(f64), w.to(f64), torch.from_numpy(t).long().cuda()
+    z = xd @ wd.t()
+    wl = torch.logsumexp(z, 1)
+    ok = (td >= 0) & (td < V)
+    at = td.clamp(0, V - 1)
+    wloss = torch.where(ok, wl - z[torch.arange(M, device="cuda"), at], 0.0)
+    p = torch.exp(z - wl[:, None])
+    ez = D * sbd.U * (xd.abs() @ wd.abs().t())
+    el = (p * ez).sum(1) + sbd.U * (100 + V / 512 + 2 * np.log(V) + 4 * wl.abs()
+                                    + 2 * z.abs().amax(1))
+    check("lse", lse, host(wl), host(el))
+    check("loss", loss, host(wloss), host(torch.where(ok, el + ez.amax(1)
+                                                      + sbd.U * (wl.abs() + z.abs().amax(1)), 0)))
+    ep = p * (ez + el[:, None] + (2 * (z - wl[:, None]).abs() + 6) * sbd.U)
+    gd = torch.where(ok, g.to(f64).nan_to_num(), 0.0)[:, None]
+    dz = p.clone()
+    dz[torch.arange(M, device="cuda")[ok], at[ok]] -= 1
+    dz *= gd
+    ed = gd.abs() * ep + (3 * sbd.U + (2.0 ** -16 if dtype == "bf16" else 0)) * dz.abs()
+    check("dx", dx, host(dz @ wd), host((ed + (V + 8) * sbd.U * dz.abs()) @ wd.abs()))
+    check("dw", dw, host(dz.t().contiguous() @ xd),
+          host((ed + (M + 8) * sbd.U * dz.abs()).t().contiguous() @ xd.abs()))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_cross_entropy_special_values(dtype):
+    """Large logits; words of -inf; rows with a NaN or +inf logit; a row of -inf alone."""
+    M, D, V = 70, 16, 300
+    dt = DT[dtype]
+    x = torch.zeros(M, D, device="cuda", dtype=dt)
+    w = torch.zeros(V, D, device="cuda", dtype=dt)
+    x[:, 0], w[:, 0] = 1.0, dev(rng(0).standard_normal(V), dt) * 5000  # logits of thousands
+    w[7, 1] = float("-inf")
+    x[3, 1], x[4, 1] = 1.0, -1.0        # the word 7 at -inf, at +inf
+    x[5, 2] = float("nan")
+    x[0:2, 1] = x[6:, 1] = 2.0
+    x[2, 1] = 1.0
+    t = torch.arange(M, device="cuda", dtype=torch.int32)
+    d = ssm.loss_dims(M, D, V, dtype)
+    loss, lse = empty(M), empty(M)
+    ws = ssm.ssm_workspace(d, ssm.CROSS_ENTROPY)
+    w[7, 0] = 0
+    ssm.swimba_cross_entropy(d, x, w, t, loss, lse, ws)
+    z = w[:, 0].double().clone()
+    z[7] = float("-inf")
+    want = torch.logsumexp(z, 0)
+    ok = [i for i in range(M) if i not in (4, 5, 7)]
+    # thousands are exact here, but for the rounding of lse
+    assert ((lse[ok].double() - want).abs() <= 8 * sbd.U * want.abs()).all()
+    wl = want - z[t[ok].long()]
+    assert ((loss[ok].double() - wl).abs() <= 8 * sbd.U * (want.abs() + wl.abs())).all()
+    assert not torch.isfinite(lse[4]) and torch.isnan(lse[5]) and loss[7] == float("inf")
+    w[:, 1] = float("-inf")
+    x[:, 1] = 1.0
+    x[5, 2] = 0.0
+    ssm.swimba_cross_entropy(d, x, w, t, loss, lse, ws)
+    assert (lse == float("-inf")).all()
+    # no target anywhere: no loss, no gradient
+    x[:, 1], w[:, 1] = 0.0, 0.0
+    none = torch.full((M,), -1, device="cuda", dtype=torch.int32)
+    none[::2] = V
+    ssm.swimba_cross_entropy(d, x, w, none, loss, lse, ws)
+    assert not loss.any() and torch.isfinite(lse).all()
+    dx, dw = empty(M, D), empty(V, D)
+    ssm.swimba_cross_entropy_backward(d, x, w, none, lse, empty(M), dx, dw,
+                                      ssm.ssm_workspace(d, ssm.CROSS_ENTROPY_BACKWARD))
+    assert not dx.any() and not dw.any()
+
+
+def test_cross_entropy_without_tokens():
+    d = ssm.loss_dims(0, 16, 40, "f32")
+    w, dw, e = torch.ones(40, 16, device="cuda"), empty(40, 16), torch.empty(0, device="cuda")
+    t = torch.empty(0, dtype=torch.int32, device="cuda")
+    ssm.swimba_cross_entropy(d, e, w, t, e, e, None)
+    ssm.swimba_cross_entropy_backward(d, e, w, t, e, e, e, dw, None)
+    assert not dw.any()
