@@ -26,13 +26,14 @@
 #include <type_traits>
 
 #include "common.hpp"
+#include "lds_tiles.hpp"
 #include "ssm.hpp"
 
 namespace swimba {
 
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr int kTok = 16;     // tokens per block
 constexpr int kQ = 4;        // states per lane
 constexpr int kWaveCh = 16;  // channels per wave
@@ -54,8 +55,14 @@ __host__ __device__ inline int group_blocks(int Ch, int N, int G) {
 template <int CTRL> __device__ __forceinline__ float dpp(float v) {
   return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xF, 0xF, true));
 }
-// Lane q of each four, to all four.
-template <int Q> __device__ __forceinline__ float quad(float v) { return dpp<Q * 0x55>(v); }
+// Lane q of each four, to all four, once: the vector units run DPP operands at half
+// the rate of registers, so the (empty) use keeps the move from being folded into
+// each of the multiplications that follow.
+template <int Q> __device__ __forceinline__ float quad(float v) {
+  float r = dpp<Q * 0x55>(v);
+  asm("" : "+v"(r));
+  return r;
+}
 // The sum over the four lanes, in all of them.
 __device__ __forceinline__ float quad_sum(float v) {
   v += dpp<0xB1>(v);         // lane ^ 1
@@ -100,23 +107,19 @@ __device__ __forceinline__ float rcp_(float x) { return __builtin_amdgcn_rcpf(x)
 __device__ __forceinline__ float sigm(float x) { return rcp_(1.f + exp2_(-x * kLog2e)); }
 
 // softplus(v) = max(v, 0) + log(1 + t), t = exp(-|v|) in (0, 1], the logarithm as
-// 2 atanh(s), s = t / (2 + t) <= 1/3, from its series up to s^17 (what it leaves
-// out is below 2^-27 of the sum): log of a rounded 1 + t would lose a small step's
-// relative precision. SIG: sigmoid(v) as well.
-template <bool SIG>
+// 2 atanh(s), s = t / (2 + t) <= 1/3 (log of a rounded 1 + t would lose a small
+// step's relative precision). atanh(s) / s is a polynomial of degree 4 in s^2,
+// fitted for this file by reweighted least squares on 0 <= s^2 <= 1/9: relative
+// error 8e-9, 7e-8 evaluated in fp32. sig: sigmoid(v) (left out where not used).
 __device__ __forceinline__ float softplus(float v, float& sig) {
   const float t = exp2_(-fabsf(v) * kLog2e);
   const float s = t * rcp_(2.f + t), q = s * s;
-  float p = 1.f / 17;
-  p = __builtin_fmaf(p, q, 1.f / 15);
-  p = __builtin_fmaf(p, q, 1.f / 13);
-  p = __builtin_fmaf(p, q, 1.f / 11);
-  p = __builtin_fmaf(p, q, 1.f / 9);
-  p = __builtin_fmaf(p, q, 1.f / 7);
-  p = __builtin_fmaf(p, q, 1.f / 5);
-  p = __builtin_fmaf(p, q, 1.f / 3);
+  float p = 0.14089155197143555f;
+  p = __builtin_fmaf(p, q, 0.13980303704738617f);
+  p = __builtin_fmaf(p, q, 0.20012454688549042f);
+  p = __builtin_fmaf(p, q, 0.3333315849304199f);
   p = __builtin_fmaf(p, q, 1.f);
-  if constexpr (SIG) sig = (v >= 0.f ? 1.f : t) * rcp_(1.f + t);
+  sig = (v >= 0.f ? 1.f : t) * rcp_(1.f + t);
   return __builtin_fmaf(2.f * s, p, fmaxf(v, 0.f));  // (NaN through s)
 }
 
@@ -184,32 +187,38 @@ __device__ __forceinline__ void store_states(float* row, int n0, int N, floatx4 
 }
 
 // One value per token and channel of a block: lane (q, j) holds tokens 4 i + j.
+// The buffer ends with the block's rows in use, so that a row past them reads
+// zeros (and a store there is dropped); lanes without a channel are out of range.
 struct Four {
   uint32_t v[4];
 };
+__device__ __forceinline__ uint32_t four_offset(const Place& p, uint32_t pitch, uint32_t es) {
+  return p.on ? p.j * pitch + p.c * es : kOOB;
+}
 template <typename T>
 __device__ __forceinline__ Four load_four(const void* t, int64_t ld, const SScanArgs& A,
                                           const Place& p, int blk) {
-  const int t0 = blk * kTok, rows = min(kTok, p.len - t0);
-  const BufRes r = rows_buffer<T>(t, (size_t)p.b * A.T + t0, ld, rows, A.Ch);
-  const uint32_t pitch = (uint32_t)ld * sizeof(T);
-  const uint32_t off = p.j * pitch + p.c * (uint32_t)sizeof(T);
+  const int t0 = blk * kTok;
+  const BufRes r = rows_buffer<T>(t, (size_t)p.b * A.T + t0, ld, min(kTok, p.len - t0), A.Ch);
+  const uint32_t pitch = (uint32_t)ld * sizeof(T), off = four_offset(p, pitch, sizeof(T));
   Four f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    f.v[i] = load_bits<T>(r, p.on && 4 * i + p.j < rows ? off : kOOB, 4 * i * pitch);
+  for (int i = 0; i < 4; ++i) f.v[i] = load_bits<T>(r, off + 4 * i * pitch, 0);
   return f;
 }
 template <typename T>
 __device__ __forceinline__ void store_four(void* t, int64_t ld, const SScanArgs& A,
                                            const Place& p, int blk, const float (&v)[4]) {
-  const int t0 = blk * kTok, rows = min(kTok, A.T - t0);
-  const BufRes r = rows_buffer<T>(t, (size_t)p.b * A.T + t0, ld, rows, A.Ch);
-  const uint32_t pitch = (uint32_t)ld * sizeof(T);
-  const uint32_t off = p.j * pitch + p.c * (uint32_t)sizeof(T);
+  const int t0 = blk * kTok;
+  const BufRes r = rows_buffer<T>(t, (size_t)p.b * A.T + t0, ld, min(kTok, A.T - t0), A.Ch);
+  const uint32_t pitch = (uint32_t)ld * sizeof(T), off = four_offset(p, pitch, sizeof(T));
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    store_one<T>(r, p.on && 4 * i + p.j < rows ? off : kOOB, 4 * i * pitch, v[i]);
+  for (int i = 0; i < 4; ++i) store_one<T>(r, off + 4 * i * pitch, 0, v[i]);
+}
+// The values of a block that reaches past the length: zeros there.
+__device__ __forceinline__ void clear_tail(const Place& p, int blk, float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = blk * kTok + 4 * i + p.j < p.len ? v[i] : 0.f;
 }
 
 // B (or C) of a block of tokens: lane (q, j) loads states n0 .. n0 + 3 of token q,
@@ -272,6 +281,57 @@ struct SegBoard {
   }
 };
 
+// f(constant 0 .. 3), and the other way.
+template <class F> __device__ __forceinline__ void up4(F f) {
+  f(std::integral_constant<int, 0>());
+  f(std::integral_constant<int, 1>());
+  f(std::integral_constant<int, 2>());
+  f(std::integral_constant<int, 3>());
+}
+template <class F> __device__ __forceinline__ void down4(F f) {
+  f(std::integral_constant<int, 3>());
+  f(std::integral_constant<int, 2>());
+  f(std::integral_constant<int, 1>());
+  f(std::integral_constant<int, 0>());
+}
+
+// A lane's constants: A (times log2 e: decays are powers of 2), dt_bias, D. Lanes
+// without a channel hold zeros, so that all they compute from is zero.
+struct Coef {
+  floatx4 A2;
+  float bias, D;
+  __device__ Coef(const SScanArgs& A, const Place& p) {
+    A2 = load_states(A.A + (size_t)p.c * A.N, p.n0, A.N, p.on) * kLog2e;
+    bias = A.bias && p.on ? A.bias[p.c] : 0.f;
+    D = A.D && p.on ? A.D[p.c] : 0.f;
+  }
+};
+
+// v, carried through the segments from `from` up (or down) to `to`, without it: a
+// batch of them loaded at once.
+__device__ __forceinline__ void join_segments(const SScanArgs& A, const Place& p, const Coef& co,
+                                              int from, int to, floatx4& v) {
+  constexpr int kBatch = 8;
+  const SegBoard sb(A);
+  const int step = to >= from ? 1 : -1, n = (to - from) * step;
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    floatx4 e[kBatch];
+    float d[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const size_t row = sb.row(A, p, from + step * min(i0 + i, n - 1));
+      e[i] = *reinterpret_cast<const floatx4*>(sb.state + row * sb.np + p.n0);
+      d[i] = sb.sum[row];
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (i0 + i >= n) break;
+#pragma unroll
+      for (int k = 0; k < kQ; ++k) v[k] = __builtin_fmaf(exp2_(d[i] * co.A2[k]), v[k], e[i][k]);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- forward
 
 // Each segment's state from zero, and its sum of delta (of all but the last).
@@ -281,8 +341,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void sscan_ends_kernel(SScanArgs A)
   const Place p = place_of(A, A.segs - 1);
   floatx4(&bt)[kTok][4] = lds[threadIdx.x >> 6];
   const bool vec = vec_bc<T>(A);
-  const floatx4 A2 = load_states(A.A + (size_t)p.c * A.N, p.n0, A.N, p.on) * kLog2e;
-  const float bias = A.bias ? A.bias[p.c] : 0.f;
+  const Coef co(A, p);
   floatx4 h = {0.f, 0.f, 0.f, 0.f};
   float sum = 0.f;
   const int blk1 = min(p.blk1, (p.len + kTok - 1) / kTok);
@@ -295,30 +354,25 @@ __global__ __launch_bounds__(64 * kMaxWaves) void sscan_ends_kernel(SScanArgs A)
   };
   if (p.blk0 < blk1) fetch(p.blk0);
   for (int blk = p.blk0; blk < blk1; ++blk) {
-    float delta[4], u[4];
+    float delta[4], u[4], sig;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) delta[i] = softplus(value<T>(dr.v[i]) + co.bias, sig);
+    if ((blk + 1) * kTok > p.len) clear_tail(p, blk, delta);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float sig;
-      const bool in = blk * kTok + 4 * i + p.j < p.len;
-      delta[i] = in ? softplus<false>(value<T>(dr.v[i]) + bias, sig) : 0.f;
-      u[i] = in ? delta[i] * value<T>(xr.v[i]) : 0.f;
+      u[i] = delta[i] * value<T>(xr.v[i]);
       sum += delta[i];
     }
     bt[p.q][p.j] = widen<T>(br);
     if (blk + 1 < blk1) fetch(blk + 1);
 #pragma unroll
-    for (int t = 0; t < kTok; ++t) {
-      const floatx4 Bv = bt[t][p.j];
-      const auto one = [&](auto Q) {
-        const float d = quad<Q()>(delta[t / 4]), ut = quad<Q()>(u[t / 4]);
+    for (int i = 0; i < 4; ++i)
+      up4([&](auto Q) {
+        const floatx4 Bv = bt[4 * i + Q()][p.j];
+        const float d = quad<Q()>(delta[i]), ut = quad<Q()>(u[i]);
 #pragma unroll
-        for (int k = 0; k < kQ; ++k) h[k] = __builtin_fmaf(exp2_(d * A2[k]), h[k], ut * Bv[k]);
-      };
-      if (t % 4 == 0) one(std::integral_constant<int, 0>());
-      else if (t % 4 == 1) one(std::integral_constant<int, 1>());
-      else if (t % 4 == 2) one(std::integral_constant<int, 2>());
-      else one(std::integral_constant<int, 3>());
-    }
+        for (int k = 0; k < kQ; ++k) h[k] = __builtin_fmaf(exp2_(d * co.A2[k]), h[k], ut * Bv[k]);
+      });
   }
   sum = quad_sum(sum);
   if (!p.on) return;
@@ -339,8 +393,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256) void sscan_kernel(SSc
   const int nb = state_blocks(A.N), cw = channel_waves(A.N), np = nb * kStates;
   BC& bc = lds[wave];
   const bool vec = vec_bc<T>(A);
-  const floatx4 A2 = load_states(A.A + (size_t)p.c * A.N, p.n0, A.N, p.on) * kLog2e;
-  const float bias = A.bias ? A.bias[p.c] : 0.f, Dc = A.D ? A.D[p.c] : 0.f;
+  const Coef co(A, p);
   const int nblk = (A.T + kTok - 1) / kTok, live = (p.len + kTok - 1) / kTok;
   const int blk1 = min(p.blk1, live);
   Four xr, dr, zr;
@@ -357,27 +410,21 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256) void sscan_kernel(SSc
   floatx4 h = load_states(A.h_init ? A.h_init + ((size_t)p.b * A.Ch + p.c) * A.N : nullptr, p.n0,
                           A.N, p.on);
   if (A.segs > 1) {
-    const SegBoard sb(A);
-    for (int s = 0; s < p.seg; ++s) {
-      const size_t row = sb.row(A, p, s);
-      const floatx4 e = *reinterpret_cast<const floatx4*>(sb.state + row * sb.np + p.n0);
-      const float d = sb.sum[row];
-#pragma unroll
-      for (int k = 0; k < kQ; ++k) h[k] = __builtin_fmaf(exp2_(d * A2[k]), h[k], e[k]);
-    }
+    join_segments(A, p, co, 0, p.seg, h);
   }
   for (int blk = p.blk0; blk < blk1; ++blk) {
     if (A.carry && p.on)
       *reinterpret_cast<floatx4*>(A.carry + (((size_t)p.b * nblk + blk) * A.Ch + p.c) * np +
                                   p.n0) = h;
-    float x[4], delta[4], u[4], gate[4], out[4];
+    float x[4], delta[4], u[4], gate[4], out[4], sig;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) delta[i] = softplus(value<T>(dr.v[i]) + co.bias, sig);
+    const bool tail = (blk + 1) * kTok > p.len;
+    if (tail) clear_tail(p, blk, delta);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float sig;
-      const bool in = blk * kTok + 4 * i + p.j < p.len;
-      delta[i] = in ? softplus<false>(value<T>(dr.v[i]) + bias, sig) : 0.f;
       x[i] = value<T>(xr.v[i]);
-      u[i] = in ? delta[i] * x[i] : 0.f;
+      u[i] = delta[i] * x[i];
       if constexpr (GATED) {
         const float z = value<T>(zr.v[i]);
         gate[i] = z * sigm(z);
@@ -389,29 +436,24 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256) void sscan_kernel(SSc
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float y[4];
-      const auto one = [&](auto Q) {
-        constexpr int qq = Q();
-        const floatx4 Bv = bc.b[4 * i + qq][p.j], Cv = bc.c[4 * i + qq][p.j];
-        const float d = quad<qq>(delta[i]), ut = quad<qq>(u[i]);
+      up4([&](auto Q) {
+        const floatx4 Bv = bc.b[4 * i + Q()][p.j], Cv = bc.c[4 * i + Q()][p.j];
+        const float d = quad<Q()>(delta[i]), ut = quad<Q()>(u[i]);
         float s = 0.f;
 #pragma unroll
         for (int k = 0; k < kQ; ++k) {
-          h[k] = __builtin_fmaf(exp2_(d * A2[k]), h[k], ut * Bv[k]);
+          h[k] = __builtin_fmaf(exp2_(d * co.A2[k]), h[k], ut * Bv[k]);
           s = __builtin_fmaf(Cv[k], h[k], s);
         }
-        y[qq] = s;
-      };
-      one(std::integral_constant<int, 0>());
-      one(std::integral_constant<int, 1>());
-      one(std::integral_constant<int, 2>());
-      one(std::integral_constant<int, 3>());
+        y[Q()] = s;
+      });
       out[i] = quad_spread(y, p.j);
     }
     if constexpr (SPLIT) {
       const int half = blk & 1;
 #pragma unroll
       for (int i = 0; i < 4; ++i) part[half][wave][i][lane] = out[i];
-      __syncthreads();
+      stage_barrier();
       if (p.sb == 0)
         for (int s = 1; s < nb; ++s)
 #pragma unroll
@@ -420,10 +462,10 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256) void sscan_kernel(SSc
     if (!SPLIT || p.sb == 0) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        out[i] = __builtin_fmaf(Dc, x[i], out[i]);
+        out[i] = __builtin_fmaf(co.D, x[i], out[i]);
         if constexpr (GATED) out[i] *= gate[i];
-        if (blk * kTok + 4 * i + p.j >= p.len) out[i] = 0.f;
       }
+      if (tail) clear_tail(p, blk, out);
       store_four<T>(A.y, A.Ch, A, p, blk, out);
     }
   }
@@ -438,17 +480,6 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256) void sscan_kernel(SSc
 
 // ---------------------------------------------------------------- backward
 
-// What a block gives per token and channel, without the states.
-template <typename T, bool GATED>
-__device__ __forceinline__ void gate_grad(uint32_t dyb, uint32_t zb, bool in, float& v) {
-  v = value<T>(dyb);
-  if constexpr (GATED) {
-    const float z = value<T>(zb);
-    v *= z * sigm(z);
-  }
-  v = in ? v : 0.f;
-}
-
 // Each segment's gradient of the state that enters it, from zero behind it, and
 // its sum of delta (of all but the first).
 template <typename T, bool GATED>
@@ -461,8 +492,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void sscan_bwd_ends_kernel(SScanArg
   p.blk1 = min(nblk, p.blk0 + A.seg_blocks);
   floatx4(&ct)[kTok][4] = lds[threadIdx.x >> 6];
   const bool vec = vec_bc<T>(A);
-  const floatx4 A2 = load_states(A.A + (size_t)p.c * A.N, p.n0, A.N, p.on) * kLog2e;
-  const float bias = A.bias ? A.bias[p.c] : 0.f;
+  const Coef co(A, p);
   floatx4 c = {0.f, 0.f, 0.f, 0.f};
   float sum = 0.f;
   const int blk1 = min(p.blk1, (p.len + kTok - 1) / kTok);
@@ -476,30 +506,30 @@ __global__ __launch_bounds__(64 * kMaxWaves) void sscan_bwd_ends_kernel(SScanArg
   };
   if (p.blk0 < blk1) fetch(blk1 - 1);
   for (int blk = blk1 - 1; blk >= p.blk0; --blk) {
-    float delta[4], v[4];
+    float delta[4], v[4], sig;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) delta[i] = softplus(value<T>(dr.v[i]) + co.bias, sig);
+    if ((blk + 1) * kTok > p.len) clear_tail(p, blk, delta);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float sig;
-      const bool in = blk * kTok + 4 * i + p.j < p.len;
-      delta[i] = in ? softplus<false>(value<T>(dr.v[i]) + bias, sig) : 0.f;
-      gate_grad<T, GATED>(gr.v[i], GATED ? zr.v[i] : 0, in, v[i]);
+      v[i] = value<T>(gr.v[i]);
+      if constexpr (GATED) {
+        const float z = value<T>(zr.v[i]);
+        v[i] *= z * sigm(z);
+      }
       sum += delta[i];
     }
     ct[p.q][p.j] = widen<T>(cr);
     if (blk > p.blk0) fetch(blk - 1);
 #pragma unroll
-    for (int t = kTok - 1; t >= 0; --t) {
-      const floatx4 Cv = ct[t][p.j];
-      const auto one = [&](auto Q) {
-        const float d = quad<Q()>(delta[t / 4]), vt = quad<Q()>(v[t / 4]);
+    for (int i = 3; i >= 0; --i)
+      down4([&](auto Q) {
+        const floatx4 Cv = ct[4 * i + Q()][p.j];
+        const float d = quad<Q()>(delta[i]), vt = quad<Q()>(v[i]);
 #pragma unroll
-        for (int k = 0; k < kQ; ++k) c[k] = exp2_(d * A2[k]) * __builtin_fmaf(Cv[k], vt, c[k]);
-      };
-      if (t % 4 == 0) one(std::integral_constant<int, 0>());
-      else if (t % 4 == 1) one(std::integral_constant<int, 1>());
-      else if (t % 4 == 2) one(std::integral_constant<int, 2>());
-      else one(std::integral_constant<int, 3>());
-    }
+        for (int k = 0; k < kQ; ++k)
+          c[k] = exp2_(d * co.A2[k]) * __builtin_fmaf(Cv[k], vt, c[k]);
+      });
   }
   sum = quad_sum(sum);
   if (!p.on) return;
@@ -531,8 +561,8 @@ struct BwdBoard {
   }
 };
 
-// r[i] of lanes l and l ^ 32, l ^ 16 exchanged and added: values a and b of all
-// lanes become one register, a's sum in the lower and b's in the upper of the two.
+// Values a and b of lanes l and l ^ 32 (or l ^ 16) exchanged and added: one register
+// with a's sum in the lower and b's in the upper of the two.
 __device__ __forceinline__ float fold32(float a, float b) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
@@ -556,6 +586,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256, SPLIT ? 1 : 2) void s
     SScanArgs A) {
   constexpr int WV = SPLIT ? kMaxWaves : 4;
   __shared__ BC lds[WV];
+  __shared__ floatx4 kept[WV][4][64];  // x, sigmoid, dy silu'(z), u: for the block's end
   __shared__ float2 dbc[2][WV][kTok][kStates];  // [token][kind, pair of states]
   __shared__ float part[SPLIT ? 2 : 1][SPLIT ? WV : 1][12][64];
   const Place p = place_of(A, A.segs);
@@ -563,14 +594,14 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256, SPLIT ? 1 : 2) void s
   const int nb = state_blocks(A.N), cw = channel_waves(A.N);
   BC& bc = lds[wave];
   const bool vec = vec_bc<T>(A);
-  const floatx4 Av = load_states(A.A + (size_t)p.c * A.N, p.n0, A.N, p.on), A2 = Av * kLog2e;
-  const float bias = A.bias ? A.bias[p.c] : 0.f, Dc = A.D ? A.D[p.c] : 0.f;
+  const Coef co(A, p);
   const int nblk = (A.T + kTok - 1) / kTok, live = (p.len + kTok - 1) / kTok;
   const int blk1 = min(p.blk1, live);
   const BwdBoard board(A);
   const int np = board.np;
   Four xr, dr, zr, gr;
   typename Bits<T>::t br, cr;
+  floatx4 hr;
   auto fetch = [&](int blk) {
     xr = load_four<T>(A.x, A.ldx, A, p, blk);
     dr = load_four<T>(A.dt, A.lddt, A, p, blk);
@@ -578,121 +609,131 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256, SPLIT ? 1 : 2) void s
     if constexpr (GATED) zr = load_four<T>(A.z, A.ldz, A, p, blk);
     br = load_bc<T>(A.B, A, p, blk, vec);
     cr = load_bc<T>(A.C, A, p, blk, vec);
+    // (of a lane without a channel: another channel's, which meets only zeros)
+    hr = *reinterpret_cast<const floatx4*>(
+        A.carry_in + (((size_t)p.b * nblk + blk) * A.Ch + p.c) * np + p.n0);
   };
   if (p.blk0 < blk1) fetch(blk1 - 1);
   // the gradient of the state that leaves the segment
   floatx4 c = load_states(A.dh_final ? A.dh_final + ((size_t)p.b * A.Ch + p.c) * A.N : nullptr,
                           p.n0, A.N, p.on);
   if (A.segs > 1) {
-    const SegBoard sb(A);
-    for (int s = A.segs - 1; s > p.seg; --s) {
-      const size_t row = sb.row(A, p, s);
-      const floatx4 e = *reinterpret_cast<const floatx4*>(sb.state + row * sb.np + p.n0);
-      const float d = sb.sum[row];
-#pragma unroll
-      for (int k = 0; k < kQ; ++k) c[k] = __builtin_fmaf(exp2_(d * A2[k]), c[k], e[k]);
-    }
+    join_segments(A, p, co, A.segs - 1, p.seg, c);
+    if (!p.on) c = floatx4{0.f, 0.f, 0.f, 0.f};
   }
   floatx4 dA = {0.f, 0.f, 0.f, 0.f};
   float dD = 0.f, dbias = 0.f;
   for (int blk = blk1 - 1; blk >= p.blk0; --blk) {
     const int half = blk & 1;
-    float x[4], delta[4], sig[4], u[4], v[4], dyv[4], zv[4];
+    const bool tail = (blk + 1) * kTok > p.len;
+    float delta[4], u[4], v[4];
+    {
+      float sig[4], g2[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool in = blk * kTok + 4 * i + p.j < p.len;
-      delta[i] = in ? softplus<true>(value<T>(dr.v[i]) + bias, sig[i]) : 0.f;
-      x[i] = value<T>(xr.v[i]);
-      u[i] = in ? delta[i] * x[i] : 0.f;
-      dyv[i] = value<T>(gr.v[i]);
-      if constexpr (GATED) zv[i] = value<T>(zr.v[i]);
-      gate_grad<T, GATED>(gr.v[i], GATED ? zr.v[i] : 0, in, v[i]);
+      for (int i = 0; i < 4; ++i) delta[i] = softplus(value<T>(dr.v[i]) + co.bias, sig[i]);
+      if (tail) clear_tail(p, blk, delta);
+      floatx4 xs;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        xs[i] = value<T>(xr.v[i]);
+        u[i] = delta[i] * xs[i];
+        v[i] = value<T>(gr.v[i]);
+        if constexpr (GATED) {
+          const float z = value<T>(zr.v[i]), sg = sigm(z);
+          g2[i] = v[i] * (sg * __builtin_fmaf(z, 1.f - sg, 1.f));
+          v[i] *= z * sg;
+        }
+        dD = __builtin_fmaf(v[i], xs[i], dD);
+      }
+      kept[wave][0][lane] = xs;
+      kept[wave][1][lane] = floatx4{sig[0], sig[1], sig[2], sig[3]};
+      if constexpr (GATED) kept[wave][2][lane] = floatx4{g2[0], g2[1], g2[2], g2[3]};
     }
     bc.b[p.q][p.j] = widen<T>(br);
     bc.c[p.q][p.j] = widen<T>(cr);
     floatx4 h[kTok + 1], a[kTok];
-    h[0] = floatx4{0.f, 0.f, 0.f, 0.f};
-    if (p.on)
-      h[0] = *reinterpret_cast<const floatx4*>(
-          A.carry_in + (((size_t)p.b * nblk + blk) * A.Ch + p.c) * np + p.n0);
-    if (blk > p.blk0) fetch(blk - 1);
+    h[0] = hr;
     // the block's states and u
-    float uy[4], eb[4], fa[4];
+    float eb[4], fa[4];
+    floatx4 uy = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float y[4];
-      const auto one = [&](auto Q) {
-        constexpr int qq = Q();
-        const int t = 4 * i + qq;
-        const floatx4 Bv = bc.b[t][p.j], Cv = bc.c[t][p.j];
-        const float d = quad<qq>(delta[i]), ut = quad<qq>(u[i]);
-        float s = 0.f;
+      up4([&](auto Q) {
+        const int t = 4 * i + Q();
+        const floatx4 Bv = bc.b[t][p.j];
+        const float d = quad<Q()>(delta[i]), ut = quad<Q()>(u[i]);
 #pragma unroll
         for (int k = 0; k < kQ; ++k) {
-          a[t][k] = exp2_(d * A2[k]);
+          a[t][k] = exp2_(d * co.A2[k]);
           h[t + 1][k] = __builtin_fmaf(a[t][k], h[t][k], ut * Bv[k]);
-          if constexpr (GATED) s = __builtin_fmaf(Cv[k], h[t + 1][k], s);
         }
-        y[qq] = s;
-      };
-      one(std::integral_constant<int, 0>());
-      one(std::integral_constant<int, 1>());
-      one(std::integral_constant<int, 2>());
-      one(std::integral_constant<int, 3>());
-      uy[i] = GATED ? quad_spread(y, p.j) : 0.f;
+        if constexpr (GATED) {
+          const floatx4 Cv = bc.c[t][p.j];
+          float s = 0.f;
+#pragma unroll
+          for (int k = 0; k < kQ; ++k) s = __builtin_fmaf(Cv[k], h[t + 1][k], s);
+          y[Q()] = s;
+        }
+      });
+      if constexpr (GATED) uy[i] = quad_spread(y, p.j);
+      __builtin_amdgcn_sched_barrier(0);  // (reads of many tokens ahead would spill)
     }
+    if constexpr (GATED) kept[wave][3][lane] = uy;
     // back through it
 #pragma unroll
     for (int i = 3; i >= 0; --i) {
-      float yb[4], ya[4], w[4][8];  // w[q]: the token's dB and dC of this lane
-      const auto one = [&](auto Q) {
-        constexpr int qq = Q();
-        const int t = 4 * i + qq;
+      float yb[4], ya[4], w[2][8], r16[2][8];  // w: two tokens' dB and dC of this lane
+      down4([&](auto Q) {
+        const int t = 4 * i + Q();
         const floatx4 Bv = bc.b[t][p.j], Cv = bc.c[t][p.j];
-        const float d = quad<qq>(delta[i]), ut = quad<qq>(u[i]), vt = quad<qq>(v[i]);
+        const float d = quad<Q()>(delta[i]), ut = quad<Q()>(u[i]), vt = quad<Q()>(v[i]);
         float sb = 0.f, sa = 0.f;
 #pragma unroll
         for (int k = 0; k < kQ; ++k) {
           const float e = __builtin_fmaf(Cv[k], vt, c[k]);
-          const float flow = e * (a[t][k] * h[t][k]);
-          sb = __builtin_fmaf(e, Bv[k], sb);
-          sa = __builtin_fmaf(flow, Av[k], sa);
-          dA[k] = __builtin_fmaf(flow, d, dA[k]);
           c[k] = a[t][k] * e;
-          w[qq][k] = p.on ? e * ut : 0.f;
-          w[qq][4 + k] = p.on ? vt * h[t + 1][k] : 0.f;
+          const float flow = c[k] * h[t][k];
+          sb = __builtin_fmaf(e, Bv[k], sb);
+          sa = __builtin_fmaf(flow, co.A2[k], sa);
+          dA[k] = __builtin_fmaf(flow, d, dA[k]);
+          w[Q() & 1][k] = e * ut;
+          w[Q() & 1][4 + k] = vt * h[t + 1][k];
         }
-        yb[qq] = sb;
-        ya[qq] = sa;
-      };
-      one(std::integral_constant<int, 3>());
-      one(std::integral_constant<int, 2>());
-      one(std::integral_constant<int, 1>());
-      one(std::integral_constant<int, 0>());
+        yb[Q()] = sb;
+        ya[Q()] = sa;
+        // sums over the wave's channels: lane (bit 5: the later token of a pair, bit 4:
+        // the pair, bit 3: dB or dC, bit 2: which pair of its four states, j) ends with
+        // two of them
+        if constexpr (Q() % 2 == 0) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) r16[Q() / 2][k] = fold32(w[0][k], w[1][k]);
+        }
+      });
       eb[i] = quad_spread(yb, p.j);
       fa[i] = quad_spread(ya, p.j);
-      // sums over the wave's channels: lane (bits 5, 4: token of the four, bit 3: dB or
-      // dC, bit 2: which pair of its four states, j) ends with two of them
-      float r8[8], r4[4], r2[2];
+      float r4[4], r2[2];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        r8[k] = fold16(fold32(w[0][k], w[2][k]), fold32(w[1][k], w[3][k]));
-#pragma unroll
-      for (int k = 0; k < 4; ++k) r4[k] = fold8(r8[k], r8[4 + k], lane & 8);
+      for (int k = 0; k < 4; ++k)
+        r4[k] = fold8(fold16(r16[0][k], r16[1][k]), fold16(r16[0][4 + k], r16[1][4 + k]), lane & 8);
 #pragma unroll
       for (int k = 0; k < 2; ++k) r2[k] = fold4(r4[k], r4[2 + k], lane & 4);
-      dbc[half][wave][4 * i + (lane >> 4)][(lane >> 3 & 1) * 8 + 2 * p.j + (lane >> 2 & 1)] =
+      const int t = 4 * i + 2 * (lane >> 4 & 1) + (lane >> 5);
+      dbc[half][wave][t][(lane >> 3 & 1) * 8 + 2 * p.j + (lane >> 2 & 1)] =
           make_float2(r2[0], r2[1]);
+      // the next block's loads, once half of this one's states are done with
+      if (i == 2 && blk > p.blk0) fetch(blk - 1);
+      __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (SPLIT) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        part[half][wave][i][lane] = uy[i];
+        if constexpr (GATED) part[half][wave][i][lane] = kept[wave][3][lane][i];
         part[half][wave][4 + i][lane] = eb[i];
         part[half][wave][8 + i][lane] = fa[i];
       }
     }
-    __syncthreads();
+    stage_barrier();
     // partial dB and dC of the workgroup's channels: the waves of channels in order
     {
       const int rows = min(kTok, A.T - blk * kTok);
@@ -710,34 +751,40 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256, SPLIT ? 1 : 2) void s
           *reinterpret_cast<float2*>(out + ((size_t)2 * t + m / 8) * np + s * kStates + 2 * (m % 8)) = r;
       }
     }
+    if constexpr (GATED) uy = kept[wave][3][lane];
     if constexpr (SPLIT) {
       if (p.sb == 0)
         for (int s = 1; s < nb; ++s)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uy[i] += part[half][s * cw + p.cw][i][lane];
+            if constexpr (GATED) uy[i] += part[half][s * cw + p.cw][i][lane];
             eb[i] += part[half][s * cw + p.cw][4 + i][lane];
             fa[i] += part[half][s * cw + p.cw][8 + i][lane];
           }
     }
     if (!SPLIT || p.sb == 0) {
+      const floatx4 x = kept[wave][0][lane], sig = kept[wave][1][lane];
       float ox[4], od[4], oz[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const bool in = blk * kTok + 4 * i + p.j < p.len;
-        const float dd = __builtin_fmaf(x[i], eb[i], fa[i]) * sig[i];
-        ox[i] = in ? __builtin_fmaf(delta[i], eb[i], Dc * v[i]) : 0.f;
-        od[i] = in ? dd : 0.f;
-        dbias += od[i];
-        dD += in ? v[i] * x[i] : 0.f;
-        if constexpr (GATED) {
-          const float sg = sigm(zv[i]), uu = __builtin_fmaf(Dc, x[i], uy[i]);
-          oz[i] = in ? dyv[i] * uu * (sg * __builtin_fmaf(zv[i], 1.f - sg, 1.f)) : 0.f;
-        }
+        ox[i] = __builtin_fmaf(delta[i], eb[i], co.D * v[i]);
+        od[i] = __builtin_fmaf(x[i], eb[i], fa[i] * kLn2) * sig[i];
       }
+      if (tail) {
+        clear_tail(p, blk, ox);
+        clear_tail(p, blk, od);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dbias += od[i];
       store_four<T>(A.dx, A.lddx, A, p, blk, ox);
       store_four<T>(A.ddt, A.ldddt, A, p, blk, od);
-      if constexpr (GATED) store_four<T>(A.dz, A.lddz, A, p, blk, oz);
+      if constexpr (GATED) {
+        const floatx4 g2 = kept[wave][2][lane];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) oz[i] = g2[i] * __builtin_fmaf(co.D, x[i], uy[i]);
+        if (tail) clear_tail(p, blk, oz);
+        store_four<T>(A.dz, A.lddz, A, p, blk, oz);
+      }
     }
   }
   if (!SPLIT || p.sb == 0) {
@@ -780,23 +827,40 @@ __global__ __launch_bounds__(256) void sscan_sum_kernel(SScanArgs A, unsigned fi
     if (A.lens) len = A.lens[b];
     if (t < len) {
       const float* p = bd.bc + (size_t)g * gb * bd.bc_step + (m * 2 + kind) * bd.np + n;
+#pragma unroll 8
       for (int s = 0; s < gb; ++s) v += p[s * bd.bc_step];
     }
     static_cast<T*>(kind ? A.dC : A.dB)[m * A.lddbc + gn] = from_f32<T>(v);
     return;
   }
-  const size_t q = (size_t)(blockIdx.x - first) * 256 + threadIdx.x;
-  const int rows = A.Bt * A.segs;
-  const size_t na = (size_t)A.Ch * A.N;
+  // 64 of them a workgroup, a quarter of the rows each wave
+  __shared__ float sum[4][64];
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  const size_t q = (size_t)(blockIdx.x - first) * 64 + lane, na = (size_t)A.Ch * A.N;
+  const int rows = A.Bt * A.segs, per = (rows + 3) / 4, r1 = min(rows, (wave + 1) * per);
+  const float* p = nullptr;
+  size_t pitch = 0;
   if (q < na) {
     const size_t c = q / A.N, n = q - c * A.N;
-    float v = 0.f;
-    for (int r = 0; r < rows; ++r) v += bd.da[((size_t)r * A.Ch + c) * bd.np + n];
-    A.dA[q] = v;
+    p = bd.da + c * bd.np + n;
+    pitch = (size_t)A.Ch * bd.np;
   } else if (q < na + 2 * (size_t)A.Ch) {
+    p = bd.dd + (q - na);
+    pitch = 2 * (size_t)A.Ch;
+  }
+  float v = 0.f;
+  if (p) {
+#pragma unroll 8
+    for (int r = wave * per; r < r1; ++r) v += p[r * pitch];
+  }
+  sum[wave][lane] = v;
+  __syncthreads();
+  if (wave || !p) return;
+  v = sum[0][lane] + sum[1][lane] + sum[2][lane] + sum[3][lane];
+  if (q < na) {
+    A.dA[q] = v;
+  } else {
     const size_t i = q - na;
-    float v = 0.f;
-    for (int r = 0; r < rows; ++r) v += bd.dd[(size_t)r * 2 * A.Ch + i];
     float* out = i < (size_t)A.Ch ? A.dD : A.dbias;
     if (out) out[i < (size_t)A.Ch ? i : i - A.Ch] = v;
   }
@@ -821,7 +885,7 @@ __global__ __launch_bounds__(256) void sscan_step_kernel(SScanArgs A) {
   const float* Ap = A.A + (size_t)c * A.N;
   float* ho = A.h + q * A.N;
   float sig;
-  const float delta = softplus<false>(dt, sig), u = delta * x;
+  const float delta = softplus(dt, sig), u = delta * x;
   float s = 0.f;
   const bool vec = vec_bc<T>(A);
   for (int n0 = 4 * j; n0 < A.N; n0 += kStates) {
@@ -870,7 +934,7 @@ void segments(SScanArgs& A, int64_t want) {
   A.seg_blocks = (int)((nblk + s - 1) / s);
   A.segs = (nblk + A.seg_blocks - 1) / A.seg_blocks;
 }
-constexpr int64_t kWant = 512, kWantBwd = 512;
+constexpr int64_t kWant = 2048, kWantBwd = 2048;
 
 unsigned workgroups(const SScanArgs& A, int segs) {
   return (unsigned)((int64_t)A.Bt * segs * A.G * group_blocks(A.Ch, A.N, A.G));
@@ -925,7 +989,7 @@ hipError_t backward(SScanArgs A, hipStream_t s) {
   const size_t na = (size_t)A.Ch * (A.N + 2);
   const unsigned first = (unsigned)((nbc + 255) / 256);
   return launch("selective_scan_sum", sscan_sum_kernel<T>,
-                dim3(first + (unsigned)((na + 255) / 256)), dim3(256), 0, s, A, first);
+                dim3(first + (unsigned)((na + 63) / 64)), dim3(256), 0, s, A, first);
 }
 
 }  // namespace
