@@ -2,10 +2,10 @@
 // backward and one token:
 //   s_t = bias + sum_k w[k] x_{t-W+1+k},  y = act(s);
 //   ds = dy act'(s),  dx_t = sum_k w[k] ds_{t+W-1-k},  dw[k] = sum_t ds_t x_{t-W+1+k}.
-// Bound by HBM: a thread owns 16 bytes of channels (one element where rows do not
-// allow it) and walks a run of tokens with the last W inputs (backward: and the
-// last W ds) in registers, the next 8 rows requested while 8 are computed; only
-// the W - 1 rows at the ends of a run are read twice. The backward recomputes s,
+// Bound by HBM: a thread owns 16 bytes of channels (backward: 8; one element where
+// rows do not allow it) and walks a run of tokens with the last W inputs (backward:
+// and the last W ds) in registers, the next 8 (4) rows requested while as many are
+// computed; only the W - 1 rows at the ends of a run are read twice. The backward recomputes s,
 // so the forward keeps nothing. Sums over tokens: a run's in registers, the runs'
 // in a second kernel, in order.
 #include <algorithm>
@@ -19,7 +19,8 @@ namespace swimba {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kStep = 8;  // rows in flight per thread
+constexpr int kStep = 8;     // rows in flight per thread
+constexpr int kStepBwd = 4;  // the same of the backward, of x and of dy
 
 template <typename T, int VEC> struct Raw {
   typedef T t __attribute__((ext_vector_type(VEC)));
@@ -180,9 +181,9 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs A) {
   };
   // the outputs of the run are complete W - 1 tokens behind its end
   const int end = t1 + W - 1;
-  Vt<T, VEC> nx[kStep], nd[kStep];
+  Vt<T, VEC> nx[kStepBwd], nd[kStepBwd];
 #pragma unroll
-  for (int i = 0; i < kStep; ++i) {
+  for (int i = 0; i < kStepBwd; ++i) {
     nx[i] = input_at<T, VEC, W>(A, r.b, r.c, r.t0 + i, min(r.len, end));
     nd[i] = r.t0 + i < end ? gradient(r.t0 + i) : zero_raw<T, VEC>();
   }
@@ -192,18 +193,18 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs A) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) win[k][j] = to_f32(v[j]);
   }
-  for (int t = r.t0; t < end; t += kStep) {
-    Vt<T, VEC> cx[kStep], cd[kStep];
+  for (int t = r.t0; t < end; t += kStepBwd) {
+    Vt<T, VEC> cx[kStepBwd], cd[kStepBwd];
 #pragma unroll
-    for (int i = 0; i < kStep; ++i) {
-      const int tn = t + kStep + i;
+    for (int i = 0; i < kStepBwd; ++i) {
+      const int tn = t + kStepBwd + i;
       cx[i] = nx[i];
       cd[i] = nd[i];
       nx[i] = input_at<T, VEC, W>(A, r.b, r.c, tn, min(r.len, end));
       nd[i] = tn < end ? gradient(tn) : zero_raw<T, VEC>();
     }
 #pragma unroll
-    for (int i = 0; i < kStep; ++i) {
+    for (int i = 0; i < kStepBwd; ++i) {
       const int tt = t + i, out = tt - (W - 1);  // ds of tt completes the gradient of input out
       const bool mine = tt < t1 && tt < r.len;
       float g[VEC];
@@ -253,20 +254,23 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs A) {
   store_f32<VEC>(part + (size_t)W * A.C, db);
 }
 
-// dw and db: the runs' sums added in order, 64 columns a workgroup, a quarter of
+// dw and db: the runs' sums added in order, 64 columns a workgroup, a sixteenth of
 // the runs each wave.
-__global__ __launch_bounds__(256) void conv_sum_kernel(ConvArgs A, size_t runs) {
-  __shared__ float sum[4][64];
+__global__ __launch_bounds__(1024) void conv_sum_kernel(ConvArgs A, size_t runs) {
+  __shared__ float sum[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const size_t cols = (size_t)(A.W + 1) * A.C, q = (size_t)blockIdx.x * 64 + lane;
-  const size_t per = (runs + 3) / 4, r1 = min(runs, (wave + 1) * per);
+  const size_t per = (runs + 15) / 16, r1 = min(runs, (wave + 1) * per);
   float v = 0.f;
-  if (q < cols)
+  if (q < cols) {
+#pragma unroll 8
     for (size_t r = wave * per; r < r1; ++r) v += A.part[r * cols + q];
+  }
   sum[wave][lane] = v;
   __syncthreads();
   if (wave || q >= cols) return;
-  v = sum[0][lane] + sum[1][lane] + sum[2][lane] + sum[3][lane];
+#pragma unroll
+  for (int w = 1; w < 16; ++w) v += sum[w][lane];
   const int k = (int)(q / A.C), c = (int)(q - (size_t)k * A.C);
   if (k < A.W) A.dw[(size_t)c * A.W + k] = v;
   else if (A.db) A.db[c] = v;
@@ -308,18 +312,25 @@ __global__ __launch_bounds__(256) void conv_state_kernel(const T* from, T* to, s
 }
 
 // Tokens per thread: long runs read few rows twice and leave few partial sums, as
-// long as some 2^17 threads remain to fill the card.
-int run_length(int64_t Bt, int64_t T, int64_t vecs) {
-  const int64_t r = Bt * T * vecs >> 17;
+// long as enough threads remain to fill the card, some 2^18 forward (8 x 2048 x
+// 1536: 20 us; 2^17: 23, 2^19: 22) and, for the partial sums, 2^17 backward (41 us;
+// 2^16: 57, 2^18: 43, 2^19: 50).
+constexpr int kFwdThreads = 18, kBwdThreads = 17;
+int run_length(int64_t Bt, int64_t T, int64_t vecs, int threads) {
+  const int64_t r = Bt * T * vecs >> threads;
   return (int)std::min<int64_t>(256, std::max<int64_t>(kStep, r / kStep * kStep));
 }
-int vec_of(bool is_bf16, int C, int64_t ldx, int64_t lddx) {
-  const int v = is_bf16 ? 8 : 4;
+// Channels per thread: v, where rows allow it.
+int vec_of(int v, int C, int64_t ldx, int64_t lddx) {
   return C % v == 0 && ldx % v == 0 && lddx % v == 0 ? v : 1;
 }
+// 16 bytes of them forward; 8 in the backward, whose registers then leave room for
+// four waves instead of one (padded 8 x 2048 x 1536: 78 -> 40 us; 4 bytes: 54).
+int vec_fwd(bool is_bf16) { return is_bf16 ? 8 : 4; }
+int vec_bwd(bool is_bf16) { return is_bf16 ? 4 : 2; }
 
 // f(element type, channels per thread, width)
-template <class F>
+template <int VB, int VF, class F>
 hipError_t with_kernel(bool is_bf16, int vec, int W, F f) {
   auto width = [&](auto t, auto v) {
     if (W == 2) return f(t, v, std::integral_constant<int, 2>());
@@ -328,8 +339,8 @@ hipError_t with_kernel(bool is_bf16, int vec, int W, F f) {
   };
   const std::integral_constant<int, 1> one{};
   if (is_bf16)
-    return vec == 1 ? width(bf16(), one) : width(bf16(), std::integral_constant<int, 8>());
-  return vec == 1 ? width(0.f, one) : width(0.f, std::integral_constant<int, 4>());
+    return vec == 1 ? width(bf16(), one) : width(bf16(), std::integral_constant<int, VB>());
+  return vec == 1 ? width(0.f, one) : width(0.f, std::integral_constant<int, VF>());
 }
 
 dim3 blocks_of(size_t threads) { return dim3((unsigned)((threads + 255) / 256)); }
@@ -341,34 +352,34 @@ size_t runs_of(const ConvArgs& A) { return (size_t)A.Bt * ((A.T + A.run - 1) / A
 size_t conv_bwd_ws_bytes(int Bt, int T, int C) {
   // the shortest runs that any strides lead to
   size_t runs = 0;
-  for (int v : {1, 4, 8}) {
-    const int run = run_length(Bt, T, std::max(1, C / v));
+  for (int v : {1, 2, 4}) {
+    const int run = run_length(Bt, T, std::max(1, C / v), kBwdThreads);
     runs = std::max(runs, (size_t)Bt * ((T + run - 1) / run));
   }
   return sizeof(float) * runs * 5 * C;
 }
 
 hipError_t launch_conv(bool is_bf16, const ConvArgs& a, hipStream_t s) {
-  const int vec = vec_of(is_bf16, a.C, a.ldx, 0);
+  const int vec = vec_of(vec_fwd(is_bf16), a.C, a.ldx, 0);
   ConvArgs A = a;
-  A.run = run_length(A.Bt, A.T, A.C / vec);
-  return with_kernel(is_bf16, vec, A.W, [&](auto t, auto v, auto w) {
+  A.run = run_length(A.Bt, A.T, A.C / vec, kFwdThreads);
+  return with_kernel<8, 4>(is_bf16, vec, A.W, [&](auto t, auto v, auto w) {
     return launch("causal_conv", conv_kernel<decltype(t), v(), w()>,
                   blocks_of(runs_of(A) * (A.C / vec)), dim3(256), 0, s, A);
   });
 }
 
 hipError_t launch_conv_backward(bool is_bf16, const ConvArgs& a, hipStream_t s) {
-  const int vec = vec_of(is_bf16, a.C, a.ldx, a.lddx);
+  const int vec = vec_of(vec_bwd(is_bf16), a.C, a.ldx, a.lddx);
   ConvArgs A = a;
-  A.run = run_length(A.Bt, A.T, A.C / vec);
-  const hipError_t e = with_kernel(is_bf16, vec, A.W, [&](auto t, auto v, auto w) {
+  A.run = run_length(A.Bt, A.T, A.C / vec, kBwdThreads);
+  const hipError_t e = with_kernel<4, 2>(is_bf16, vec, A.W, [&](auto t, auto v, auto w) {
     return launch("causal_conv_bwd", conv_bwd_kernel<decltype(t), v(), w()>,
                   blocks_of(runs_of(A) * (A.C / vec)), dim3(256), 0, s, A);
   });
   if (e != hipSuccess) return e;
   const size_t cols = (size_t)(A.W + 1) * A.C;
-  return launch("causal_conv_sum", conv_sum_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(256),
+  return launch("causal_conv_sum", conv_sum_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(1024),
                 0, s, A, runs_of(A));
 }
 
@@ -383,8 +394,8 @@ hipError_t launch_conv_state(bool is_bf16, const void* from, void* to, size_t n,
 }
 
 hipError_t launch_conv_step(bool is_bf16, const ConvArgs& A, hipStream_t s) {
-  const int vec = vec_of(is_bf16, A.C, A.ldx, 0);
-  return with_kernel(is_bf16, vec, A.W, [&](auto t, auto v, auto w) {
+  const int vec = vec_of(vec_fwd(is_bf16), A.C, A.ldx, 0);
+  return with_kernel<8, 4>(is_bf16, vec, A.W, [&](auto t, auto v, auto w) {
     return launch("causal_conv_step", conv_step_kernel<decltype(t), v(), w()>,
                   blocks_of((size_t)A.Bt * (A.C / vec)), dim3(256), 0, s, A);
   });

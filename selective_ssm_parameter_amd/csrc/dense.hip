@@ -956,21 +956,25 @@ hipError_t launch_dense_tn(bool is_bf16, const char* name, int M, int R, int S, 
 namespace {
 
 // Each row's logarithm of the sum of exponentials from the tiles' statistics, and
-// its loss: 64 rows a workgroup, a quarter of the tiles each wave, joined in order.
+// its loss: a workgroup takes ROWS rows, each of its 256 / ROWS groups of threads a
+// run of the tiles, joined in order.
+template <int ROWS>
 __global__ __launch_bounds__(256) void xent_finish_kernel(XentArgs X, int M, int tiles,
                                                           float* loss, float* lse) {
-  __shared__ float2 part[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int row = blockIdx.x * 64 + lane;
-  const int per = (tiles + 3) / 4, t1 = min(tiles, (wave + 1) * per);
+  constexpr int GROUPS = 256 / ROWS;
+  __shared__ float2 part[GROUPS][ROWS];
+  const int r = threadIdx.x % ROWS, g = threadIdx.x / ROWS;
+  const int row = blockIdx.x * ROWS + r;
+  const int per = (tiles + GROUPS - 1) / GROUPS, t1 = min(tiles, (g + 1) * per);
   float2 v = make_float2(-INFINITY, 0.f);
-  if (row < M)
-    for (int t = wave * per; t < t1; ++t) v = xent_join(v, X.part[(size_t)t * M + row]);
-  part[wave][lane] = v;
+  if (row < M) {
+#pragma unroll 4
+    for (int t = g * per; t < t1; ++t) v = xent_join(v, X.part[(size_t)t * M + row]);
+  }
+  part[g][r] = v;
   __syncthreads();
-  if (wave || row >= M) return;
-#pragma unroll
-  for (int w = 1; w < 4; ++w) v = xent_join(v, part[w][lane]);
+  if (g || row >= M) return;
+  for (int w = 1; w < GROUPS; ++w) v = xent_join(v, part[w][r]);
   // a row of -inf alone: -inf
   const float l = v.x == -INFINITY && v.y == 0.f ? -INFINITY : v.x + logf(v.y);
   const int t = X.targets[row];
@@ -992,8 +996,13 @@ hipError_t xent_forward(int M, int D, int V, const void* x, const void* w, const
   const hipError_t e = go_rows<T, kXent>("cross_entropy", A, s);
   if (e != hipSuccess) return e;
   const int cols = xent_tile_cols(xent_tile(sizeof(T) == 2, M, V, D));
-  return launch("cross_entropy_finish", xent_finish_kernel, dim3((unsigned)((M + 63) / 64)),
-                dim3(256), 0, s, A.xe, M, (V + cols - 1) / cols, loss, lse);
+  const int tiles = (V + cols - 1) / cols;
+  // rows that share a line of 128 bytes, as long as that leaves workgroups enough
+  if (M >= 2048)
+    return launch("cross_entropy_finish", xent_finish_kernel<16>, dim3((unsigned)((M + 15) / 16)),
+                  dim3(256), 0, s, A.xe, M, tiles, loss, lse);
+  return launch("cross_entropy_finish", xent_finish_kernel<4>, dim3((unsigned)((M + 3) / 4)),
+                dim3(256), 0, s, A.xe, M, tiles, loss, lse);
 }
 
 }  // namespace
