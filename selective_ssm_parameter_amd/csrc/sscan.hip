@@ -55,14 +55,8 @@ __host__ __device__ inline int group_blocks(int Ch, int N, int G) {
 template <int CTRL> __device__ __forceinline__ float dpp(float v) {
   return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xF, 0xF, true));
 }
-// Lane q of each four, to all four, once: the vector units run DPP operands at half
-// the rate of registers, so the (empty) use keeps the move from being folded into
-// each of the multiplications that follow.
-template <int Q> __device__ __forceinline__ float quad(float v) {
-  float r = dpp<Q * 0x55>(v);
-  asm("" : "+v"(r));
-  return r;
-}
+// Lane q of each four, to all four.
+template <int Q> __device__ __forceinline__ float quad(float v) { return dpp<Q * 0x55>(v); }
 // The sum over the four lanes, in all of them.
 __device__ __forceinline__ float quad_sum(float v) {
   v += dpp<0xB1>(v);         // lane ^ 1
@@ -198,22 +192,32 @@ __device__ __forceinline__ uint32_t four_offset(const Place& p, uint32_t pitch, 
 template <typename T>
 __device__ __forceinline__ Four load_four(const void* t, int64_t ld, const SScanArgs& A,
                                           const Place& p, int blk) {
-  const int t0 = blk * kTok;
-  const BufRes r = rows_buffer<T>(t, (size_t)p.b * A.T + t0, ld, min(kTok, p.len - t0), A.Ch);
+  const int t0 = blk * kTok, rows = min(kTok, p.len - t0);
+  const BufRes r = rows_buffer<T>(t, (size_t)p.b * A.T + t0, ld, rows, A.Ch);
   const uint32_t pitch = (uint32_t)ld * sizeof(T), off = four_offset(p, pitch, sizeof(T));
   Four f;
+  if (rows == kTok) {  // no arithmetic per row
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f.v[i] = load_bits<T>(r, off + 4 * i * pitch, 0);
+    for (int i = 0; i < 4; ++i) f.v[i] = load_bits<T>(r, off, 4 * i * pitch);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.v[i] = load_bits<T>(r, off + 4 * i * pitch, 0);
+  }
   return f;
 }
 template <typename T>
 __device__ __forceinline__ void store_four(void* t, int64_t ld, const SScanArgs& A,
                                            const Place& p, int blk, const float (&v)[4]) {
-  const int t0 = blk * kTok;
-  const BufRes r = rows_buffer<T>(t, (size_t)p.b * A.T + t0, ld, min(kTok, A.T - t0), A.Ch);
+  const int t0 = blk * kTok, rows = min(kTok, A.T - t0);
+  const BufRes r = rows_buffer<T>(t, (size_t)p.b * A.T + t0, ld, rows, A.Ch);
   const uint32_t pitch = (uint32_t)ld * sizeof(T), off = four_offset(p, pitch, sizeof(T));
+  if (rows == kTok) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) store_one<T>(r, off + 4 * i * pitch, 0, v[i]);
+    for (int i = 0; i < 4; ++i) store_one<T>(r, off, 4 * i * pitch, v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) store_one<T>(r, off + 4 * i * pitch, 0, v[i]);
+  }
 }
 // The values of a block that reaches past the length: zeros there.
 __device__ __forceinline__ void clear_tail(const Place& p, int blk, float (&v)[4]) {
@@ -934,7 +938,7 @@ void segments(SScanArgs& A, int64_t want) {
   A.seg_blocks = (int)((nblk + s - 1) / s);
   A.segs = (nblk + A.seg_blocks - 1) / A.seg_blocks;
 }
-constexpr int64_t kWant = 2048, kWantBwd = 2048;
+constexpr int64_t kWant = 3072, kWantBwd = 3072;
 
 unsigned workgroups(const SScanArgs& A, int segs) {
   return (unsigned)((int64_t)A.Bt * segs * A.G * group_blocks(A.Ch, A.N, A.G));
