@@ -281,35 +281,43 @@ __device__ __forceinline__ void xent_stats(const DenseArgs& A,
   const int wm = wave / C::WN, wn = wave % C::WN;
   float2* part = reinterpret_cast<float2*>(lds);  // [WN][BM]
   __syncthreads();                                // the stage is no longer read
+  // (the largest and the sum by themselves, without a test of each column where all exist)
+  auto rows = [&](auto whole) {
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int r = wm * TM * 16 + 16 * i + c;
-    const bool on = r0 + r < A.R;
-    const int hit = on ? A.xe.targets[r0 + r] - A.xe.v0 : -1;
-    float m = -INFINITY, sum = 0.f;
+    for (int i = 0; i < TM; ++i) {
+      const int r = wm * TM * 16 + 16 * i + c;
+      const int hit = r0 + r < A.R ? A.xe.targets[r0 + r] - A.xe.v0 : -1;
+      float m = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
+      for (int jj = 0; jj < TN / 2; ++jj) {
+        const int col = s0 + (wn * (TN / 2) + jj) * 32 + 8 * g;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = s0 + wn * TN * 16 + 32 * (j >> 1) + 8 * g + 4 * (j & 1) + q;
-        if (col < A.S) {
-          m = fmaxf(m, acc[i][j][q]);
-          if (on && col == hit) A.xe.zt[r0 + r] = acc[i][j][q];
+        for (int q = 0; q < 8; ++q)
+          if (whole || col + q < A.S) m = fmaxf(m, acc[i][2 * jj + (q >> 2)][q & 3]);
+        if (hit >= col && hit < min(col + 8, A.S)) {
+          float z = 0.f;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) z = hit == col + q ? acc[i][2 * jj + (q >> 2)][q & 3] : z;
+          A.xe.zt[r0 + r] = z;
         }
       }
-    m = over_groups(m, [](float a, float b) { return fmaxf(a, b); });
-    const float base = m == -INFINITY ? 0.f : m;
+      m = over_groups(m, [](float a, float b) { return fmaxf(a, b); });
+      const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
+      for (int jj = 0; jj < TN / 2; ++jj) {
+        const int col = s0 + (wn * (TN / 2) + jj) * 32 + 8 * g;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = s0 + wn * TN * 16 + 32 * (j >> 1) + 8 * g + 4 * (j & 1) + q;
-        const float e = __builtin_amdgcn_exp2f((acc[i][j][q] - base) * kLog2e);
-        sum += col < A.S ? e : 0.f;
+        for (int q = 0; q < 8; ++q) {
+          const float e = __builtin_amdgcn_exp2f((acc[i][2 * jj + (q >> 2)][q & 3] - base) * kLog2e);
+          sum += whole || col + q < A.S ? e : 0.f;
+        }
       }
-    sum = over_groups(sum, [](float a, float b) { return a + b; });
-    if (g == 0) part[wn * C::BM + r] = make_float2(m, sum);
-  }
+      sum = over_groups(sum, [](float a, float b) { return a + b; });
+      if (g == 0) part[wn * C::BM + r] = make_float2(m, sum);
+    }
+  };
+  if (s0 + C::BN <= A.S) rows(std::true_type());
+  else rows(std::false_type());
   __syncthreads();
   for (int r = threadIdx.x; r < C::BM; r += C::NTH) {
     if (r0 + r >= A.R) break;
@@ -330,14 +338,22 @@ __device__ __forceinline__ void xent_dz(const DenseArgs& A, const floatx4 (&acc)
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
   const int ld = (A.S + 7) / 8 * 8;
+  // what a row needs, all requested before the first use
+  int target[TM];
+  float lse[TM], dl[TM];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int row = min(r0 + wm * TM * 16 + 16 * i + c, A.R - 1);
+    target[i] = A.xe.targets[row];
+    lse[i] = A.xe.lse[row];
+    dl[i] = A.xe.dloss[row];
+  }
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int row = r0 + wm * TM * 16 + 16 * i + c;
     if (row >= A.R) continue;
-    const int t = A.xe.targets[row];
-    const bool counts = t >= 0 && t < A.xe.V;
-    const float lse = A.xe.lse[row], dl = counts ? A.xe.dloss[row] : 0.f;
-    const int hit = counts ? t - A.xe.v0 : -1;
+    const bool counts = target[i] >= 0 && target[i] < A.xe.V;
+    const int hit = counts ? target[i] - A.xe.v0 : -1;
 #pragma unroll
     for (int jj = 0; jj < TN / 2; ++jj) {
       const int col = s0 + (wn * (TN / 2) + jj) * 32 + 8 * g;
@@ -346,8 +362,17 @@ __device__ __forceinline__ void xent_dz(const DenseArgs& A, const floatx4 (&acc)
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const float z = acc[i][2 * jj + (q >> 2)][q & 3];
-        const float p = __builtin_amdgcn_exp2f((z - lse) * kLog2e);
-        d[q] = counts && col + q < A.S ? (p - (col + q == hit ? 1.f : 0.f)) * dl : 0.f;
+        d[q] = __builtin_amdgcn_exp2f((z - lse[i]) * kLog2e);
+      }
+      if (hit >= col && hit < col + 8) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) d[q] -= hit == col + q ? 1.f : 0.f;
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) d[q] = counts ? d[q] * dl[i] : 0.f;
+      if (col + 8 > A.S) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) d[q] = col + q < A.S ? d[q] : 0.f;
       }
       T* hi = static_cast<T*>(A.out) + (size_t)row * ld + col;
       const typename Vec<T>::x8 h = convert8<T, float>(d);
