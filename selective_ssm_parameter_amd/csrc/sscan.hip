@@ -872,60 +872,81 @@ __global__ __launch_bounds__(256) void sscan_sum_kernel(SScanArgs A, unsigned fi
 
 // ---------------------------------------------------------------- one token
 
-// Four lanes a channel, four states a lane at a time.
-template <typename T>
+// Four lanes a channel, four states a lane at a time; R sequences a thread, whose
+// states are requested together and which share A, D and dt_bias.
+template <typename T, int R>
 __global__ __launch_bounds__(256) void sscan_step_kernel(SScanArgs A) {
   const size_t q = ((size_t)blockIdx.x * 256 + threadIdx.x) >> 2;
   const int j = threadIdx.x & 3;
-  const size_t b = q / A.Ch;
-  if (b >= (size_t)A.Bt) return;  // (the four lanes together)
-  const int c = (int)(q - b * A.Ch), g = c / (A.Ch / A.G);
-  const float x = to_f32(static_cast<const T*>(A.x)[b * A.ldx + c]);
-  float dt = to_f32(static_cast<const T*>(A.dt)[b * A.lddt + c]);
-  if (A.bias) dt += A.bias[c];
-  const T* Bp = static_cast<const T*>(A.B) + b * A.ldbc + (size_t)g * A.N;
-  const T* Cp = static_cast<const T*>(A.C) + b * A.ldbc + (size_t)g * A.N;
-  const float* hp = A.h_prev + q * A.N;
-  const float* Ap = A.A + (size_t)c * A.N;
-  float* ho = A.h + q * A.N;
-  float sig;
-  const float delta = softplus(dt, sig), u = delta * x;
-  float s = 0.f;
+  const size_t bq = q / A.Ch;
+  const int b0 = (int)bq * R;
+  if (bq * R >= (size_t)A.Bt) return;  // (the four lanes together)
+  const int c = (int)(q - bq * A.Ch), g = c / (A.Ch / A.G);
   const bool vec = vec_bc<T>(A);
+  const float* Ap = A.A + (size_t)c * A.N;
+  const float bias = A.bias ? A.bias[c] : 0.f, D = A.D ? A.D[c] : 0.f;
+  // (past the last sequence: its values again, not stored)
+  size_t b[R];
+  float x[R], dt[R], z[R], s[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    b[r] = min(b0 + r, A.Bt - 1);
+    x[r] = to_f32(static_cast<const T*>(A.x)[b[r] * A.ldx + c]);
+    dt[r] = to_f32(static_cast<const T*>(A.dt)[b[r] * A.lddt + c]);
+    z[r] = A.z ? to_f32(static_cast<const T*>(A.z)[b[r] * A.ldz + c]) : 0.f;
+    s[r] = 0.f;
+  }
   for (int n0 = 4 * j; n0 < A.N; n0 += kStates) {
-    floatx4 h = load_states(hp, n0, A.N, true);
+    floatx4 h[R];
+    float Bv[R][4], Cv[R][4];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      h[r] = load_states(A.h_prev + (b[r] * A.Ch + c) * A.N, n0, A.N, true);
+      const T* Bp = static_cast<const T*>(A.B) + b[r] * A.ldbc + (size_t)g * A.N;
+      const T* Cp = static_cast<const T*>(A.C) + b[r] * A.ldbc + (size_t)g * A.N;
+      if (vec) {
+        typedef typename Vec<T>::x4 V4;
+        const V4 bv = *reinterpret_cast<const V4*>(Bp + n0),
+                 cv = *reinterpret_cast<const V4*>(Cp + n0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          Bv[r][k] = to_f32(bv[k]);
+          Cv[r][k] = to_f32(cv[k]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          Bv[r][k] = n0 + k < A.N ? to_f32(Bp[n0 + k]) : 0.f;
+          Cv[r][k] = n0 + k < A.N ? to_f32(Cp[n0 + k]) : 0.f;
+        }
+      }
+    }
     const floatx4 Av = load_states(Ap, n0, A.N, true) * kLog2e;
-    float Bv[4], Cv[4];
-    if (vec) {
-      typedef typename Vec<T>::x4 V4;
-      const V4 bv = *reinterpret_cast<const V4*>(Bp + n0), cv = *reinterpret_cast<const V4*>(Cp + n0);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float sig;
+      const float delta = softplus(dt[r] + bias, sig), u = delta * x[r];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        Bv[k] = to_f32(bv[k]);
-        Cv[k] = to_f32(cv[k]);
+        h[r][k] = __builtin_fmaf(exp2_(delta * Av[k]), h[r][k], u * Bv[r][k]);
+        s[r] = __builtin_fmaf(Cv[r][k], h[r][k], s[r]);
       }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        Bv[k] = n0 + k < A.N ? to_f32(Bp[n0 + k]) : 0.f;
-        Cv[k] = n0 + k < A.N ? to_f32(Cp[n0 + k]) : 0.f;
-      }
+      float* to = A.h + (b[r] * A.Ch + c) * A.N;
+      if (b0 + r >= A.Bt) continue;
+      // past the L2's reuse order where a wave's channels are one run of whole lines (a
+      // hint; 256 x 4096 x 16: 35 -> 25.5 us)
+      if (A.N <= kStates && A.N % 4 == 0)
+        __builtin_nontemporal_store(h[r], reinterpret_cast<floatx4*>(to + n0));
+      else
+        store_states(to, n0, A.N, h[r]);
     }
+  }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      h[k] = __builtin_fmaf(exp2_(delta * Av[k]), h[k], u * Bv[k]);
-      s = __builtin_fmaf(Cv[k], h[k], s);
-    }
-    store_states(ho, n0, A.N, h);
+  for (int r = 0; r < R; ++r) {
+    s[r] = __builtin_fmaf(D, x[r], quad_sum(s[r]));
+    if (A.z) s[r] *= z[r] * sigm(z[r]);
+    if (j == 0 && b0 + r < A.Bt) static_cast<T*>(A.y)[b[r] * A.Ch + c] = from_f32<T>(s[r]);
   }
-  s = quad_sum(s);
-  if (j) return;
-  if (A.D) s = __builtin_fmaf(A.D[c], x, s);
-  if (A.z) {
-    const float z = to_f32(static_cast<const T*>(A.z)[b * A.ldz + c]);
-    s *= z * sigm(z);
-  }
-  static_cast<T*>(A.y)[q] = from_f32<T>(s);
 }
 
 // ---------------------------------------------------------------- launch
@@ -1031,9 +1052,17 @@ hipError_t launch_sscan_backward(bool is_bf16, const SScanArgs& a, hipStream_t s
 }
 
 hipError_t launch_sscan_step(bool is_bf16, const SScanArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(((size_t)a.Bt * a.Ch * 4 + 255) / 256));
-  return is_bf16 ? launch("selective_step", sscan_step_kernel<bf16>, grid, dim3(256), 0, s, a)
-                 : launch("selective_step", sscan_step_kernel<float>, grid, dim3(256), 0, s, a);
+  auto run = [&](auto t, auto r) {
+    const size_t rows = (a.Bt + r() - 1) / r();
+    return launch("selective_step", sscan_step_kernel<decltype(t), r()>,
+                  dim3((unsigned)((rows * a.Ch * 4 + 255) / 256)), dim3(256), 0, s, a);
+  };
+  // two sequences a thread where that leaves threads enough to fill the card (256 x 4096
+  // x 16: 34 us; one: 39, four: 38, eight: 56)
+  const std::integral_constant<int, 2> two{};
+  const std::integral_constant<int, 1> one{};
+  if ((int64_t)a.Bt * a.Ch >= (int64_t)1 << 18) return is_bf16 ? run(bf16(), two) : run(0.f, two);
+  return is_bf16 ? run(bf16(), one) : run(0.f, one);
 }
 
 }  // namespace swimba
