@@ -23,6 +23,7 @@
 // the states and decays of 16 tokens in registers from it, with one exponential
 // each.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "common.hpp"
@@ -951,11 +952,16 @@ __global__ __launch_bounds__(256) void sscan_step_kernel(SScanArgs A) {
 
 // ---------------------------------------------------------------- launch
 
-// Segments per sequence, so that some `want` workgroups run.
+// Segments per sequence, so that some `want` workgroups run; at most kSegRoot
+// sqrt(blocks): where so few workgroups run that each one's time is that of its own
+// instructions, a block takes some 2 to 3 us and the join some 0.15 us a segment, and
+// the sum of both is least about there.
+constexpr double kSegRoot = 4;
 void segments(SScanArgs& A, int64_t want) {
   const int64_t wg = (int64_t)A.Bt * A.G * group_blocks(A.Ch, A.N, A.G);
   const int nblk = (A.T + kTok - 1) / kTok;
-  int64_t s = std::max<int64_t>(1, std::min<int64_t>((want + wg - 1) / wg, nblk / 4));
+  const int64_t most = (int64_t)(kSegRoot * std::sqrt((double)nblk));
+  int64_t s = std::max<int64_t>(1, std::min({(want + wg - 1) / wg, most, (int64_t)nblk}));
   A.seg_blocks = (int)((nblk + s - 1) / s);
   A.segs = (nblk + A.seg_blocks - 1) / A.seg_blocks;
 }
@@ -1040,7 +1046,7 @@ int64_t sscan_threads(int64_t Bt, int64_t T, int64_t Ch, int64_t N, int64_t G) {
   const int64_t wg = Bt * G * group_blocks((int)Ch, (int)N, (int)G);
   const int64_t threads = 64 * (int64_t)channel_waves((int)N) * state_blocks((int)N);
   const int64_t scan = (wg + std::max(kWant, kWantBwd)) * threads;
-  return std::max({scan, Bt * T * 2 * G * N + Ch * (N + 2) + 1024, Bt * Ch * 4});
+  return std::max({scan, Bt * T * 2 * G * N + 4 * Ch * (N + 2) + 1024, Bt * Ch * 4});
 }
 
 hipError_t launch_sscan(bool is_bf16, const SScanArgs& a, hipStream_t s) {

@@ -520,6 +520,40 @@ def test_cross_entropy_special_values(dtype):
     assert not dx.any() and not dw.any()
 
 
+def test_cross_entropy_of_weights_past_2_gib():
+    """The backward's pieces are cut where a buffer would not reach: dx of a few tokens
+    against float64, dw where the targets are."""
+    M, D, V = 9, 8192, 140000
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    x, w = r(M, D).bfloat16(), torch.empty(V, D, device="cuda", dtype=torch.bfloat16)
+    for v in range(0, V, 10000):
+        w[v:v + 10000] = (r(10000, D) * 2 * D ** -0.5).bfloat16()
+    t = torch.tensor([0, 5, 130815, 130816, 131071, 131072, V - 1, -1, V], device="cuda",
+                     dtype=torch.int32)
+    d, g = ssm.loss_dims(M, D, V, "bf16"), torch.ones(M, device="cuda")
+    loss, lse, dx, dw = empty(M), empty(M), empty(M, D), empty(V, D)
+    ssm.swimba_cross_entropy(d, x, w, t, loss, lse, ssm.ssm_workspace(d, ssm.CROSS_ENTROPY))
+    ssm.swimba_cross_entropy_backward(d, x, w, t, lse, g, dx, dw,
+                                      ssm.ssm_workspace(d, ssm.CROSS_ENTROPY_BACKWARD))
+    f64 = torch.float64
+    xd = x.to(f64)
+    z = torch.cat([xd @ w[v:v + 10000].to(f64).t() for v in range(0, V, 10000)], 1)
+    wl = torch.logsumexp(z, 1)
+    # a logit is off by at most D U sum |x w| < D U 8192 * 2 / sqrt(8192); on average far less
+    assert (lse.to(f64) - wl).abs().max() < 2e-4
+    dz = torch.exp(z - wl[:, None])
+    ok = [i for i in range(M) if 0 <= int(t[i]) < V]
+    dz[torch.tensor(ok, device="cuda"), t[ok].long()] -= 1
+    dz[[i for i in range(M) if i not in ok]] = 0
+    want = sum(dz[:, v:v + 10000] @ w[v:v + 10000].to(f64) for v in range(0, V, 10000))
+    # dz to 2^-16 and the logits' error, sums of V terms of random sign
+    assert (dx.to(f64) - want).norm() < 1e-4 * want.norm()
+    rows = t[ok].long()
+    assert (dw[rows].to(f64) - dz.t()[rows] @ xd).norm() < 1e-4 * (dz.t()[rows] @ xd).norm()
+    assert torch.isfinite(dw[::1000]).all()
+
+
 def test_cross_entropy_without_tokens():
     d = ssm.loss_dims(0, 16, 40, "f32")
     w, dw, e = torch.ones(40, 16, device="cuda"), empty(40, 16), torch.empty(0, device="cuda")

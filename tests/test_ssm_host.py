@@ -180,6 +180,9 @@ def test_loss_refusals():
     for call in (loss, loss_b):
         assert call(ldims(d=100)) == -3 and "multiple of 8" in err()
         assert call(ldims(tokens=1 << 24, v=1 << 20, d=8)) == -2
+        assert call(ldims(tokens=1 << 28, v=8, d=8)) == -2
+        # 2^16 tokens over 2^18 words are within a launch
+        assert call(ldims(tokens=1 << 16, v=1 << 18, d=8), ws=None, nb=0) == -4
         assert call(ldims(d=(1 << 20) + 8, v=8)) == -2
     for c, call in ((ssm.CROSS_ENTROPY, loss), (ssm.CROSS_ENTROPY_BACKWARD, loss_b)):
         need = ssm.ssm_workspace_size(d, c)
