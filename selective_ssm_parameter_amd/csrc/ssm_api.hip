@@ -70,12 +70,14 @@ swimba_status check_loss(const Dims& d) {
 // The backward's pieces of the vocabulary: dz of one (two bf16 numbers or one
 // float32 an element) takes some 512 MB at most, in whole tiles (256 MB: 2 % slower,
 // 1 GB: 1.5 % faster at 16384 x 768 over 32768 words). Each piece but the first reads
-// and writes dx once more, so they are as large as that allows. A piece's weights are
-// read through one buffer.
+// and writes dx once more, so they are as few as that allows, and then equally large.
+// A piece's weights are read through one buffer.
 int64_t xent_piece(const Dims& d) {
   const int64_t cols = (int64_t(1) << 27) / std::max<int64_t>(1, d.M) / 256 * 256;
   const int64_t rows = kMaxRecord / (d.D * (d.bf16 ? 2 : 4)) / 256 * 256;
-  return std::min({d.HP, rows, std::max<int64_t>(1024, cols)});
+  const int64_t most = std::min({d.HP, rows, std::max<int64_t>(1024, cols)});
+  const int64_t pieces = (d.HP + most - 1) / most;
+  return std::min(most, ((d.HP + pieces - 1) / pieces + 255) / 256 * 256);
 }
 int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
 

@@ -445,7 +445,10 @@ def test_cross_entropy(M, D, V, dtype):
 
 
 @pytest.mark.parametrize("dtype,M,D,V", [("bf16", 16500, 16, 9001), ("f32", 12000, 8, 11003),
-                                         ("bf16", 4100, 384, 8200), ("f32", 4100, 64, 4096)])
+                                         ("bf16", 4100, 384, 8200), ("f32", 4100, 64, 4096),
+                                         ("bf16", 8200, 1032, 20003), ("bf16", 16400, 768, 9001),
+                                         ("bf16", 700, 1032, 20003), ("bf16", 700, 768, 9001),
+                                         ("f32", 16400, 64, 20003)])
 def test_cross_entropy_of_several_pieces_and_large_tiles(dtype, M, D, V):
     """Against float64 on the GPU, with the same bounds."""
     d, x, w, t, g = loss_case(M, D, V, dtype, seed=V)
