@@ -181,78 +181,109 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs A) {
   for (int k = 0; k < W; ++k)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) dw[k][j] = ds[k][j] = db[j] = 0.f;
-  auto gradient = [&](int t) {
-    return t < r.len ? load_raw<T, VEC>(dy + (size_t)t * A.C) : zero_raw<T, VEC>();
-  };
-  // the outputs of the run are complete W - 1 tokens behind its end
-  const int end = t1 + W - 1;
+  // tokens of the run in use; its outputs are complete W - 1 tokens behind their end
+  const int live = max(min(t1, r.len), r.t0), end = live + W - 1, last = min(r.len, end);
+  const T* x = static_cast<const T*>(A.x) + (size_t)r.b * A.T * A.ldx + r.c;
   Vt<T, VEC> nx[kStepBwd], nd[kStepBwd];
+  auto fetch = [&](int t) {
+    if (t + kStepBwd <= last) {
 #pragma unroll
-  for (int i = 0; i < kStepBwd; ++i) {
-    nx[i] = input_at<T, VEC, W>(A, r.b, r.c, r.t0 + i, min(r.len, end));
-    nd[i] = r.t0 + i < end ? gradient(r.t0 + i) : zero_raw<T, VEC>();
-  }
+      for (int i = 0; i < kStepBwd; ++i) {
+        nx[i] = load_raw<T, VEC>(x + (size_t)(t + i) * A.ldx);
+        nd[i] = load_raw<T, VEC>(dy + (size_t)(t + i) * A.C);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kStepBwd; ++i) {
+        nx[i] = nd[i] = zero_raw<T, VEC>();
+        if (t + i < last) {
+          nx[i] = load_raw<T, VEC>(x + (size_t)(t + i) * A.ldx);
+          nd[i] = load_raw<T, VEC>(dy + (size_t)(t + i) * A.C);
+        }
+      }
+    }
+  };
+  fetch(r.t0);
 #pragma unroll
   for (int k = 1; k < W; ++k) {
     const Vt<T, VEC> v = input_at<T, VEC, W>(A, r.b, r.c, r.t0 - W + k, r.len);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) win[k][j] = to_f32(v[j]);
   }
-  for (int t = r.t0; t < end; t += kStepBwd) {
-    Vt<T, VEC> cx[kStepBwd], cd[kStepBwd];
+  // One token: INNER where it and the output that it completes lie within the run and
+  // before the inputs that the state behind the sequence holds.
+  auto token = [&](int tt, const Vt<T, VEC>& xv, const Vt<T, VEC>& dv, auto inner) {
+    constexpr bool INNER = decltype(inner)::value;
+    const int out = tt - (W - 1);  // ds of tt completes the gradient of input out
+    const bool in = INNER || tt < r.len, mine = INNER || (tt < t1 && tt < r.len);
+    float g[VEC];
 #pragma unroll
-    for (int i = 0; i < kStepBwd; ++i) {
-      const int tn = t + kStepBwd + i;
-      cx[i] = nx[i];
-      cd[i] = nd[i];
-      nx[i] = input_at<T, VEC, W>(A, r.b, r.c, tn, min(r.len, end));
-      nd[i] = tn < end ? gradient(tn) : zero_raw<T, VEC>();
+    for (int j = 0; j < VEC; ++j) {
+#pragma unroll
+      for (int k = 0; k + 1 < W; ++k) {
+        win[k][j] = win[k + 1][j];
+        ds[k][j] = ds[k + 1][j];
+      }
+      win[W - 1][j] = to_f32(xv[j]);
+      float s = bias[j];
+#pragma unroll
+      for (int k = 0; k < W; ++k) s = __builtin_fmaf(w[k][j], win[k][j], s);
+      float d = to_f32(dv[j]);
+      if (A.silu) {
+        const float sg = sigm(s);
+        d *= sg * __builtin_fmaf(s, 1.f - sg, 1.f);
+      }
+      if constexpr (!INNER) d = in ? d : 0.f;
+      ds[W - 1][j] = d;
+      if (mine) {
+        db[j] += d;
+#pragma unroll
+        for (int k = 0; k < W; ++k) dw[k][j] = __builtin_fmaf(d, win[k][j], dw[k][j]);
+      }
+      g[j] = w[0][j] * ds[W - 1][j];
+#pragma unroll
+      for (int k = 1; k < W; ++k) g[j] = __builtin_fmaf(w[k][j], ds[W - 1 - k][j], g[j]);
     }
+    if constexpr (INNER) {
+      store_raw<T, VEC, NT>(dx + (size_t)out * A.lddx, g);
+      return;
+    }
+    // the state behind the last token holds inputs len - W + 1 .. len - 1
+    const int js = out - (r.len - (W - 1));
+    if (A.dstate_out && js >= 0 && js < W - 1 && tt < end) {
+      const float* p = A.dstate_out + ((size_t)r.b * (W - 1) + js) * A.C + r.c;
 #pragma unroll
-    for (int i = 0; i < kStepBwd; ++i) {
-      const int tt = t + i, out = tt - (W - 1);  // ds of tt completes the gradient of input out
-      const bool mine = tt < t1 && tt < r.len;
-      float g[VEC];
+      for (int j = 0; j < VEC; ++j) g[j] += p[j];
+    }
+    if (out >= r.t0 && out < live) {
+      store_raw<T, VEC, NT>(dx + (size_t)out * A.lddx, g);
+    } else if (r.t0 == 0 && out < 0 && A.dstate_in) {
+      store_f32<VEC>(A.dstate_in + ((size_t)r.b * (W - 1) + tt) * A.C + r.c, g);
+    }
+  };
+  // (a run past the length has nothing but zeros to write, the first its state besides)
+  if (live > r.t0 || r.t0 == 0) {
+    for (int t = r.t0; t < end; t += kStepBwd) {
+      Vt<T, VEC> cx[kStepBwd], cd[kStepBwd];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-#pragma unroll
-        for (int k = 0; k + 1 < W; ++k) {
-          win[k][j] = win[k + 1][j];
-          ds[k][j] = ds[k + 1][j];
-        }
-        win[W - 1][j] = to_f32(cx[i][j]);
-        float s = bias[j];
-#pragma unroll
-        for (int k = 0; k < W; ++k) s = __builtin_fmaf(w[k][j], win[k][j], s);
-        float d = to_f32(cd[i][j]);
-        if (A.silu) {
-          const float sg = sigm(s);
-          d *= sg * __builtin_fmaf(s, 1.f - sg, 1.f);
-        }
-        ds[W - 1][j] = d = tt < r.len ? d : 0.f;
-        if (mine) {
-          db[j] += d;
-#pragma unroll
-          for (int k = 0; k < W; ++k) dw[k][j] = __builtin_fmaf(d, win[k][j], dw[k][j]);
-        }
-        g[j] = 0.f;
-#pragma unroll
-        for (int k = 0; k < W; ++k) g[j] = __builtin_fmaf(w[k][j], ds[W - 1 - k][j], g[j]);
+      for (int i = 0; i < kStepBwd; ++i) {
+        cx[i] = nx[i];
+        cd[i] = nd[i];
       }
-      // the state behind the last token holds inputs len - W + 1 .. len - 1
-      const int js = out - (r.len - (W - 1));
-      if (A.dstate_out && js >= 0 && js < W - 1 && tt < end) {
-        const float* p = A.dstate_out + ((size_t)r.b * (W - 1) + js) * A.C + r.c;
+      fetch(t + kStepBwd);
+      if (t >= r.t0 + W - 1 && t + kStepBwd <= live) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) g[j] += p[j];
-      }
-      if (out >= r.t0 && out < t1) {
-        store_raw<T, VEC, NT>(dx + (size_t)out * A.lddx, g);  // (zeros past the length)
-      } else if (r.t0 == 0 && out < 0 && A.dstate_in) {
-        store_f32<VEC>(A.dstate_in + ((size_t)r.b * (W - 1) + tt) * A.C + r.c, g);
+        for (int i = 0; i < kStepBwd; ++i) token(t + i, cx[i], cd[i], std::true_type());
+      } else {
+#pragma unroll
+        for (int i = 0; i < kStepBwd; ++i) token(t + i, cx[i], cd[i], std::false_type());
       }
     }
   }
+  float zeros[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) zeros[j] = 0.f;
+  for (int t = live; t < t1; ++t) store_raw<T, VEC, NT>(dx + (size_t)t * A.lddx, zeros);
   float* part = A.part + r.index * (W + 1) * A.C + r.c;
 #pragma unroll
   for (int k = 0; k < W; ++k) store_f32<VEC>(part + (size_t)k * A.C, dw[k]);
