@@ -38,8 +38,8 @@ __device__ __forceinline__ Vt<T, VEC> load_raw(const T* p) {
   return *reinterpret_cast<const Vt<T, VEC>*>(p);
 }
 // NT: past the L2's reuse order, where rows start on 128-byte lines (nothing here
-// reads them again; a hint only): 8 x 2048 x 1536 forward 19.5 -> 16.4 us, backward
-// 41 -> 38. (As a test at each store it gained nothing.)
+// reads them again; a hint only): 8 x 2048 x 1536 forward 19.5 -> 16.7 us, backward
+// 41 -> 38 when it was measured. (As a test at each store it gained nothing.)
 template <typename T, int VEC, bool NT = false>
 __device__ __forceinline__ void store_raw(T* p, const float* v) {
   Vt<T, VEC> r;
@@ -349,8 +349,8 @@ __global__ __launch_bounds__(256) void conv_state_kernel(const T* from, T* to, s
 
 // Tokens per thread: long runs read few rows twice and leave few partial sums, as
 // long as enough threads remain to fill the card, some 2^18 forward (8 x 2048 x
-// 1536: 20 us; 2^17: 23, 2^19: 22) and, for the partial sums, 2^17 backward (41 us;
-// 2^16: 57, 2^18: 43, 2^19: 50).
+// 1536: 20 us; 2^17: 23, 2^19: 22) and, for the partial sums, 2^17 backward (36 us with
+// their addition; 2^16: 43, 2^18: 34 but slower in float32, 2^19: 51).
 constexpr int kFwdThreads = 18, kBwdThreads = 17;
 int run_length(int64_t Bt, int64_t T, int64_t vecs, int threads) {
   const int64_t r = Bt * T * vecs >> threads;
@@ -361,7 +361,8 @@ int vec_of(int v, int C, int64_t ldx, int64_t lddx) {
   return C % v == 0 && ldx % v == 0 && lddx % v == 0 ? v : 1;
 }
 // 16 bytes of them forward; 8 in the backward, whose registers then leave room for
-// four waves instead of one (padded 8 x 2048 x 1536: 78 -> 40 us; 4 bytes: 54).
+// three waves instead of one (padded 8 x 2048 x 1536: 78 -> 40 us when it was measured;
+// 4 bytes: 54, now 32 against 31).
 int vec_fwd(bool is_bf16) { return is_bf16 ? 8 : 4; }
 int vec_bwd(bool is_bf16) { return is_bf16 ? 4 : 2; }
 
