@@ -952,20 +952,24 @@ __global__ __launch_bounds__(256) void sscan_step_kernel(SScanArgs A) {
 
 // ---------------------------------------------------------------- launch
 
-// Segments per sequence, so that some `want` workgroups run; at most kSegRoot
+// Segments per sequence, so that some kWant workgroups run (twelve a CU: fewer leave
+// CUs idle at the end, more join more segments;
+// at 8, 12, 16 a CU 65536 x 2048 forward takes 980, 975, 987 us, a padded 8 x 2048 x
+// 1536 training step 486, 471, 479, an unpadded one 717, 692, 709); at most kSegRoot
 // sqrt(blocks): where so few workgroups run that each one's time is that of its own
 // instructions, a block takes some 2 to 3 us and the join some 0.15 us a segment, and
-// the sum of both is least about there.
+// the sum of both is least about there (a 2 x 777 x 402 fp32 training step: 59 us,
+// 70 without this limit).
+constexpr int64_t kWant = 12 * 256;
 constexpr double kSegRoot = 4;
-void segments(SScanArgs& A, int64_t want) {
+void segments(SScanArgs& A) {
   const int64_t wg = (int64_t)A.Bt * A.G * group_blocks(A.Ch, A.N, A.G);
   const int nblk = (A.T + kTok - 1) / kTok;
   const int64_t most = (int64_t)(kSegRoot * std::sqrt((double)nblk));
-  int64_t s = std::max<int64_t>(1, std::min({(want + wg - 1) / wg, most, (int64_t)nblk}));
+  int64_t s = std::max<int64_t>(1, std::min({(kWant + wg - 1) / wg, most, (int64_t)nblk}));
   A.seg_blocks = (int)((nblk + s - 1) / s);
   A.segs = (nblk + A.seg_blocks - 1) / A.seg_blocks;
 }
-constexpr int64_t kWant = 3072, kWantBwd = 3072;
 
 unsigned workgroups(const SScanArgs& A, int segs) {
   return (unsigned)((int64_t)A.Bt * segs * A.G * group_blocks(A.Ch, A.N, A.G));
@@ -984,7 +988,7 @@ template <class F> hipError_t by_flag(bool f, F run) {
 
 template <typename T>
 hipError_t forward(SScanArgs A, hipStream_t s) {
-  segments(A, kWant);
+  segments(A);
   if (A.segs > 1) {
     const hipError_t e = launch("selective_scan_ends", sscan_ends_kernel<T>,
                                 dim3(workgroups(A, A.segs - 1)), dim3(threads_of(A)), 0, s, A);
@@ -1000,7 +1004,7 @@ hipError_t forward(SScanArgs A, hipStream_t s) {
 
 template <typename T>
 hipError_t backward(SScanArgs A, hipStream_t s) {
-  segments(A, kWantBwd);
+  segments(A);
   hipError_t e;
   if (A.segs > 1) {
     e = by_flag(A.z, [&](auto gated) {
@@ -1031,21 +1035,21 @@ size_t sscan_carry_bytes(int Bt, int T, int Ch, int N) {
 
 size_t sscan_ws_bytes(int Bt, int T, int Ch, int N, int G) {
   SScanArgs A = sizes(Bt, T, Ch, N, G);
-  segments(A, kWant);
+  segments(A);
   if (A.segs <= 1) return 0;
   return sizeof(float) * (size_t)Bt * A.segs * Ch * (state_blocks(N) * kStates + 1);
 }
 
 size_t sscan_bwd_ws_bytes(int Bt, int T, int Ch, int N, int G) {
   SScanArgs A = sizes(Bt, T, Ch, N, G);
-  segments(A, kWantBwd);
+  segments(A);
   return sizeof(float) * BwdBoard(A).floats(A);
 }
 
 int64_t sscan_threads(int64_t Bt, int64_t T, int64_t Ch, int64_t N, int64_t G) {
   const int64_t wg = Bt * G * group_blocks((int)Ch, (int)N, (int)G);
   const int64_t threads = 64 * (int64_t)channel_waves((int)N) * state_blocks((int)N);
-  const int64_t scan = (wg + std::max(kWant, kWantBwd)) * threads;
+  const int64_t scan = (wg + kWant) * threads;
   return std::max({scan, Bt * T * 2 * G * N + 4 * Ch * (N + 2) + 1024, Bt * Ch * 4});
 }
 
