@@ -194,7 +194,7 @@ swimba_status swimba_selective_step(const swimba_dims* dims, const void* x, int6
  * Softmax cross entropy of each token over a vocabulary, without the logits:
  *   z = x w^T (float32),   lse = log sum_v exp(z_v),   loss = lse - z[target].
  * A target outside [0, V) is no target: its loss is 0 and it gives no
- * gradient (its lse is that of the token). An infinite or NaN logit makes its
+ * gradient, whatever its row of x holds (its lse is that of the token). An infinite or NaN logit makes its
  * token's lse infinite or NaN.
  *   x         [M, D] dtype;  w [V, D] dtype
  *   targets   [M] int32

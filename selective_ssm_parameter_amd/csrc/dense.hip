@@ -1013,6 +1013,20 @@ __global__ __launch_bounds__(256) void xent_finish_kernel(XentArgs X, int M, int
   loss[row] = t >= 0 && t < X.V ? l - X.zt[row] : 0.f;
 }
 
+// x with zeros in the rows of tokens without a target (which may hold NaN), for the
+// product of dw: a wave per row of `per` vectors of 16 bytes
+// (16384 x 768 bf16: 8.5 us of 4800 of a training step).
+__global__ __launch_bounds__(256) void xent_rows_kernel(const uint4* x, const int32_t* targets,
+                                                        int V, int per, int M, uint4* out) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t r = blockIdx.x * 4 + (threadIdx.x >> 6); r < M; r += gridDim.x * 4) {
+    const int t = targets[r];
+    const bool counts = t >= 0 && t < V;
+    for (int i = lane; i < per; i += 64)
+      out[r * per + i] = counts ? x[r * per + i] : make_uint4(0, 0, 0, 0);
+  }
+}
+
 int xent_tile_cols(int tile) { return tile == 256256 ? 256 : 128; }
 
 template <typename T>
@@ -1047,6 +1061,14 @@ hipError_t launch_xent(bool is_bf16, int M, int D, int V, const void* x, const v
                        const int32_t* targets, float* loss, float* lse, void* ws, hipStream_t s) {
   return is_bf16 ? xent_forward<bf16>(M, D, V, x, w, targets, loss, lse, ws, s)
                  : xent_forward<float>(M, D, V, x, w, targets, loss, lse, ws, s);
+}
+
+hipError_t launch_xent_rows(bool is_bf16, int M, int D, int V, const void* x,
+                            const int32_t* targets, void* out, hipStream_t s) {
+  const int per = D / (is_bf16 ? 8 : 4);  // D is a multiple of 8
+  return launch("cross_entropy_rows", xent_rows_kernel,
+                dim3((unsigned)std::min<int64_t>(((int64_t)M + 3) / 4, 4096)), dim3(256), 0, s,
+                (const uint4*)x, targets, V, per, M, (uint4*)out);
 }
 
 hipError_t launch_xent_dz(bool is_bf16, int M, int D, int V, int v0, int nv, const void* x,

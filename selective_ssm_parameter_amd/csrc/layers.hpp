@@ -86,6 +86,9 @@ hipError_t launch_dense_tn(bool is_bf16, const char* name, int M, int R, int S, 
 size_t xent_ws_bytes(bool is_bf16, int M, int D, int V);
 hipError_t launch_xent(bool is_bf16, int M, int D, int V, const void* x, const void* w,
                        const int32_t* targets, float* loss, float* lse, void* ws, hipStream_t s);
+// out = x [M, D], zeros where a token's target counts for nothing.
+hipError_t launch_xent_rows(bool is_bf16, int M, int D, int V, const void* x,
+                            const int32_t* targets, void* out, hipStream_t s);
 // dz = (softmax - [target]) dloss of the nv vocabulary rows from v0 on (w: the
 // first of them): [M, nv rounded up to 8], float32, or for bf16 problems hi and
 // then lo, as gated_dz_bytes.

@@ -83,6 +83,9 @@ int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
 
 size_t xent_dz_bytes(const Dims& d, int64_t nv) { return align256(4 * (size_t)(d.M * round8(nv))); }
 
+// x without the rows of tokens that have no target, behind dz.
+size_t xent_rows_bytes(const Dims& d) { return align256((size_t)(d.M * d.D) * (d.bf16 ? 2 : 4)); }
+
 size_t xent_bwd_ws(const Dims& d) {
   const int M = (int)d.M, D = (int)d.D;
   const int64_t piece = xent_piece(d);
@@ -92,7 +95,7 @@ size_t xent_bwd_ws(const Dims& d) {
     sums = std::max({sums, dense_ws_bytes(d.bf16, d.bf16, false, M, D, (int)round8(nv)),
                      dense_ws_bytes(d.bf16, d.bf16, true, (int)nv, D, M)});
   }
-  return xent_dz_bytes(d, piece) + sums;
+  return xent_dz_bytes(d, piece) + xent_rows_bytes(d) + sums;
 }
 
 size_t ssm_ws(const Dims& d, int32_t call) {
@@ -398,18 +401,21 @@ swimba_status swimba_cross_entropy_backward(const swimba_dims* dims, const void*
   const int M = (int)d.M, D = (int)d.D, V = (int)d.HP, piece = (int)xent_piece(d);
   const size_t es = d.bf16 ? 2 : 4;
   unsigned char* dz = static_cast<unsigned char*>(ws);
-  unsigned char* part = dz + xent_dz_bytes(d, piece);
+  unsigned char* rows = dz + xent_dz_bytes(d, piece);
+  unsigned char* part = rows + xent_rows_bytes(d);
+  hipError_t e = launch_xent_rows(d.bf16, M, D, V, x, targets, rows, stream);
+  if (e != hipSuccess) return hip_status(e, "cross_entropy_backward rows launch");
   for (int v0 = 0; v0 < V; v0 += piece) {
     const int nv = std::min(piece, V - v0), ld = (int)round8(nv);
     const void* wp = static_cast<const unsigned char*>(w) + (size_t)v0 * D * es;
     const void* lo = d.bf16 ? dz + (size_t)M * ld * 2 : nullptr;
-    hipError_t e = launch_xent_dz(d.bf16, M, D, V, v0, nv, x, wp, targets, lse, dloss, dz, stream);
+    e = launch_xent_dz(d.bf16, M, D, V, v0, nv, x, wp, targets, lse, dloss, dz, stream);
     if (e != hipSuccess) return hip_status(e, "cross_entropy_backward dz launch");
     e = launch_dense_nn(d.bf16, "cross_entropy_dx", M, ld, D, dz, lo, wp, dx, part, stream, nv,
                         v0 > 0);
     if (e != hipSuccess) return hip_status(e, "cross_entropy_backward dx launch");
-    e = launch_dense_tn(d.bf16, "cross_entropy_dw", M, nv, D, dz, lo, x, dw + (size_t)v0 * D, part,
-                        stream, ld);
+    e = launch_dense_tn(d.bf16, "cross_entropy_dw", M, nv, D, dz, lo, rows, dw + (size_t)v0 * D,
+                        part, stream, ld);
     if (e != hipSuccess) return hip_status(e, "cross_entropy_backward dw launch");
   }
   return SWIMBA_OK;

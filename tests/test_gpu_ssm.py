@@ -523,6 +523,25 @@ def test_cross_entropy_special_values(dtype):
     assert not dx.any() and not dw.any()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_cross_entropy_without_targets_ignores_their_rows(dtype):
+    """NaN and infinities in the rows of tokens without a target give what zeros there give."""
+    for M, D, V in ((70, 64, 133), (1500, 264, 4100)):
+        d, x, w, t, g = loss_case(M, D, V, dtype, seed=3)
+        t[:5], t[5] = -1, 0
+        none = torch.from_numpy((t < 0) | (t >= V)).cuda()
+        g[none] = float("nan")
+        g[5] = 1.0
+        x[none] = 0
+        want = loss_run(d, x, w, t, g)
+        x[none] = float("nan")
+        x[0], x[1] = float("inf"), float("-inf")
+        got = loss_run(d, x, w, t, g)
+        assert (got[0][none] == 0).all() and (got[2][none] == 0).all()
+        for k, (a, b) in enumerate(zip(got, want)):  # (an lse is that of its row)
+            assert torch.equal(a[~none], b[~none]) if k == 1 else torch.equal(a, b)
+
+
 def test_cross_entropy_of_weights_past_2_gib():
     """The backward's pieces are cut where a buffer would not reach: dx of a few tokens
     against float64, dw where the targets are."""
