@@ -10,8 +10,7 @@
 // some 8 and, with the sums over channels and what a token needs by itself, 28, and the
 // segments' first passes another 5 each. Measured: 65536 x 2048 x 16 bf16 975 us (first
 // pass 385 to 430; vector units issuing 98 % of the cycles), padded 8 x 2048 x 1536 x
-// 16 forward and backward 471 to 491 us (first passes 56 and 61, forward 95, backward
-// 250 to 290 at 72 % issuing, sums 12), 256 x 4096 x 16 one token 25 us (HBM).
+// 16 forward and backward 441 us, 256 x 4096 x 16 one token 25 us (HBM).
 //
 // A wave walks the tokens of 16 channels x 16 states: lane (channel q = lane / 4,
 // j = lane % 4) holds states 4 j .. 4 j + 3 of its channel, so that sums over
@@ -133,16 +132,21 @@ struct Place {
   int sb, cw;              // the wave's block of states, its place among the channels' waves
   int j, q;                // lane % 4, lane / 4
   int blk0, blk1;          // blocks of the segment
+  int off0, off1;          // blocks past the length, whose zeros it writes
   bool on;                 // the channel exists
   uint32_t cb;             // index of the workgroup's block of channels in its group
 };
-__device__ __forceinline__ Place place_of(const SScanArgs& A, int segs) {
+// segs: the segments that have workgroups, from `from` on. A sequence's blocks in
+// use are shared by all of its segments, and so are those past its length (segments
+// of equal length for all sequences leave the card to the long ones: a padded 8 x 2048
+// x 1536 training step 472 instead of 453 us, with twelve workgroups a CU).
+__device__ __forceinline__ Place place_of(const SScanArgs& A, int segs, int from = 0) {
   Place p;
   const int cw = channel_waves(A.N), gb = group_blocks(A.Ch, A.N, A.G), per = A.Ch / A.G;
   const unsigned cols = gb * A.G, id = blockIdx.x;
   const unsigned bs = id / cols, col = id - bs * cols;
   p.b = __builtin_amdgcn_readfirstlane(bs / segs);
-  p.seg = __builtin_amdgcn_readfirstlane(bs - p.b * segs);
+  p.seg = __builtin_amdgcn_readfirstlane(bs - p.b * segs) + from;
   p.g = __builtin_amdgcn_readfirstlane(col / gb);
   p.cb = __builtin_amdgcn_readfirstlane(col - p.g * gb);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -157,9 +161,12 @@ __device__ __forceinline__ Place place_of(const SScanArgs& A, int segs) {
   p.n0 = p.sb * kStates + p.j * kQ;
   p.len = A.T;
   if (A.lens) p.len = __builtin_amdgcn_readfirstlane(min(max(A.lens[p.b], 0), A.T));
-  const int nblk = (A.T + kTok - 1) / kTok;
-  p.blk0 = p.seg * A.seg_blocks;
-  p.blk1 = min(nblk, p.blk0 + A.seg_blocks);
+  const int nblk = (A.T + kTok - 1) / kTok, live = (p.len + kTok - 1) / kTok;
+  const int run = (live + A.segs - 1) / A.segs, off = (nblk - live + A.segs - 1) / A.segs;
+  p.blk0 = min(live, p.seg * run);
+  p.blk1 = min(live, p.blk0 + run);
+  p.off0 = min(nblk, live + p.seg * off);
+  p.off1 = min(nblk, p.off0 + off);
   return p;
 }
 
@@ -354,7 +361,6 @@ __global__ __launch_bounds__(64 * kMaxWaves) void sscan_ends_kernel(SScanArgs A)
   const Coef co(A, p);
   floatx4 h = {0.f, 0.f, 0.f, 0.f};
   float sum = 0.f;
-  const int blk1 = min(p.blk1, (p.len + kTok - 1) / kTok);
   Four xr, dr;
   typename Bits<T>::t br;
   auto fetch = [&](int blk) {
@@ -362,8 +368,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void sscan_ends_kernel(SScanArgs A)
     dr = load_four<T>(A.dt, A.lddt, A, p, blk);
     br = load_bc<T>(A.B, A, p, blk, vec);
   };
-  if (p.blk0 < blk1) fetch(p.blk0);
-  for (int blk = p.blk0; blk < blk1; ++blk) {
+  if (p.blk0 < p.blk1) fetch(p.blk0);
+  for (int blk = p.blk0; blk < p.blk1; ++blk) {
     float delta[4], u[4], sig;
 #pragma unroll
     for (int i = 0; i < 4; ++i) delta[i] = softplus(value<T>(dr.v[i]) + co.bias, sig);
@@ -374,7 +380,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void sscan_ends_kernel(SScanArgs A)
       sum += delta[i];
     }
     bt[p.q][p.j] = widen<T>(br);
-    if (blk + 1 < blk1) fetch(blk + 1);
+    if (blk + 1 < p.blk1) fetch(blk + 1);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       up4([&](auto Q) {
@@ -404,8 +410,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256) void sscan_kernel(SSc
   BC& bc = lds[wave];
   const bool vec = vec_bc<T>(A);
   const Coef co(A, p);
-  const int nblk = (A.T + kTok - 1) / kTok, live = (p.len + kTok - 1) / kTok;
-  const int blk1 = min(p.blk1, live);
+  const int nblk = (A.T + kTok - 1) / kTok;
   Four xr, dr, zr;
   typename Bits<T>::t br, cr;
   auto fetch = [&](int blk) {
@@ -415,14 +420,14 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256) void sscan_kernel(SSc
     br = load_bc<T>(A.B, A, p, blk, vec);
     cr = load_bc<T>(A.C, A, p, blk, vec);
   };
-  if (p.blk0 < blk1) fetch(p.blk0);
+  if (p.blk0 < p.blk1) fetch(p.blk0);
   // the state that enters the segment
   floatx4 h = load_states(A.h_init ? A.h_init + ((size_t)p.b * A.Ch + p.c) * A.N : nullptr, p.n0,
                           A.N, p.on);
   if (A.segs > 1) {
     join_segments(A, p, co, 0, p.seg, h);
   }
-  for (int blk = p.blk0; blk < blk1; ++blk) {
+  for (int blk = p.blk0; blk < p.blk1; ++blk) {
     if (A.carry && p.on)
       *reinterpret_cast<floatx4*>(A.carry + (((size_t)p.b * nblk + blk) * A.Ch + p.c) * np +
                                   p.n0) = h;
@@ -442,7 +447,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256) void sscan_kernel(SSc
     }
     bc.b[p.q][p.j] = widen<T>(br);
     bc.c[p.q][p.j] = widen<T>(cr);
-    if (blk + 1 < blk1) fetch(blk + 1);
+    if (blk + 1 < p.blk1) fetch(blk + 1);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float y[4];
@@ -481,10 +486,10 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256) void sscan_kernel(SSc
   }
   if (!SPLIT || p.sb == 0) {
     const float zeros[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int blk = max(p.blk0, live); blk < p.blk1; ++blk)
+    for (int blk = p.off0; blk < p.off1; ++blk)
       store_four<T>(A.y, A.Ch, A, p, blk, zeros);
   }
-  if (A.h_final && p.on && p.blk1 == nblk)
+  if (A.h_final && p.on && p.seg == A.segs - 1)
     store_states(A.h_final + ((size_t)p.b * A.Ch + p.c) * A.N, p.n0, A.N, h);
 }
 
@@ -495,17 +500,12 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256) void sscan_kernel(SSc
 template <typename T, bool GATED>
 __global__ __launch_bounds__(64 * kMaxWaves) void sscan_bwd_ends_kernel(SScanArgs A) {
   __shared__ floatx4 lds[kMaxWaves][kTok][4];
-  Place p = place_of(A, A.segs - 1);
-  p.seg += 1;
-  const int nblk = (A.T + kTok - 1) / kTok;
-  p.blk0 = p.seg * A.seg_blocks;
-  p.blk1 = min(nblk, p.blk0 + A.seg_blocks);
+  const Place p = place_of(A, A.segs - 1, 1);
   floatx4(&ct)[kTok][4] = lds[threadIdx.x >> 6];
   const bool vec = vec_bc<T>(A);
   const Coef co(A, p);
   floatx4 c = {0.f, 0.f, 0.f, 0.f};
   float sum = 0.f;
-  const int blk1 = min(p.blk1, (p.len + kTok - 1) / kTok);
   Four dr, gr, zr;
   typename Bits<T>::t cr;
   auto fetch = [&](int blk) {
@@ -514,8 +514,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void sscan_bwd_ends_kernel(SScanArg
     if constexpr (GATED) zr = load_four<T>(A.z, A.ldz, A, p, blk);
     cr = load_bc<T>(A.C, A, p, blk, vec);
   };
-  if (p.blk0 < blk1) fetch(blk1 - 1);
-  for (int blk = blk1 - 1; blk >= p.blk0; --blk) {
+  if (p.blk0 < p.blk1) fetch(p.blk1 - 1);
+  for (int blk = p.blk1 - 1; blk >= p.blk0; --blk) {
     float delta[4], v[4], sig;
 #pragma unroll
     for (int i = 0; i < 4; ++i) delta[i] = softplus(value<T>(dr.v[i]) + co.bias, sig);
@@ -605,8 +605,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256, SPLIT ? 1 : 2) void s
   BC& bc = lds[wave];
   const bool vec = vec_bc<T>(A);
   const Coef co(A, p);
-  const int nblk = (A.T + kTok - 1) / kTok, live = (p.len + kTok - 1) / kTok;
-  const int blk1 = min(p.blk1, live);
+  const int nblk = (A.T + kTok - 1) / kTok;
   const BwdBoard board(A);
   const int np = board.np;
   Four xr, dr, zr, gr;
@@ -623,7 +622,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256, SPLIT ? 1 : 2) void s
     hr = *reinterpret_cast<const floatx4*>(
         A.carry_in + (((size_t)p.b * nblk + blk) * A.Ch + p.c) * np + p.n0);
   };
-  if (p.blk0 < blk1) fetch(blk1 - 1);
+  if (p.blk0 < p.blk1) fetch(p.blk1 - 1);
   // the gradient of the state that leaves the segment
   floatx4 c = load_states(A.dh_final ? A.dh_final + ((size_t)p.b * A.Ch + p.c) * A.N : nullptr,
                           p.n0, A.N, p.on);
@@ -633,7 +632,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256, SPLIT ? 1 : 2) void s
   }
   floatx4 dA = {0.f, 0.f, 0.f, 0.f};
   float dD = 0.f, dbias = 0.f;
-  for (int blk = blk1 - 1; blk >= p.blk0; --blk) {
+  for (int blk = p.blk1 - 1; blk >= p.blk0; --blk) {
     const int half = blk & 1;
     const bool tail = (blk + 1) * kTok > p.len;
     float delta[4], u[4], v[4];
@@ -799,7 +798,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * kMaxWaves : 256, SPLIT ? 1 : 2) void s
   }
   if (!SPLIT || p.sb == 0) {
     const float zeros[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int blk = max(p.blk0, live); blk < p.blk1; ++blk) {
+    for (int blk = p.off0; blk < p.off1; ++blk) {
       store_four<T>(A.dx, A.lddx, A, p, blk, zeros);
       store_four<T>(A.ddt, A.ldddt, A, p, blk, zeros);
       if constexpr (GATED) store_four<T>(A.dz, A.lddz, A, p, blk, zeros);
@@ -957,23 +956,25 @@ __global__ __launch_bounds__(256) void sscan_step_kernel(SScanArgs A) {
 
 // ---------------------------------------------------------------- launch
 
-// Segments per sequence, so that some kWant workgroups run (twelve a CU: fewer leave
-// CUs idle at the end, more join more segments;
-// at 8, 12, 16 a CU 65536 x 2048 forward takes 980, 975, 987 us, a padded 8 x 2048 x
-// 1536 training step 486, 471, 479, an unpadded one 717, 692, 709); at most kSegRoot
+// Segments per sequence, as many as give at most kWant workgroups, eight a CU: fewer
+// leave CUs idle at the end, more join more segments and start more walks. Up to 6, 8,
+// 12 and 16 a CU: 65536 x 2048 forward 1023, 984, 981, 996 us, 32 x 700 x 3000 forward
+// 310, 307, 395, 395, a padded 8 x 2048 x 1536 training step 461, 441, 453, 461, an
+// unpadded one 706, 711, 696, 718, a padded 64 x 512 x 1536 one 771, 771, 814, 817 (at
+// least 12: 32 x 700 x 3000 423, the others as up to 12). And at most kSegRoot
 // sqrt(blocks): where so few workgroups run that each one's time is that of its own
 // instructions, a block takes some 2 to 3 us and the join some 0.15 us a segment, and
 // the sum of both is least about there (a 2 x 777 x 402 fp32 training step: 59 us,
 // 70 without this limit).
-constexpr int64_t kWant = 12 * 256;
+constexpr int64_t kWant = 8 * 256;
 constexpr double kSegRoot = 4;
 void segments(SScanArgs& A) {
   const int64_t wg = (int64_t)A.Bt * A.G * group_blocks(A.Ch, A.N, A.G);
   const int nblk = (A.T + kTok - 1) / kTok;
   const int64_t most = (int64_t)(kSegRoot * std::sqrt((double)nblk));
-  int64_t s = std::max<int64_t>(1, std::min({(kWant + wg - 1) / wg, most, (int64_t)nblk}));
-  A.seg_blocks = (int)((nblk + s - 1) / s);
-  A.segs = (nblk + A.seg_blocks - 1) / A.seg_blocks;
+  int64_t s = std::max<int64_t>(1, std::min({kWant / wg, most, (int64_t)nblk}));
+  const int64_t run = (nblk + s - 1) / s;
+  A.segs = (int)((nblk + run - 1) / run);
 }
 
 unsigned workgroups(const SScanArgs& A, int segs) {

@@ -60,7 +60,7 @@ struct SScanArgs {
   float* h;
   void* ws;
   int Bt, T, Ch, N, G;
-  int segs, seg_blocks;  // the sequence in segs runs of seg_blocks blocks of tokens
+  int segs;  // runs of blocks of tokens that a sequence is cut into
 };
 size_t sscan_carry_bytes(int Bt, int T, int Ch, int N);
 size_t sscan_ws_bytes(int Bt, int T, int Ch, int N, int G);

@@ -260,6 +260,31 @@ def test_selective_scan(Bt, T, Ch, N, G, gate, lens, pad, h0, dtype):
         assert torch.equal(o2[k], o[k]), k
 
 
+@pytest.mark.parametrize("N,gate", [(16, True), (5, False), (40, True)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_selective_scan_shares_blocks_in_use_among_segments(N, gate, dtype):
+    """Many segments; lengths of none, of fewer blocks than segments, of a few and of all."""
+    Bt, T, Ch = 7, 700, 12
+    ln = np.array([0, 1, 16, 17, 333, 700, 689], np.int32)
+    q = scan_case(Bt, T, Ch, N, 1, dtype, gate, ln, 0, True, True, True, seed=N)
+    carry = ssm.selective_scan_carry(q["d"])
+    y, h = scan_forward(q, carry)
+    o = scan_backward(q, carry)
+    tol = sbd.scan_bounds(q["v"], ln, q["dt"], q["dyh"], q["dhh"])
+    wy, _, hs = osm.selective_scan(*q["v"].values(), ln)
+    check("y", y, wy, tol["y"])
+    check("h", h, hs[:, -1], tol["h"])
+    want = osm.selective_scan_backward(*q["v"].values(), q["dyh"], q["dhh"], ln)
+    for k, got in o.items():
+        if got is not None:
+            check(k, got, want[k], tol[k])
+    off = np.arange(T)[None] >= ln[:, None]
+    for k in ("dx", "ddt", "dB", "dC"):
+        assert not host(o[k]).reshape(Bt, T, -1)[off].any(), k
+    assert not host(y).reshape(Bt, T, -1)[off].any()
+    assert torch.equal(h[0], q["t"]["h_init"][0]) and torch.equal(o["dh_init"][0], q["dh"][0])
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("Ch,N,G,gate", [(40, 16, 1, True), (7, 5, 1, False), (12, 64, 2, True),
                                          (300, 17, 3, True), (9, 128, 1, True)])
