@@ -210,8 +210,9 @@ swimba_status swimba_cross_entropy(const swimba_dims* dims, const void* x, const
  * Backward of swimba_cross_entropy. The logits are computed again, a piece of
  * the vocabulary at a time:
  *   dz_v = (exp(z_v - lse) - [v = target]) dloss,   dx = dz w,   dw = dz^T x.
- * bf16 problems take dz into both products as the sum of two bf16 numbers: an
- * element is off by at most 2^-16 of itself.
+ * bf16 problems take dz into both products as the sum of bf16 numbers, of three
+ * for up to 8192 tokens (all of its bits) and of two beyond (an element is off
+ * by at most 2^-16 of itself).
  *   x, w, targets  as given to the forward;  lse [M] float32 as it wrote it
  *   dloss     [M] float32: gradient of each token's loss (not looked at
  *             where there is no target)

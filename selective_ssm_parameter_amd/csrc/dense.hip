@@ -72,6 +72,7 @@ struct XentArgs {
   float2* part;            // kXent: [tile columns][R]
   const float *lse, *dloss;  // kXentBwd
   int V, v0;               // the vocabulary; the first row of the piece at hand
+  int three;               // kXentBwd, bf16: dz as three numbers, not two
 };
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -335,7 +336,8 @@ __device__ __forceinline__ void xent_stats(const DenseArgs& A,
 }
 // dz = (exp(z - lse) - [target]) dloss, zeros where the target counts for nothing
 // and in the columns from S to the next multiple of 8; bf16: as two bf16 numbers,
-// the second in a half of its own (see the top of this file).
+// the second in a half of its own (see the top of this file), or three (all of its
+// 24 bits), the third behind them.
 template <typename T, class C>
 __device__ __forceinline__ void xent_dz(const DenseArgs& A, const floatx4 (&acc)[C::TM][C::TN],
                                         int r0, int s0) {
@@ -386,7 +388,13 @@ __device__ __forceinline__ void xent_dz(const DenseArgs& A, const floatx4 (&acc)
       if constexpr (sizeof(T) == 2) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) d[q] -= to_f32(h[q]);
-        store8<T>(hi + (size_t)A.R * ld, convert8<T, float>(d));
+        const typename Vec<T>::x8 lo = convert8<T, float>(d);
+        store8<T>(hi + (size_t)A.R * ld, lo);
+        if (A.xe.three) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) d[q] -= to_f32(lo[q]);
+          store8<T>(hi + (size_t)A.R * ld * 2, convert8<T, float>(d));
+        }
       }
     }
   }
@@ -711,7 +719,7 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
           ON o;
 #pragma unroll
           for (int j = 0; j < TN; ++j) o[j] = from_f32<TO>(acc[i][j][q]);
-          if constexpr (MODE == kNN && sizeof(TO) == 4)
+          if constexpr (sizeof(TO) == 4)
             if (A.add) o = o + *reinterpret_cast<const ON*>(row + col);
           *reinterpret_cast<ON*>(row + col) = o;
         }
@@ -724,7 +732,7 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
           O4 o;
 #pragma unroll
           for (int q = 0; q < 4; ++q) o[q] = from_f32<TO>(acc[i][j][q]);
-          if constexpr (MODE == kNN && sizeof(TO) == 4)
+          if constexpr (sizeof(TO) == 4)
             if (A.add) o = o + *reinterpret_cast<const O4*>(row + col);
           *reinterpret_cast<O4*>(row + col) = o;
         }
@@ -958,7 +966,7 @@ hipError_t launch_dense_nn(bool is_bf16, const char* name, int M, int K, int S, 
   hipError_t e;
   if (!is_bf16) e = go_tile<float, kNN, float, false>(r.tile, name, A, s);
   else if (a_lo) e = go_tile<bf16, kNN, float, true>(r.tile, name, A, s);
-  else if (r.splits > 1) e = go_tile<bf16, kNN, float, false>(r.tile, name, A, s);
+  else if (r.splits > 1 || add) e = go_tile<bf16, kNN, float, false>(r.tile, name, A, s);
   else e = go_tile<bf16, kNN, bf16, false>(r.tile, name, A, s);
   if (e != hipSuccess || r.splits == 1) return e;
   if (add) return sum_runs<float, true>(A, ws, out, s);
@@ -967,19 +975,20 @@ hipError_t launch_dense_nn(bool is_bf16, const char* name, int M, int K, int S, 
 
 hipError_t launch_dense_tn(bool is_bf16, const char* name, int M, int R, int S, const void* a,
                            const void* a_lo, const void* b, float* out, void* ws, hipStream_t s,
-                           int lda) {
+                           int lda, bool add) {
   DenseArgs A{};
   A.a = a; A.a_lo = a_lo; A.b = b; A.R = R; A.S = S; A.K = M; A.lda = lda < 0 ? R : lda;
   const Runs r = runs_of(is_bf16, a_lo != nullptr, true, R, S, M);
   A.splits = r.splits;
   A.ksplit = r.ksplit;
   A.out = r.splits > 1 ? ws : (void*)out;
+  A.add = add && r.splits == 1;
   hipError_t e;
   if (!is_bf16) e = go_tile<float, kTN, float, false>(r.tile, name, A, s);
   else if (a_lo) e = go_tile<bf16, kTN, float, true>(r.tile, name, A, s);
   else e = go_tile<bf16, kTN, float, false>(r.tile, name, A, s);
   if (e != hipSuccess || r.splits == 1) return e;
-  return sum_runs<float>(A, ws, out, s);
+  return add ? sum_runs<float, true>(A, ws, out, s) : sum_runs<float>(A, ws, out, s);
 }
 
 // ---- cross entropy
@@ -1071,7 +1080,7 @@ hipError_t launch_xent_rows(bool is_bf16, int M, int D, int V, const void* x,
                 (const uint4*)x, targets, V, per, M, (uint4*)out);
 }
 
-hipError_t launch_xent_dz(bool is_bf16, int M, int D, int V, int v0, int nv, const void* x,
+hipError_t launch_xent_dz(bool is_bf16, bool three, int M, int D, int V, int v0, int nv, const void* x,
                           const void* w, const int32_t* targets, const float* lse,
                           const float* dloss, void* dz, hipStream_t s) {
   DenseArgs A{};
@@ -1081,6 +1090,7 @@ hipError_t launch_xent_dz(bool is_bf16, int M, int D, int V, int v0, int nv, con
   A.xe.dloss = dloss;
   A.xe.V = V;
   A.xe.v0 = v0;
+  A.xe.three = three;
   return is_bf16 ? go_rows<bf16, kXentBwd>("cross_entropy_dz", A, s)
                  : go_rows<float, kXentBwd>("cross_entropy_dz", A, s);
 }

@@ -80,7 +80,7 @@ hipError_t launch_dense_nn(bool is_bf16, const char* name, int M, int K, int S, 
 // be null), b [M, S]; lda: a's rows are so far apart (R, or more).
 hipError_t launch_dense_tn(bool is_bf16, const char* name, int M, int R, int S, const void* a,
                            const void* a_lo, const void* b, float* out, void* ws, hipStream_t s,
-                           int lda = -1);
+                           int lda = -1, bool add = false);
 
 // ---- cross entropy over the rows of w [V, D]
 size_t xent_ws_bytes(bool is_bf16, int M, int D, int V);
@@ -91,8 +91,8 @@ hipError_t launch_xent_rows(bool is_bf16, int M, int D, int V, const void* x,
                             const int32_t* targets, void* out, hipStream_t s);
 // dz = (softmax - [target]) dloss of the nv vocabulary rows from v0 on (w: the
 // first of them): [M, nv rounded up to 8], float32, or for bf16 problems hi and
-// then lo, as gated_dz_bytes.
-hipError_t launch_xent_dz(bool is_bf16, int M, int D, int V, int v0, int nv, const void* x,
+// then lo, as gated_dz_bytes, and with `three` what those two leave.
+hipError_t launch_xent_dz(bool is_bf16, bool three, int M, int D, int V, int v0, int nv, const void* x,
                           const void* w, const int32_t* targets, const float* lse,
                           const float* dloss, void* dz, hipStream_t s);
 

@@ -81,7 +81,19 @@ int64_t xent_piece(const Dims& d) {
 }
 int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
 
-size_t xent_dz_bytes(const Dims& d, int64_t nv) { return align256(4 * (size_t)(d.M * round8(nv))); }
+// bf16 problems take dz through both products as two bf16 numbers, an element off by
+// 2^-16 of itself at most. dx and dw are then off by up to 4e-6 (2-norm; 1.9e-6 at
+// 16384 x 768 over 32768 words), which is what long sums in float32 are off by anyway
+// (elementary float32 products: 2 to 3e-6 at 16384 tokens); for shorter ones it would
+// be the larger part (4e-6 against 3e-7 at 246 tokens). There a third number, half as
+// much again in both products (8192 x 768 over 16000 words: 1655 us, with two 1232),
+// makes it all of dz: 2e-7 at 246 tokens, 8e-7 at 8192.
+constexpr int64_t kThreeTokens = 8192;
+bool xent_three(const Dims& d) { return d.bf16 && d.M <= kThreeTokens; }
+
+size_t xent_dz_bytes(const Dims& d, int64_t nv) {
+  return align256((xent_three(d) ? 6 : 4) * (size_t)(d.M * round8(nv)));
+}
 
 // x without the rows of tokens that have no target, behind dz.
 size_t xent_rows_bytes(const Dims& d) { return align256((size_t)(d.M * d.D) * (d.bf16 ? 2 : 4)); }
@@ -92,8 +104,10 @@ size_t xent_bwd_ws(const Dims& d) {
   size_t sums = 0;
   for (int64_t nv : {piece, d.HP % piece}) {
     if (nv == 0) continue;
-    sums = std::max({sums, dense_ws_bytes(d.bf16, d.bf16, false, M, D, (int)round8(nv)),
-                     dense_ws_bytes(d.bf16, d.bf16, true, (int)nv, D, M)});
+    for (bool split : {false, true})  // (the third number goes through by itself)
+      if (split ? d.bf16 : !d.bf16 || xent_three(d))
+        sums = std::max({sums, dense_ws_bytes(d.bf16, split, false, M, D, (int)round8(nv)),
+                         dense_ws_bytes(d.bf16, split, true, (int)nv, D, M)});
   }
   return xent_dz_bytes(d, piece) + xent_rows_bytes(d) + sums;
 }
@@ -400,6 +414,7 @@ swimba_status swimba_cross_entropy_backward(const swimba_dims* dims, const void*
   CHECK(check_ws(ws, ws_bytes, ssm_ws(d, SWIMBA_SSM_CROSS_ENTROPY_BACKWARD)));
   const int M = (int)d.M, D = (int)d.D, V = (int)d.HP, piece = (int)xent_piece(d);
   const size_t es = d.bf16 ? 2 : 4;
+  const bool three = xent_three(d);
   unsigned char* dz = static_cast<unsigned char*>(ws);
   unsigned char* rows = dz + xent_dz_bytes(d, piece);
   unsigned char* part = rows + xent_rows_bytes(d);
@@ -409,13 +424,20 @@ swimba_status swimba_cross_entropy_backward(const swimba_dims* dims, const void*
     const int nv = std::min(piece, V - v0), ld = (int)round8(nv);
     const void* wp = static_cast<const unsigned char*>(w) + (size_t)v0 * D * es;
     const void* lo = d.bf16 ? dz + (size_t)M * ld * 2 : nullptr;
-    e = launch_xent_dz(d.bf16, M, D, V, v0, nv, x, wp, targets, lse, dloss, dz, stream);
+    const void* rest = dz + (size_t)M * ld * 4;
+    e = launch_xent_dz(d.bf16, three, M, D, V, v0, nv, x, wp, targets, lse, dloss, dz, stream);
     if (e != hipSuccess) return hip_status(e, "cross_entropy_backward dz launch");
     e = launch_dense_nn(d.bf16, "cross_entropy_dx", M, ld, D, dz, lo, wp, dx, part, stream, nv,
                         v0 > 0);
+    if (e == hipSuccess && three)
+      e = launch_dense_nn(true, "cross_entropy_dx", M, ld, D, rest, nullptr, wp, dx, part, stream,
+                          nv, true);
     if (e != hipSuccess) return hip_status(e, "cross_entropy_backward dx launch");
     e = launch_dense_tn(d.bf16, "cross_entropy_dw", M, nv, D, dz, lo, rows, dw + (size_t)v0 * D,
                         part, stream, ld);
+    if (e == hipSuccess && three)
+      e = launch_dense_tn(true, "cross_entropy_dw", M, nv, D, rest, nullptr, rows,
+                          dw + (size_t)v0 * D, part, stream, ld, true);
     if (e != hipSuccess) return hip_status(e, "cross_entropy_backward dw launch");
   }
   return SWIMBA_OK;
