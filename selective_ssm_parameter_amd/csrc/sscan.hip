@@ -325,7 +325,9 @@ struct Coef {
 };
 
 // v, carried through the segments from `from` up (or down) to `to`, without it: a
-// batch of them loaded at once.
+// batch of them loaded at once. Where A > 0 a segment's factor may pass float32's range
+// while v, and v times it, do not: it is applied as two halves, each held below 2^127,
+// so that a zero stays one (any other number is past the range after both of those).
 __device__ __forceinline__ void join_segments(const SScanArgs& A, const Place& p, const Coef& co,
                                               int from, int to, floatx4& v) {
   constexpr int kBatch = 8;
@@ -344,7 +346,10 @@ __device__ __forceinline__ void join_segments(const SScanArgs& A, const Place& p
     for (int i = 0; i < kBatch; ++i) {
       if (i0 + i >= n) break;
 #pragma unroll
-      for (int k = 0; k < kQ; ++k) v[k] = __builtin_fmaf(exp2_(d[i] * co.A2[k]), v[k], e[i][k]);
+      for (int k = 0; k < kQ; ++k) {
+        const float half = exp2_(fminf(0.5f * d[i] * co.A2[k], 127.f));
+        v[k] = __builtin_fmaf(half, half * v[k], e[i][k]);
+      }
     }
   }
 }
