@@ -193,9 +193,13 @@ swimba_status swimba_selective_step(const swimba_dims* dims, const void* x, int6
 /*
  * Softmax cross entropy of each token over a vocabulary, without the logits:
  *   z = x w^T (float32),   lse = log sum_v exp(z_v),   loss = lse - z[target].
+ * The loss is formed from the largest logit and the sum of exponentials below
+ * it, so that a small one keeps its precision next to large logits.
  * A target outside [0, V) is no target: its loss is 0 and it gives no
- * gradient, whatever its row of x holds (its lse is that of the token). An infinite or NaN logit makes its
- * token's lse infinite or NaN.
+ * gradient, whatever its row of x holds (its lse is that of the token). A
+ * logit of +inf or NaN makes its token's lse infinite or NaN; one of -inf
+ * counts for nothing, but where all are (lse -inf) or it is the target's
+ * (loss +inf).
  *   x         [M, D] dtype;  w [V, D] dtype
  *   targets   [M] int32
  *   loss      [M] float32 out;  lse [M] float32 out
@@ -210,6 +214,8 @@ swimba_status swimba_cross_entropy(const swimba_dims* dims, const void* x, const
  * Backward of swimba_cross_entropy. The logits are computed again, a piece of
  * the vocabulary at a time:
  *   dz_v = (exp(z_v - lse) - [v = target]) dloss,   dx = dz w,   dw = dz^T x.
+ * (An exponential is off by the rounding of its lse, up to 2^-24 |lse| of
+ * itself.)
  * bf16 problems take dz into both products as the sum of bf16 numbers, of three
  * for up to 8192 tokens (all of its bits) and of two beyond (an element is off
  * by at most 2^-16 of itself).

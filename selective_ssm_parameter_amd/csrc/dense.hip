@@ -1015,11 +1015,12 @@ __global__ __launch_bounds__(256) void xent_finish_kernel(XentArgs X, int M, int
   __syncthreads();
   if (g || row >= M) return;
   for (int w = 1; w < GROUPS; ++w) v = xent_join(v, part[w][r]);
-  // a row of -inf alone: -inf
-  const float l = v.x == -INFINITY && v.y == 0.f ? -INFINITY : v.x + logf(v.y);
+  const float l = logf(v.y);
   const int t = X.targets[row];
-  lse[row] = l;
-  loss[row] = t >= 0 && t < X.V ? l - X.zt[row] : 0.f;
+  // a row of -inf alone: -inf
+  lse[row] = v.x == -INFINITY && v.y == 0.f ? -INFINITY : v.x + l;
+  // (not lse - z: the rounding of a large lse would be all that is left of a small loss)
+  loss[row] = t >= 0 && t < X.V ? l + (v.x - X.zt[row]) : 0.f;
 }
 
 // x with zeros in the rows of tokens without a target (which may hold NaN), for the
