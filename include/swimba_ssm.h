@@ -216,9 +216,8 @@ swimba_status swimba_cross_entropy(const swimba_dims* dims, const void* x, const
  *   dz_v = (exp(z_v - lse) - [v = target]) dloss,   dx = dz w,   dw = dz^T x.
  * (An exponential is off by the rounding of its lse, up to 2^-24 |lse| of
  * itself.)
- * bf16 problems take dz into both products as the sum of bf16 numbers, of three
- * for up to 8192 tokens (all of its bits) and of two beyond (an element is off
- * by at most 2^-16 of itself).
+ * bf16 problems take dz into both products as the sum of three bf16 numbers,
+ * all of its bits.
  *   x, w, targets  as given to the forward;  lse [M] float32 as it wrote it
  *   dloss     [M] float32: gradient of each token's loss (not looked at
  *             where there is no target)

@@ -21,7 +21,8 @@
 // element off by at most 2^-16 of itself, where one bf16 rounding is off by
 // 2^-8 (16384 x 768 -> 2 x 2048: dx and dw_in 2.5e-6 off in the 2-norm, against
 // 2.5e-3 with one and 1.2e-6 with an fp32 product): each LDS stage holds both,
-// three stages of them, and a fragment of the other operand serves both.
+// three stages of them, and a fragment of the other operand serves both. The cross
+// entropy's dz goes through as three, all of its 24 bits, in the same way.
 // The cross entropy's z stays in registers too: the forward's epilogue leaves a row's
 // largest z and sum of exponentials per tile, the backward's recomputes z and leaves
 // dz. 16384 tokens, 768 -> 32768 words: statistics 843 us (980 TFLOP/s; 16384 x 2048
@@ -72,7 +73,6 @@ struct XentArgs {
   float2* part;            // kXent: [tile columns][R]
   const float *lse, *dloss;  // kXentBwd
   int V, v0;               // the vocabulary; the first row of the piece at hand
-  int three;               // kXentBwd, bf16: dz as three numbers, not two
 };
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -86,7 +86,7 @@ __device__ __forceinline__ float2 xent_join(float2 a, float2 b) {
 
 struct DenseArgs {
   const void *a, *b;
-  const void* a_lo;  // split operands: a = a (bf16) + a_lo (bf16)
+  const void* a_lo[2];  // a of several bf16 numbers: what is added to it
   void* out;         // kGated: h; kGatedBwd: dz (its lo half behind it for bf16)
   void* z;           // kGated: [g | u] or null
   const void* dh;    // kGatedBwd
@@ -101,23 +101,29 @@ struct DenseArgs {
   XentArgs xe;    // kXent, kXentBwd: S = the vocabulary's (or its piece's) rows
 };
 
-template <typename T, class C, Mode MODE, bool SPLIT>
+// NUM: numbers that a is the sum of.
+template <typename T, class C, Mode MODE, int NUM>
 struct DLay {
   static constexpr int ES = sizeof(T), EPC = 16 / ES;
   // (fp32 128 x 128 gated tiles: two stages, so that two workgroups share a CU,
   // 114 against 90 TFLOP/s at 12000 x 320 x 512; no gain for columns tiles)
   // (32 x 128: three, also for two workgroups a CU)
-  static constexpr int NS =
-      SPLIT ? 3 : !(rows_b(MODE) && ES == 4) ? 4 : C::BM == 128 ? 2 : C::BM == 32 ? 3 : 4;
+  // (three numbers: what fits LDS, two workgroups a CU for 128 x 128)
+  static constexpr int NS = NUM == 3             ? (C::BM >= 128 ? 2 : 3)
+                            : NUM == 2           ? 3
+                            : !(rows_b(MODE) && ES == 4) ? 4
+                            : C::BM == 128       ? 2
+                            : C::BM == 32        ? 3
+                                                 : 4;
   static constexpr bool ACOL = MODE == kTN, BCOL = !rows_b(MODE);
   // tile in LDS: rows of CPR 16-byte chunks
   static constexpr int AROWS = ACOL ? kBK : C::BM, ACPR = (ACOL ? C::BM : kBK) / EPC;
   static constexpr int BROWS = BCOL ? kBK : C::BN, BCPR = (BCOL ? C::BN : kBK) / EPC;
-  static constexpr int AB = AROWS * ACPR * 16, BB = BROWS * BCPR * 16, STAGE = AB * (SPLIT ? 2 : 1) + BB;
+  static constexpr int AB = AROWS * ACPR * 16, BB = BROWS * BCPR * 16, STAGE = AB * NUM + BB;
   static constexpr int BOFF = STAGE - BB;  // a (, a_lo), b
   static constexpr int NA = AB / 1024, NB = BB / 1024;  // copies of 64 chunks
   static constexpr int MA = (NA + C::NW - 1) / C::NW, MB = (NB + C::NW - 1) / C::NW;  // per wave
-  static constexpr int CPW = MA * (SPLIT ? 2 : 1) + MB;
+  static constexpr int CPW = MA * NUM + MB;
   static_assert(AB % 1024 == 0 && BB % 1024 == 0, "whole copies");
 };
 
@@ -335,9 +341,8 @@ __device__ __forceinline__ void xent_stats(const DenseArgs& A,
   }
 }
 // dz = (exp(z - lse) - [target]) dloss, zeros where the target counts for nothing
-// and in the columns from S to the next multiple of 8; bf16: as two bf16 numbers,
-// the second in a half of its own (see the top of this file), or three (all of its
-// 24 bits), the third behind them.
+// and in the columns from S to the next multiple of 8; bf16: as three bf16 numbers
+// (all of its 24 bits), each in a part of its own.
 template <typename T, class C>
 __device__ __forceinline__ void xent_dz(const DenseArgs& A, const floatx4 (&acc)[C::TM][C::TN],
                                         int r0, int s0) {
@@ -390,19 +395,17 @@ __device__ __forceinline__ void xent_dz(const DenseArgs& A, const floatx4 (&acc)
         for (int q = 0; q < 8; ++q) d[q] -= to_f32(h[q]);
         const typename Vec<T>::x8 lo = convert8<T, float>(d);
         store8<T>(hi + (size_t)A.R * ld, lo);
-        if (A.xe.three) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) d[q] -= to_f32(lo[q]);
-          store8<T>(hi + (size_t)A.R * ld * 2, convert8<T, float>(d));
-        }
+        for (int q = 0; q < 8; ++q) d[q] -= to_f32(lo[q]);
+        store8<T>(hi + (size_t)A.R * ld * 2, convert8<T, float>(d));
       }
     }
   }
 }
 
-template <typename T, class C, Mode MODE, typename TO, bool SPLIT>
+template <typename T, class C, Mode MODE, typename TO, int NUM>
 __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
-  typedef DLay<T, C, MODE, SPLIT> L;
+  typedef DLay<T, C, MODE, NUM> L;
   typedef typename Vec<T>::x8 F;
   constexpr int BM = C::BM, BN = C::BN, NW = C::NW, TM = C::TM, TN = C::TN;
   constexpr int MA = L::MA, MB = L::MB, EPC = L::EPC;
@@ -442,19 +445,24 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   // split's rows have to stay below 2 GiB.
   const T* ap = static_cast<const T*>(A.a);
   const T* bp = static_cast<const T*>(A.b);
-  const T* lp = static_cast<const T*>(A.a_lo);
-  BufRes rA, rL, rB;
+  BufRes rA, rA1, rA2, rB;  // (a's numbers; the type has no arrays)
+  auto part = [&](int n) { return n == 0 ? ap : static_cast<const T*>(A.a_lo[n - 1]); };
   uint32_t aoff[MA], boff[MB];
   int akc[MA], bkc[MB];  // rows operands: the chunk's first k, to cut at K
   uint32_t astep, bstep;
   if constexpr (L::ACOL) {
-    rA = make_rsrc(ap + (size_t)kbeg * A.lda, (uint64_t)K * A.lda * ES);
-    if constexpr (SPLIT) rL = make_rsrc(lp + (size_t)kbeg * A.lda, (uint64_t)K * A.lda * ES);
+    auto rows = [&](int n) {
+      return make_rsrc(part(n) + (size_t)kbeg * A.lda, (uint64_t)K * A.lda * ES);
+    };
+    rA = rows(0);
+    if constexpr (NUM > 1) rA1 = rows(1);
+    if constexpr (NUM > 2) rA2 = rows(2);
     astep = kBK * (uint32_t)A.lda * ES;
   } else {
     const uint64_t bytes = ((uint64_t)nrows * A.K - kbeg) * ES;
-    rA = make_rsrc(ap + (size_t)r0 * A.K + kbeg, bytes);
-    if constexpr (SPLIT) rL = make_rsrc(lp + (size_t)r0 * A.K + kbeg, bytes);
+    rA = make_rsrc(part(0) + (size_t)r0 * A.K + kbeg, bytes);
+    if constexpr (NUM > 1) rA1 = make_rsrc(part(1) + (size_t)r0 * A.K + kbeg, bytes);
+    if constexpr (NUM > 2) rA2 = make_rsrc(part(2) + (size_t)r0 * A.K + kbeg, bytes);
     astep = kBK * ES;
   }
   if constexpr (L::BCOL) {
@@ -509,13 +517,15 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
 #pragma unroll
     for (int m = 0; m < MA; ++m) {
       const uint32_t off = k0 + akc[m] < K && aoff[m] != kOOB ? aoff[m] + kt * astep : kOOB;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rA, (__attribute__((address_space(3))) void*)(st + 1024 * copy_of<L::NA, NW>(m, wave)), 16,
-          off, 0, 0, 0);
-      if constexpr (SPLIT)
+      unsigned char* to = st + 1024 * copy_of<L::NA, NW>(m, wave);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (__attribute__((address_space(3))) void*)to, 16,
+                                               off, 0, 0, 0);
+      if constexpr (NUM > 1)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rL, (__attribute__((address_space(3))) void*)(st + L::AB + 1024 * copy_of<L::NA, NW>(m, wave)),
-            16, off, 0, 0, 0);
+            rA1, (__attribute__((address_space(3))) void*)(to + L::AB), 16, off, 0, 0, 0);
+      if constexpr (NUM > 2)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rA2, (__attribute__((address_space(3))) void*)(to + 2 * L::AB), 16, off, 0, 0, 0);
     }
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
@@ -566,7 +576,7 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) bd[j] = zero8<T>();
   }
-  auto compute = [&](const unsigned char* st) {
+  auto compute = [&](const unsigned char* st) __attribute__((always_inline)) {
     F bf[TN], af[TM];
     load_b(st, bf);
     load_a(st, af);
@@ -582,8 +592,10 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
     for (int i = 0; i < (DEFER ? TM - 1 : TM); ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = mma16(bf[j], af[i], acc[i][j]);
-    if constexpr (SPLIT) {
-      load_a(st + L::AB, af);
+#pragma unroll
+    for (int n = 1; n < NUM; ++n) {
+      if constexpr (NUM == 3) __builtin_amdgcn_sched_barrier(0);  // (reads ahead would spill)
+      load_a(st + n * L::AB, af);
 #pragma unroll
       for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -594,7 +606,7 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
   // whole turns of the stages, every copy unconditional (steps past K
   // multiply zeros)
   const int nks = ((K + kBK - 1) / kBK + L::NS - 1) / L::NS * L::NS;
-  auto iter = [&](int kt, const unsigned char* cur, unsigned char* far) {
+  auto iter = [&](int kt, const unsigned char* cur, unsigned char* far) __attribute__((always_inline)) {
     wait_vm<(L::NS - 2) * L::CPW>();  // step kt landed (the steps after it may be in flight)
     stage_barrier();                  // step kt visible to all waves; step kt - 1 no longer read
     fetch(far, kt + L::NS - 1);
@@ -719,7 +731,7 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
           ON o;
 #pragma unroll
           for (int j = 0; j < TN; ++j) o[j] = from_f32<TO>(acc[i][j][q]);
-          if constexpr (sizeof(TO) == 4)
+          if constexpr (MODE == kNN && sizeof(TO) == 4)
             if (A.add) o = o + *reinterpret_cast<const ON*>(row + col);
           *reinterpret_cast<ON*>(row + col) = o;
         }
@@ -732,7 +744,7 @@ __global__ __launch_bounds__(C::NTH) void dense_kernel(DenseArgs A) {
           O4 o;
 #pragma unroll
           for (int q = 0; q < 4; ++q) o[q] = from_f32<TO>(acc[i][j][q]);
-          if constexpr (sizeof(TO) == 4)
+          if constexpr (MODE == kNN && sizeof(TO) == 4)
             if (A.add) o = o + *reinterpret_cast<const O4*>(row + col);
           *reinterpret_cast<O4*>(row + col) = o;
         }
@@ -860,12 +872,12 @@ __global__ __launch_bounds__(256) void dense_sum_kernel(const float* __restrict_
   }
 }
 
-template <typename T, class C, Mode MODE, typename TO, bool SPLIT = false>
+template <typename T, class C, Mode MODE, typename TO, int NUM = 1>
 hipError_t go(const char* name, const DenseArgs& A, hipStream_t s) {
   constexpr int SN = is_gated(MODE) ? C::BN / 2 : C::BN;
   const int64_t units = (int64_t)((A.R + C::BM - 1) / C::BM) * ((A.S + SN - 1) / SN) *
                         (rows_b(MODE) ? 1 : A.splits);
-  return launch(name, dense_kernel<T, C, MODE, TO, SPLIT>, dim3((unsigned)((units + 7) / 8 * 8)),
+  return launch(name, dense_kernel<T, C, MODE, TO, NUM>, dim3((unsigned)((units + 7) / 8 * 8)),
                 dim3(C::NTH), 0, s, A);
 }
 
@@ -873,7 +885,7 @@ hipError_t go(const char* name, const DenseArgs& A, hipStream_t s) {
 template <typename T, Mode MODE>
 hipError_t go_rows(const char* name, const DenseArgs& A, hipStream_t s) {
   const int tile = is_gated(MODE)
-                       ? plan(sizeof(T) == 2, false, true, A.R, 2 * (int64_t)A.S, A.K, 1).tile
+                       ? plan(sizeof(T) == 2, 0, true, A.R, 2 * (int64_t)A.S, A.K, 1).tile
                        : xent_tile(sizeof(T) == 2, A.R, A.S, A.K);
   if constexpr (sizeof(T) == 2)
     if (tile == 256256) return go<T, Big, MODE, T>(name, A, s);
@@ -899,15 +911,15 @@ hipError_t go_skinny(const DenseArgs& A, hipStream_t s) {
   return run(std::integral_constant<int, 4>());
 }
 
-template <typename T, Mode MODE, typename TO, bool SPLIT>
+template <typename T, Mode MODE, typename TO, int NUM>
 hipError_t go_tile(int tile, const char* name, const DenseArgs& A, hipStream_t s) {
   if constexpr (sizeof(T) == 2) {
-    if (tile == 256256) return go<T, Big, MODE, TO, SPLIT>(name, A, s);
-    if (tile == 256192) return go<T, Wide, MODE, TO, SPLIT>(name, A, s);
+    if (tile == 256256) return go<T, Big, MODE, TO, NUM>(name, A, s);
+    if (tile == 256192) return go<T, Wide, MODE, TO, NUM>(name, A, s);
   }
-  if (tile == 128128) return go<T, Mid, MODE, TO, SPLIT>(name, A, s);
-  if (tile == 64064) return go<T, Small64, MODE, TO, SPLIT>(name, A, s);
-  return go<T, Tiny, MODE, TO, SPLIT>(name, A, s);
+  if (tile == 128128) return go<T, Mid, MODE, TO, NUM>(name, A, s);
+  if (tile == 64064) return go<T, Small64, MODE, TO, NUM>(name, A, s);
+  return go<T, Tiny, MODE, TO, NUM>(name, A, s);
 }
 
 }  // namespace
@@ -935,8 +947,8 @@ hipError_t launch_gated_dz(bool is_bf16, int M, int D, int F, int act, const voi
                  : go_rows<float, kGatedBwd>("gated_dz", A, s);
 }
 
-size_t dense_ws_bytes(bool is_bf16, bool split, bool tn, int R, int S, int K) {
-  const Runs r = runs_of(is_bf16, split, tn, R, S, K);
+size_t dense_ws_bytes(bool is_bf16, int numbers, bool tn, int R, int S, int K) {
+  const Runs r = runs_of(is_bf16, numbers - 1, tn, R, S, K);
   return r.splits > 1 ? sizeof(float) * (size_t)r.splits * R * S : 0;
 }
 
@@ -951,44 +963,54 @@ hipError_t sum_runs(const DenseArgs& A, const void* ws, void* out, hipStream_t s
                 A.splits, n4, (TO*)out);
 }
 
+// a as numbers of `part` elements each, one behind the other.
+void set_numbers(DenseArgs& A, const void* a, int numbers, size_t part) {
+  A.a = a;
+  for (int n = 1; n < numbers; ++n)
+    A.a_lo[n - 1] = static_cast<const unsigned char*>(a) + n * part * 2;
+}
+
 }  // namespace
 
 hipError_t launch_dense_nn(bool is_bf16, const char* name, int M, int K, int S, const void* a,
-                           const void* a_lo, const void* b, void* out, void* ws, hipStream_t s,
-                           int kb, bool add) {
+                           int numbers, const void* b, void* out, void* ws, hipStream_t s, int kb,
+                           bool add) {
   DenseArgs A{};
-  A.a = a; A.a_lo = a_lo; A.b = b; A.R = M; A.S = S; A.K = K; A.kb = kb < 0 ? K : kb;
-  const Runs r = runs_of(is_bf16, a_lo != nullptr, false, M, S, K);
+  set_numbers(A, a, numbers, (size_t)M * K);
+  A.b = b; A.R = M; A.S = S; A.K = K; A.kb = kb < 0 ? K : kb;
+  const Runs r = runs_of(is_bf16, numbers - 1, false, M, S, K);
   A.splits = r.splits;
   A.ksplit = r.ksplit;
   A.out = r.splits > 1 ? ws : out;
   A.add = add && r.splits == 1;
   hipError_t e;
-  if (!is_bf16) e = go_tile<float, kNN, float, false>(r.tile, name, A, s);
-  else if (a_lo) e = go_tile<bf16, kNN, float, true>(r.tile, name, A, s);
-  else if (r.splits > 1 || add) e = go_tile<bf16, kNN, float, false>(r.tile, name, A, s);
-  else e = go_tile<bf16, kNN, bf16, false>(r.tile, name, A, s);
+  if (!is_bf16) e = go_tile<float, kNN, float, 1>(r.tile, name, A, s);
+  else if (numbers == 3) e = go_tile<bf16, kNN, float, 3>(r.tile, name, A, s);
+  else if (numbers == 2) e = go_tile<bf16, kNN, float, 2>(r.tile, name, A, s);
+  else if (r.splits > 1) e = go_tile<bf16, kNN, float, 1>(r.tile, name, A, s);
+  else e = go_tile<bf16, kNN, bf16, 1>(r.tile, name, A, s);
   if (e != hipSuccess || r.splits == 1) return e;
   if (add) return sum_runs<float, true>(A, ws, out, s);
-  return is_bf16 && !a_lo ? sum_runs<bf16>(A, ws, out, s) : sum_runs<float>(A, ws, out, s);
+  return is_bf16 && numbers == 1 ? sum_runs<bf16>(A, ws, out, s) : sum_runs<float>(A, ws, out, s);
 }
 
 hipError_t launch_dense_tn(bool is_bf16, const char* name, int M, int R, int S, const void* a,
-                           const void* a_lo, const void* b, float* out, void* ws, hipStream_t s,
-                           int lda, bool add) {
+                           int numbers, const void* b, float* out, void* ws, hipStream_t s,
+                           int lda) {
   DenseArgs A{};
-  A.a = a; A.a_lo = a_lo; A.b = b; A.R = R; A.S = S; A.K = M; A.lda = lda < 0 ? R : lda;
-  const Runs r = runs_of(is_bf16, a_lo != nullptr, true, R, S, M);
+  A.b = b; A.R = R; A.S = S; A.K = M; A.lda = lda < 0 ? R : lda;
+  set_numbers(A, a, numbers, (size_t)M * A.lda);
+  const Runs r = runs_of(is_bf16, numbers - 1, true, R, S, M);
   A.splits = r.splits;
   A.ksplit = r.ksplit;
   A.out = r.splits > 1 ? ws : (void*)out;
-  A.add = add && r.splits == 1;
   hipError_t e;
-  if (!is_bf16) e = go_tile<float, kTN, float, false>(r.tile, name, A, s);
-  else if (a_lo) e = go_tile<bf16, kTN, float, true>(r.tile, name, A, s);
-  else e = go_tile<bf16, kTN, float, false>(r.tile, name, A, s);
+  if (!is_bf16) e = go_tile<float, kTN, float, 1>(r.tile, name, A, s);
+  else if (numbers == 3) e = go_tile<bf16, kTN, float, 3>(r.tile, name, A, s);
+  else if (numbers == 2) e = go_tile<bf16, kTN, float, 2>(r.tile, name, A, s);
+  else e = go_tile<bf16, kTN, float, 1>(r.tile, name, A, s);
   if (e != hipSuccess || r.splits == 1) return e;
-  return add ? sum_runs<float, true>(A, ws, out, s) : sum_runs<float>(A, ws, out, s);
+  return sum_runs<float>(A, ws, out, s);
 }
 
 // ---- cross entropy
@@ -1081,7 +1103,7 @@ hipError_t launch_xent_rows(bool is_bf16, int M, int D, int V, const void* x,
                 (const uint4*)x, targets, V, per, M, (uint4*)out);
 }
 
-hipError_t launch_xent_dz(bool is_bf16, bool three, int M, int D, int V, int v0, int nv, const void* x,
+hipError_t launch_xent_dz(bool is_bf16, int M, int D, int V, int v0, int nv, const void* x,
                           const void* w, const int32_t* targets, const float* lse,
                           const float* dloss, void* dz, hipStream_t s) {
   DenseArgs A{};
@@ -1091,7 +1113,6 @@ hipError_t launch_xent_dz(bool is_bf16, bool three, int M, int D, int V, int v0,
   A.xe.dloss = dloss;
   A.xe.V = V;
   A.xe.v0 = v0;
-  A.xe.three = three;
   return is_bf16 ? go_rows<bf16, kXentBwd>("cross_entropy_dz", A, s)
                  : go_rows<float, kXentBwd>("cross_entropy_dz", A, s);
 }

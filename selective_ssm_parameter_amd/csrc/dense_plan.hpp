@@ -20,16 +20,21 @@ constexpr int kBK = 32;  // k elements of a tile's step
 // (At 14 sizes drawn at random, 77 to 13483 tokens and widths of 64 to 5024 in both
 // types, the planned tile took 3 to 5 % longer than the best one on average over
 // each kind of product, 23 % at worst: fp32 6855 x 352 -> 2 x 440, 55 against 45 us.)
+// (The factors of three numbers are fitted by themselves, to which tile a product should
+// take: over dx and dw of 17 sizes of the cross entropy, 64 to 16384 tokens and 500 to
+// 131072 words, the planned tile takes 1.3 % longer than the best one on average, 15 % at
+// worst; by the factors of two, carried on, 3.3 %.)
 struct TileCost {
   int rows, cols, most;
   double busy, alone, rest;
-  double split;  // factor of a step with hi and lo
+  double split;  // factor of a step whose a is two numbers
+  double three = 1;  // and of one whose a is three
 };
-constexpr TileCost kBf16Tiles[] = {{256, 256, 1, 0.90, 0.90, 10, 1.8},
-                                   {256, 192, 1, 0.72, 0.72, 9, 1.9},
-                                   {128, 128, 2, 0.31, 0.35, 6, 1.6},
-                                   {64, 64, 4, 0.16, 0.20, 4, 1.8},
-                                   {32, 64, 6, 0.10, 0.20, 4, 1.8}};
+constexpr TileCost kBf16Tiles[] = {{256, 256, 1, 0.90, 0.90, 10, 1.8, 2.0},
+                                   {256, 192, 1, 0.72, 0.72, 9, 1.9, 1.9},
+                                   {128, 128, 2, 0.31, 0.35, 6, 1.6, 2.0},
+                                   {64, 64, 4, 0.16, 0.20, 4, 1.8, 3.5},
+                                   {32, 64, 6, 0.10, 0.20, 4, 1.8, 2.6}};
 constexpr TileCost kBf16Gated[] = {{256, 256, 1, 0.90, 0.90, 12, 1},
                                    {128, 128, 2, 0.31, 0.35, 7, 1},
                                    {64, 128, 3, 0.19, 0.22, 5, 1}};
@@ -43,8 +48,9 @@ struct Plan {
   int tile, splits;  // tile: rows * 1000 + columns
 };
 // most: the largest number of k runs; their partial sums are written, read and
-// summed at about 4 TB/s by one more launch.
-inline Plan plan(bool is_bf16, bool split, bool gated, int64_t R, int64_t S, int64_t K, int64_t most) {
+// summed at about 4 TB/s by one more launch. more: numbers that a is the sum of,
+// beyond the first.
+inline Plan plan(bool is_bf16, int more, bool gated, int64_t R, int64_t S, int64_t K, int64_t most) {
   Plan best{0, 1};
   double tbest = 1e30;
   const TileCost* tiles =
@@ -52,7 +58,7 @@ inline Plan plan(bool is_bf16, bool split, bool gated, int64_t R, int64_t S, int
   const int nt = is_bf16 ? (gated ? 3 : 5) : 3;
   for (int i = 0; i < nt; ++i) {
     const TileCost& c = tiles[i];
-    const double steps = (double)((K + kBK - 1) / kBK) * (split ? c.split : 1.0);
+    const double steps = (double)((K + kBK - 1) / kBK) * (more == 0 ? 1.0 : more == 1 ? c.split : c.three);
     const int64_t units = (R + c.rows - 1) / c.rows * ((S + c.cols - 1) / c.cols);
     if (i > 0 && units > (1 << 20)) continue;  // (a launch's threads are counted in 32 bits)
     for (int64_t n = 1; n <= most; ++n) {
@@ -78,8 +84,8 @@ inline Plan plan(bool is_bf16, bool split, bool gated, int64_t R, int64_t S, int
 struct Runs {
   int tile, splits, ksplit;
 };
-inline Runs runs_of(bool is_bf16, bool split, bool tn, int R, int S, int K) {
-  const Plan p = plan(is_bf16, split, false, R, S, K,
+inline Runs runs_of(bool is_bf16, int more, bool tn, int R, int S, int K) {
+  const Plan p = plan(is_bf16, more, false, R, S, K,
                       std::max<int64_t>(1, std::min<int64_t>(64, K / 256)));
   int64_t n = p.splits;
   if (tn) {
@@ -95,7 +101,7 @@ inline Runs runs_of(bool is_bf16, bool split, bool tn, int R, int S, int K) {
 // The tile of the cross entropy's products (tokens x vocabulary rows), by the costs
 // of the gated products' tiles, whose kernel it shares up to the epilogue.
 inline int xent_tile(bool is_bf16, int64_t R, int64_t S, int64_t K) {
-  return plan(is_bf16, false, true, R, S, K, 1).tile;
+  return plan(is_bf16, 0, true, R, S, K, 1).tile;
 }
 
 }  // namespace swimba

@@ -68,19 +68,20 @@ size_t gated_dz_bytes(bool is_bf16, int M, int F);
 hipError_t launch_gated_dz(bool is_bf16, int M, int D, int F, int act, const void* x,
                            const void* w_in, const void* dh, void* dz, hipStream_t s);
 // Partial sums of a product that runs its k in pieces (ws below): out [R, S] of
-// K terms; tn: a weight gradient; split: with a_lo.
-size_t dense_ws_bytes(bool is_bf16, bool split, bool tn, int R, int S, int K);
-// out [M, S] = a [M, K] b [K, S]; with a_lo (bf16 problems) a is a + a_lo and
-// out is float32, else out has the input type.
+// K terms; tn: a weight gradient; numbers: those that a is the sum of.
+size_t dense_ws_bytes(bool is_bf16, int numbers, bool tn, int R, int S, int K);
+// out [M, S] = a [M, K] b [K, S]; a of two or three numbers (bf16 problems) is the sum
+// of as many tensors, one behind the other, and out is float32, else out has the
+// input type.
 // kb: b has only so many rows (the others count as zeros); add (float32 out): out +=.
 hipError_t launch_dense_nn(bool is_bf16, const char* name, int M, int K, int S, const void* a,
-                           const void* a_lo, const void* b, void* out, void* ws, hipStream_t s,
+                           int numbers, const void* b, void* out, void* ws, hipStream_t s,
                            int kb = -1, bool add = false);
-// out [R, S] (float32) = (a + a_lo)^T b over M rows: a, a_lo [M, R] (a_lo may
-// be null), b [M, S]; lda: a's rows are so far apart (R, or more).
+// out [R, S] (float32) = a^T b over M rows: a [M, R] (of numbers as above), b [M, S];
+// lda: a's rows are so far apart (R, or more).
 hipError_t launch_dense_tn(bool is_bf16, const char* name, int M, int R, int S, const void* a,
-                           const void* a_lo, const void* b, float* out, void* ws, hipStream_t s,
-                           int lda = -1, bool add = false);
+                           int numbers, const void* b, float* out, void* ws, hipStream_t s,
+                           int lda = -1);
 
 // ---- cross entropy over the rows of w [V, D]
 size_t xent_ws_bytes(bool is_bf16, int M, int D, int V);
@@ -91,8 +92,8 @@ hipError_t launch_xent_rows(bool is_bf16, int M, int D, int V, const void* x,
                             const int32_t* targets, void* out, hipStream_t s);
 // dz = (softmax - [target]) dloss of the nv vocabulary rows from v0 on (w: the
 // first of them): [M, nv rounded up to 8], float32, or for bf16 problems hi and
-// then lo, as gated_dz_bytes, and with `three` what those two leave.
-hipError_t launch_xent_dz(bool is_bf16, bool three, int M, int D, int V, int v0, int nv, const void* x,
+// then lo, as gated_dz_bytes, and then what those two leave.
+hipError_t launch_xent_dz(bool is_bf16, int M, int D, int V, int v0, int nv, const void* x,
                           const void* w, const int32_t* targets, const float* lse,
                           const float* dloss, void* dz, hipStream_t s);
 

@@ -84,11 +84,11 @@ size_t layer_ws(const Dims& d, int32_t call) {
     // dz, and behind it the partial sums of dx, then those of dw_in
     case SWIMBA_LAYER_GATED_PROJECT_BACKWARD:
       return gated_bwd_dz_bytes(d) +
-             std::max(dense_ws_bytes(d.bf16, d.bf16, false, M, D, 2 * F),
-                      dense_ws_bytes(d.bf16, d.bf16, true, 2 * F, D, M));
+             std::max(dense_ws_bytes(d.bf16, d.bf16 ? 2 : 1, false, M, D, 2 * F),
+                      dense_ws_bytes(d.bf16, d.bf16 ? 2 : 1, true, 2 * F, D, M));
     case SWIMBA_LAYER_OUTPUT_PROJECT_BACKWARD:
-      return std::max(dense_ws_bytes(d.bf16, false, false, M, F, D),
-                      dense_ws_bytes(d.bf16, false, true, D, F, M));
+      return std::max(dense_ws_bytes(d.bf16, 1, false, M, F, D),
+                      dense_ws_bytes(d.bf16, 1, true, D, F, M));
     default: return 0;
   }
 }
@@ -300,12 +300,12 @@ swimba_status swimba_gated_project_backward(const swimba_dims* dims, const void*
   const int M = (int)d.M, D = (int)d.D, F = (int)d.HP;
   unsigned char* w8 = static_cast<unsigned char*>(ws);
   unsigned char* part = w8 + gated_bwd_dz_bytes(d);
-  const void* lo = d.bf16 ? w8 + (size_t)M * 2 * F * 2 : nullptr;
+  const int numbers = d.bf16 ? 2 : 1;
   hipError_t e = launch_gated_dz(d.bf16, M, D, F, act, x, w_in, dh, ws, stream);
   if (e != hipSuccess) return hip_status(e, "gated_project_backward dz launch");
-  e = launch_dense_nn(d.bf16, "gated_dx", M, 2 * F, D, ws, lo, w_in, dx, part, stream);
+  e = launch_dense_nn(d.bf16, "gated_dx", M, 2 * F, D, ws, numbers, w_in, dx, part, stream);
   if (e != hipSuccess) return hip_status(e, "gated_project_backward dx launch");
-  return hip_status(launch_dense_tn(d.bf16, "gated_dw", M, 2 * F, D, ws, lo, x, dw_in, part,
+  return hip_status(launch_dense_tn(d.bf16, "gated_dw", M, 2 * F, D, ws, numbers, x, dw_in, part,
                                     stream),
                     "gated_project_backward dw launch");
 }
@@ -329,9 +329,9 @@ swimba_status swimba_output_project_backward(const swimba_dims* dims, const void
   if ((st = check_ws(ws, ws_bytes, layer_ws(d, SWIMBA_LAYER_OUTPUT_PROJECT_BACKWARD))) != SWIMBA_OK)
     return st;
   const int M = (int)d.M, D = (int)d.D, F = (int)d.HP;
-  hipError_t e = launch_dense_nn(d.bf16, "output_project_dy", M, D, F, dout, nullptr, w_out, dy, ws, stream);
+  hipError_t e = launch_dense_nn(d.bf16, "output_project_dy", M, D, F, dout, 1, w_out, dy, ws, stream);
   if (e != hipSuccess) return hip_status(e, "output_project_backward dy launch");
-  return hip_status(launch_dense_tn(d.bf16, "output_project_dw", M, D, F, dout, nullptr, y, dw_out, ws,
+  return hip_status(launch_dense_tn(d.bf16, "output_project_dw", M, D, F, dout, 1, y, dw_out, ws,
                                     stream),
                     "output_project_backward dw launch");
 }

@@ -67,11 +67,13 @@ swimba_status check_loss(const Dims& d) {
   return SWIMBA_OK;
 }
 
-// The backward's pieces of the vocabulary: dz of one (two bf16 numbers or one
-// float32 an element) takes some 512 MB at most, in whole tiles (256 MB: 2 % slower,
-// 1 GB: 1.5 % faster at 16384 x 768 over 32768 words). Each piece but the first reads
-// and writes dx once more, so they are as few as that allows, and then equally large.
-// A piece's weights are read through one buffer.
+// The backward's pieces of the vocabulary: dz of one (three bf16 numbers or one float32
+// an element) has 2^27 elements at most, 805 or 537 MB, in whole tiles (half of that: 4
+// to 12 % slower, a quarter 7 to 15 %, at 16384 x 768 over 32768, 65536 x 512 over 32768
+// and 8192 x 768 over 131072 words, but 2 % faster at 4096 x 1024 over 131072); but past
+// 131072 tokens 1024 words, whatever that takes (6 KB a token). Each piece but the first
+// reads and writes dx once more, so they are as few as that allows, and then equally
+// large. A piece's weights are read through one buffer.
 int64_t xent_piece(const Dims& d) {
   const int64_t cols = (int64_t(1) << 27) / std::max<int64_t>(1, d.M) / 256 * 256;
   const int64_t rows = kMaxRecord / (d.D * (d.bf16 ? 2 : 4)) / 256 * 256;
@@ -81,18 +83,19 @@ int64_t xent_piece(const Dims& d) {
 }
 int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
 
-// bf16 problems take dz through both products as two bf16 numbers, an element off by
-// 2^-16 of itself at most. dx and dw are then off by up to 4e-6 (2-norm; 1.9e-6 at
-// 16384 x 768 over 32768 words), which is what long sums in float32 are off by anyway
-// (elementary float32 products: 2 to 3e-6 at 16384 tokens); for shorter ones it would
-// be the larger part (4e-6 against 3e-7 at 246 tokens). There a third number, half as
-// much again in both products (8192 x 768 over 16000 words: 1655 us, with two 1232),
-// makes it all of dz: 2e-7 at 246 tokens, 8e-7 at 8192.
-constexpr int64_t kThreeTokens = 8192;
-bool xent_three(const Dims& d) { return d.bf16 && d.M <= kThreeTokens; }
+// bf16 problems take dz through both products as three bf16 numbers, all of its 24
+// bits. Two would be off by up to 2^-17 = 7.6e-6 in the 2-norm, whatever the sums'
+// lengths (all of it where every target's dz has the same value), and are by 1.0 to
+// 4.3e-6 with the mean over the tokens as the loss; three are off by what the sums in
+// float32 are, 2e-7 at 246 tokens to 8e-7 at 16384 x 768 over 32768 words (elementary
+// float32 products: 2e-7 to 3.2e-6). Neither dx, whose sums run over the words, nor dw,
+// over the tokens, has a usual length at which two would not be the larger part. The
+// third costs nothing at 246 x 480 over 832 words (36 us), 1570 against 1210 us at 8192 x
+// 768 over 16000 and 6400 against 4750 at 16384 x 768 over 32768.
+int xent_numbers(const Dims& d) { return d.bf16 ? 3 : 1; }
 
 size_t xent_dz_bytes(const Dims& d, int64_t nv) {
-  return align256((xent_three(d) ? 6 : 4) * (size_t)(d.M * round8(nv)));
+  return align256((d.bf16 ? 6 : 4) * (size_t)(d.M * round8(nv)));
 }
 
 // x without the rows of tokens that have no target, behind dz.
@@ -104,10 +107,8 @@ size_t xent_bwd_ws(const Dims& d) {
   size_t sums = 0;
   for (int64_t nv : {piece, d.HP % piece}) {
     if (nv == 0) continue;
-    for (bool split : {false, true})  // (the third number goes through by itself)
-      if (split ? d.bf16 : !d.bf16 || xent_three(d))
-        sums = std::max({sums, dense_ws_bytes(d.bf16, split, false, M, D, (int)round8(nv)),
-                         dense_ws_bytes(d.bf16, split, true, (int)nv, D, M)});
+    sums = std::max({sums, dense_ws_bytes(d.bf16, xent_numbers(d), false, M, D, (int)round8(nv)),
+                     dense_ws_bytes(d.bf16, xent_numbers(d), true, (int)nv, D, M)});
   }
   return xent_dz_bytes(d, piece) + xent_rows_bytes(d) + sums;
 }
@@ -414,7 +415,7 @@ swimba_status swimba_cross_entropy_backward(const swimba_dims* dims, const void*
   CHECK(check_ws(ws, ws_bytes, ssm_ws(d, SWIMBA_SSM_CROSS_ENTROPY_BACKWARD)));
   const int M = (int)d.M, D = (int)d.D, V = (int)d.HP, piece = (int)xent_piece(d);
   const size_t es = d.bf16 ? 2 : 4;
-  const bool three = xent_three(d);
+  const int numbers = xent_numbers(d);
   unsigned char* dz = static_cast<unsigned char*>(ws);
   unsigned char* rows = dz + xent_dz_bytes(d, piece);
   unsigned char* part = rows + xent_rows_bytes(d);
@@ -423,21 +424,13 @@ swimba_status swimba_cross_entropy_backward(const swimba_dims* dims, const void*
   for (int v0 = 0; v0 < V; v0 += piece) {
     const int nv = std::min(piece, V - v0), ld = (int)round8(nv);
     const void* wp = static_cast<const unsigned char*>(w) + (size_t)v0 * D * es;
-    const void* lo = d.bf16 ? dz + (size_t)M * ld * 2 : nullptr;
-    const void* rest = dz + (size_t)M * ld * 4;
-    e = launch_xent_dz(d.bf16, three, M, D, V, v0, nv, x, wp, targets, lse, dloss, dz, stream);
+    e = launch_xent_dz(d.bf16, M, D, V, v0, nv, x, wp, targets, lse, dloss, dz, stream);
     if (e != hipSuccess) return hip_status(e, "cross_entropy_backward dz launch");
-    e = launch_dense_nn(d.bf16, "cross_entropy_dx", M, ld, D, dz, lo, wp, dx, part, stream, nv,
+    e = launch_dense_nn(d.bf16, "cross_entropy_dx", M, ld, D, dz, numbers, wp, dx, part, stream, nv,
                         v0 > 0);
-    if (e == hipSuccess && three)
-      e = launch_dense_nn(true, "cross_entropy_dx", M, ld, D, rest, nullptr, wp, dx, part, stream,
-                          nv, true);
     if (e != hipSuccess) return hip_status(e, "cross_entropy_backward dx launch");
-    e = launch_dense_tn(d.bf16, "cross_entropy_dw", M, nv, D, dz, lo, rows, dw + (size_t)v0 * D,
+    e = launch_dense_tn(d.bf16, "cross_entropy_dw", M, nv, D, dz, numbers, rows, dw + (size_t)v0 * D,
                         part, stream, ld);
-    if (e == hipSuccess && three)
-      e = launch_dense_tn(true, "cross_entropy_dw", M, nv, D, rest, nullptr, rows,
-                          dw + (size_t)v0 * D, part, stream, ld, true);
     if (e != hipSuccess) return hip_status(e, "cross_entropy_backward dw launch");
   }
   return SWIMBA_OK;
