@@ -120,8 +120,10 @@ size_t ssm_ws(const Dims& d, int32_t call) {
     case SWIMBA_SSM_CONV_BACKWARD: return conv_bwd_ws_bytes(Bt, T, C);
     case SWIMBA_SSM_SCAN: return N > kScanMaxN ? 0 : sscan_ws_bytes(Bt, T, C, N, G);
     case SWIMBA_SSM_SCAN_BACKWARD: return N > kScanMaxN ? 0 : sscan_bwd_ws_bytes(Bt, T, C, N, G);
-    case SWIMBA_SSM_CROSS_ENTROPY: return xent_ws_bytes(d.bf16, (int)d.M, (int)d.D, C);
-    case SWIMBA_SSM_CROSS_ENTROPY_BACKWARD: return xent_bwd_ws(d);
+    // (d_model is theirs alone)
+    case SWIMBA_SSM_CROSS_ENTROPY:
+      return d.D > kMaxD ? 0 : xent_ws_bytes(d.bf16, (int)d.M, (int)d.D, C);
+    case SWIMBA_SSM_CROSS_ENTROPY_BACKWARD: return d.D > kMaxD ? 0 : xent_bwd_ws(d);
     default: return 0;
   }
 }
@@ -138,7 +140,7 @@ extern "C" {
 
 size_t swimba_ssm_workspace_size(const swimba_dims* dims, int32_t call) {
   Dims d;
-  if (!query_dims(dims, d) || d.D > kMaxD) return 0;
+  if (!query_dims(dims, d)) return 0;
   return ssm_ws(d, call);
 }
 
