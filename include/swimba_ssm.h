@@ -204,7 +204,9 @@ swimba_status swimba_selective_step(const swimba_dims* dims, const void* x, int6
  *   targets   [M] int32
  *   loss      [M] float32 out;  lse [M] float32 out
  *   ws        workspace of SWIMBA_SSM_CROSS_ENTROPY
- * D must be a multiple of 8 (else SWIMBA_ERR_UNSUPPORTED); V is any.
+ * D must be a multiple of 8 (else SWIMBA_ERR_UNSUPPORTED) and at most 2^20;
+ * V at most 2^20, with (V + 2) D below 2^31; M V below some 2^37 (a launch's
+ * threads), M below 2^28 (SWIMBA_ERR_DIMS otherwise).
  */
 swimba_status swimba_cross_entropy(const swimba_dims* dims, const void* x, const void* w,
                                    const int32_t* targets, float* loss, float* lse, void* ws,
@@ -222,7 +224,10 @@ swimba_status swimba_cross_entropy(const swimba_dims* dims, const void* x, const
  *   dloss     [M] float32: gradient of each token's loss (not looked at
  *             where there is no target)
  *   dx        [M, D] float32 out;  dw [V, D] float32 out (zeros without tokens)
- *   ws        workspace of SWIMBA_SSM_CROSS_ENTROPY_BACKWARD
+ *   ws        workspace of SWIMBA_SSM_CROSS_ENTROPY_BACKWARD: x, dz of a piece of
+ *             the vocabulary (for bf16 problems 6 bytes an element, 805 MB at most
+ *             up to 2^17 tokens, 6 KB a token beyond; float32 two thirds of it)
+ *             and partial sums of the products
  */
 swimba_status swimba_cross_entropy_backward(const swimba_dims* dims, const void* x, const void* w,
                                             const int32_t* targets, const float* lse,
