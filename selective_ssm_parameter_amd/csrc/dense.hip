@@ -890,9 +890,13 @@ hipError_t go_rows(const char* name, const DenseArgs& A, hipStream_t s) {
   if constexpr (sizeof(T) == 2)
     if (tile == 256256) return go<T, Big, MODE, T>(name, A, s);
   if (tile == 128128) return go<T, Mid, MODE, T>(name, A, s);
-  if constexpr (sizeof(T) == 4)
-    if (tile == 32128) return go<T, TinyGated, MODE, T>(name, A, s);
-  return go<T, Small, MODE, T>(name, A, s);
+  if constexpr (is_xent(MODE) && sizeof(T) == 4) {
+    return go<T, TinyGated, MODE, T>(name, A, s);  // (of two tiles)
+  } else {
+    if constexpr (sizeof(T) == 4)
+      if (tile == 32128) return go<T, TinyGated, MODE, T>(name, A, s);
+    return go<T, Small, MODE, T>(name, A, s);
+  }
 }
 
 constexpr int kSkinnyTokens = 64;
