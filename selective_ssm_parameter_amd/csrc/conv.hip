@@ -14,14 +14,13 @@
 
 #include "common.hpp"
 #include "ssm.hpp"
+#include "ssm_plan.hpp"
 
 namespace swimba {
 
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kStep = 8;     // rows in flight per thread
-constexpr int kStepBwd = 4;  // the same of the backward, of x and of dy
 
 template <typename T, int VEC> struct Raw {
   typedef T t __attribute__((ext_vector_type(VEC)));
@@ -347,25 +346,6 @@ __global__ __launch_bounds__(256) void conv_state_kernel(const T* from, T* to, s
   for (size_t q = (size_t)blockIdx.x * 256 + threadIdx.x; q < n; q += (size_t)gridDim.x * 256)
     to[q] = from ? from[q] : from_f32<T>(0.f);
 }
-
-// Tokens per thread: long runs read few rows twice and leave few partial sums, as
-// long as enough threads remain to fill the card, some 2^18 forward (8 x 2048 x
-// 1536: 20 us; 2^17: 23, 2^19: 22) and, for the partial sums, 2^17 backward (36 us with
-// their addition; 2^16: 43, 2^18: 34 but slower in float32, 2^19: 51).
-constexpr int kFwdThreads = 18, kBwdThreads = 17;
-int run_length(int64_t Bt, int64_t T, int64_t vecs, int threads) {
-  const int64_t r = Bt * T * vecs >> threads;
-  return (int)std::min<int64_t>(256, std::max<int64_t>(kStep, r / kStep * kStep));
-}
-// Channels per thread: v, where rows allow it.
-int vec_of(int v, int C, int64_t ldx, int64_t lddx) {
-  return C % v == 0 && ldx % v == 0 && lddx % v == 0 ? v : 1;
-}
-// 16 bytes of them forward; 8 in the backward, whose registers then leave room for
-// three waves instead of one (padded 8 x 2048 x 1536: 78 -> 40 us when it was measured;
-// 4 bytes: 54, now 32 against 31).
-int vec_fwd(bool is_bf16) { return is_bf16 ? 8 : 4; }
-int vec_bwd(bool is_bf16) { return is_bf16 ? 4 : 2; }
 
 // f(element type, channels per thread, width)
 template <int VB, int VF, class F>

@@ -33,6 +33,7 @@
 #include "common.hpp"
 #include "lds_tiles.hpp"
 #include "ssm.hpp"
+#include "ssm_plan.hpp"
 
 namespace swimba {
 
@@ -1078,11 +1079,9 @@ hipError_t launch_sscan_step(bool is_bf16, const SScanArgs& a, hipStream_t s) {
     return launch("selective_step", sscan_step_kernel<decltype(t), r()>,
                   dim3((unsigned)((rows * a.Ch * 4 + 255) / 256)), dim3(256), 0, s, a);
   };
-  // two sequences a thread where that leaves threads enough to fill the card (256 x 4096
-  // x 16: 34 us; one: 39, four: 38, eight: 56)
   const std::integral_constant<int, 2> two{};
   const std::integral_constant<int, 1> one{};
-  if ((int64_t)a.Bt * a.Ch >= (int64_t)1 << 18) return is_bf16 ? run(bf16(), two) : run(0.f, two);
+  if (step_sequences(a.Bt, a.Ch) == 2) return is_bf16 ? run(bf16(), two) : run(0.f, two);
   return is_bf16 ? run(bf16(), one) : run(0.f, one);
 }
 
