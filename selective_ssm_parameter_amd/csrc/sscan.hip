@@ -944,9 +944,10 @@ __global__ __launch_bounds__(256) void sscan_step_kernel(SScanArgs A) {
       }
       float* to = A.h + (b[r] * A.Ch + c) * A.N;
       if (b0 + r >= A.Bt) continue;
-      // past the L2's reuse order where a wave's channels are one run of whole lines (a
-      // hint; 256 x 4096 x 16: 35 -> 25.5 us)
-      if (A.N <= kStates && A.N % 4 == 0)
+      // past the L2's reuse order (a hint) where four lanes store 64 aligned bytes or a wave's
+      // channels are one run; us without and with it: 256 x 4096 x 4 22.2, 21.8, x 16 37.3,
+      // 25.5, x 32 78.3, 68.3, x 64 151, 140, 64 x 4096 x 64 45.2, 27.7; but x 20 57.3, 63.6
+      if (A.N % kStates == 0 || (A.N < kStates && A.N % 4 == 0))
         __builtin_nontemporal_store(h[r], reinterpret_cast<floatx4*>(to + n0));
       else
         store_states(to, n0, A.N, h[r]);
