@@ -1078,8 +1078,10 @@ hipError_t xent_forward(int M, int D, int V, const void* x, const void* w, const
   if (e != hipSuccess) return e;
   const int cols = xent_tile_cols(xent_tile(sizeof(T) == 2, M, V, D));
   const int tiles = (V + cols - 1) / cols;
-  // rows that share a line of 128 bytes, as long as that leaves workgroups enough
-  if (M >= 2048)
+  // 16 rows share a line of 128 bytes, 4 leave four times the workgroups: forward with 4
+  // and with 16, D = 64, us: 128 tokens over 32768 and 131072 words 11.3, 10.2 and 21.2, 23.3,
+  // 512 tokens 17.3, 15.1 and 46.3, 45.8, 2048 46.2, 41.5 and 155, 151, 16384 305, 291
+  if (M >= 512)
     return launch("cross_entropy_finish", xent_finish_kernel<16>, dim3((unsigned)((M + 15) / 16)),
                   dim3(256), 0, s, A.xe, M, tiles, loss, lse);
   return launch("cross_entropy_finish", xent_finish_kernel<4>, dim3((unsigned)((M + 3) / 4)),
