@@ -121,7 +121,8 @@ swimba_status swimba_causal_conv_step(const swimba_dims* dims, int32_t width, co
  *   h_t[n] = a_t[n] h_{t-1}[n] + delta_t B_t[g, n] x_t,
  *   u_t = sum_n C_t[g, n] h_t[n] + D[c] x_t,   y_t = u_t silu(z_t)   (u_t without z),
  *   h_{-1} = h_init.
- * States are held in float32. A is used as it is (a state decays where A < 0).
+ * States are held in float32. A is used as it is (a state decays where A < 0,
+ * grows where A > 0 and is forgotten at every step above zero where A is -inf).
  *   x, dt, z  [M, C] dtype, rows ldx, lddt and ldz apart; z may be NULL
  *   B, C      [M, G * N] dtype, rows ldbc apart (both)
  *   A         [C, N] float32

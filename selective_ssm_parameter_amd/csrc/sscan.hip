@@ -313,13 +313,24 @@ template <class F> __device__ __forceinline__ void down4(F f) {
   f(std::integral_constant<int, 0>());
 }
 
-// A lane's constants: A (times log2 e: decays are powers of 2), dt_bias, D. Lanes
+// A times log2 e (decays are powers of 2), -inf as the largest finite number: a step of
+// zero (a token past the length, a segment without tokens) then keeps the state as with
+// any other decay, and any other step forgets it all the same. (NaN stays.)
+__device__ __forceinline__ floatx4 rates(floatx4 a) {
+  constexpr float kMost = 3.4028234e38f;
+  a = a * kLog2e;
+#pragma unroll
+  for (int k = 0; k < kQ; ++k) a[k] = a[k] < -kMost ? -kMost : a[k];
+  return a;
+}
+
+// A lane's constants: A (rates), dt_bias, D. Lanes
 // without a channel hold zeros, so that all they compute from is zero.
 struct Coef {
   floatx4 A2;
   float bias, D;
   __device__ Coef(const SScanArgs& A, const Place& p) {
-    A2 = load_states(A.A + (size_t)p.c * A.N, p.n0, A.N, p.on) * kLog2e;
+    A2 = rates(load_states(A.A + (size_t)p.c * A.N, p.n0, A.N, p.on));
     bias = A.bias && p.on ? A.bias[p.c] : 0.f;
     D = A.D && p.on ? A.D[p.c] : 0.f;
   }
@@ -932,7 +943,7 @@ __global__ __launch_bounds__(256) void sscan_step_kernel(SScanArgs A) {
         }
       }
     }
-    const floatx4 Av = load_states(Ap, n0, A.N, true) * kLog2e;
+    const floatx4 Av = rates(load_states(Ap, n0, A.N, true));
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float sig;

@@ -99,3 +99,53 @@ def test_small_states_grow_into_range(N):
     tol = tolerance(T, N, growth, "f32")
     close("y", y, wy, tol)
     close("h", h, hs[:, -1], tol)
+
+
+def forget(A, value):
+    A = A.clone()
+    A[::3, ::2] = value
+    return A
+
+
+@pytest.mark.parametrize("T,N,lens", [(37, 16, None), (700, 5, [700, 33, 0]), (130, 40, [130, 1, 64])])
+def test_states_that_forget_at_once(T, N, lens):
+    """A of -inf (what -exp of a large number is) gives the bits of the largest finite one,
+    whose decays are zeros too, wherever a sequence ends."""
+    Bt, Ch = 1 if lens is None else len(lens), 12
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    d, M = ssm.ssm_dims(Bt, T, Ch, N, 1, "f32"), Bt * T
+    x, dt, z, B, C, dy = r(M, Ch), r(M, Ch), r(M, Ch), r(M, N), r(M, N), r(M, Ch)
+    A, h0, dh = -torch.exp(r(Ch, N)), r(Bt, Ch, N), r(Bt, Ch, N)
+    ln = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    outs = []
+    for value in (-torch.finfo(torch.float32).max, float("-inf")):
+        Av = forget(A, value)
+        y, h, carry = empty(M, Ch), empty(Bt, Ch, N), ssm.selective_scan_carry(d)
+        carry.zero_()
+        inputs = (x, dt, z, B, C, Av, None, None)
+        ssm.swimba_selective_scan(d, *inputs, ln, h0, y, h, carry,
+                                  ssm.ssm_workspace(d, ssm.SELECTIVE_SCAN))
+        g = [empty(M, Ch) for _ in range(3)] + [empty(M, N), empty(M, N), empty(Ch, N), empty(Ch),
+                                                empty(Ch), empty(Bt, Ch, N)]
+        ssm.swimba_selective_scan_backward(d, *inputs, ln, carry, dy, dh, *g,
+                                           ssm.ssm_workspace(d, ssm.SELECTIVE_SCAN_BACKWARD))
+        d1 = ssm.ssm_dims(Bt, 1, Ch, N, 1, "f32")
+        y1, h1, dt1 = empty(Bt, Ch), empty(Bt, Ch, N), dt[:Bt].clone()
+        dt1[:, ::2] = -200.0  # a step of zero: the state stays
+        ssm.swimba_selective_step(d1, x[:Bt], dt1, None, B[:Bt], C[:Bt], Av, None, None, h0, h1, y1)
+        assert torch.equal(h1[:, ::2], h0[:, ::2])
+        outs.append([y, h, *g, y1, h1])
+    for i, (a, b) in enumerate(zip(*outs)):
+        assert bool(torch.isfinite(a).all()) and torch.equal(a, b), i
+
+
+def test_nan_decays_stay_nan():
+    d, r = ssm.ssm_dims(1, 40, 4, 4, 1, "f32"), lambda *s: torch.randn(*s, device="cuda")
+    A = -torch.ones(4, 4, device="cuda")
+    A[2, 1] = float("nan")
+    y, h = empty(40, 4), empty(1, 4, 4)
+    ssm.swimba_selective_scan(d, r(40, 4), r(40, 4), None, r(40, 4), r(40, 4), A, None, None, None,
+                              None, y, h, None, ssm.ssm_workspace(d, ssm.SELECTIVE_SCAN))
+    bad = torch.isnan(h[0])
+    assert bool(bad[2, 1]) and int(bad.sum()) == 1 and torch.isnan(y[:, 2]).all()
