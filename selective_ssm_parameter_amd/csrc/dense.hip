@@ -25,9 +25,9 @@
 // entropy's dz goes through as three, all of its 24 bits, in the same way.
 // The cross entropy's z stays in registers too: the forward's epilogue leaves a row's
 // largest z and sum of exponentials per tile, the backward's recomputes z and leaves
-// dz. 16384 tokens, 768 -> 32768 words: statistics 843 us (980 TFLOP/s; 16384 x 2048
-// -> 65536 3500 us, 1260), dz 4 x 262 (790, with 537 MB of stores each), dx 4 x 382
-// (1080), dw 4 x 315 (1310); 128 tokens, 2048 -> 65536 words 69 us (w at 3.9 TB/s).
+// dz. 16384 tokens, 768 -> 32768 words: statistics 814 us (1010 TFLOP/s; 16384 x 2048
+// -> 65536 3460 us, 1270), dz 4 x 357 (580, with 805 MB of stores each), dx 4 x 570
+// (1080), dw 4 x 449 (1380); 128 tokens, 2048 -> 65536 words 68 us (w at 3.9 TB/s).
 // Bound by the matrix cores for many tokens.
 #include <algorithm>
 #include <type_traits>

@@ -10,7 +10,7 @@
 // some 8 and, with the sums over channels and what a token needs by itself, 28, and the
 // segments' first passes another 5 each. Measured: 65536 x 2048 x 16 bf16 975 us (first
 // pass 385 to 430; vector units issuing 98 % of the cycles), padded 8 x 2048 x 1536 x
-// 16 forward and backward 441 us, 256 x 4096 x 16 one token 25 us (HBM).
+// 16 forward and backward 434 to 470 us, 256 x 4096 x 16 one token 25 us (HBM).
 //
 // A wave walks the tokens of 16 channels x 16 states: lane (channel q = lane / 4,
 // j = lane % 4) holds states 4 j .. 4 j + 3 of its channel, so that sums over
